@@ -27,6 +27,8 @@ _BINDING_NAMES = {
     "ep_register_layer_rank_major", "ep_rank_major_count", "ep_rank_major_prepare",
     "ep_rank_major_dispatch", "ep_rank_major_combine", "ep_rank_major_combine_bwd",
     "ep_rank_major_dispatch_bwd",
+    "ep_expert_gemm", "ep_expert_gemm_swiglu", "ep_expert_dgrad", "ep_expert_dgrad_swiglu", "ep_expert_wgrad",
+    "ep_expert_gemv_w4", "ep_expert_gemv_w4_swiglu", "pack_w4", "ep_router", "ep_router_bwd",
 }
 
 

@@ -44,6 +44,17 @@ class LayerConfig(ctypes.Structure):
 DTYPE_CODES = {"bf16": 0, "fp16": 1, "fp32": 2}
 TORCH_DTYPES = {0: torch.bfloat16, 1: torch.float16, 2: torch.float32}
 _layer_dtype = {}  # layer id -> torch dtype of its payload rows
+_layer_experts = {}  # layer id -> (experts whose rows this rank holds, receive capacity)
+
+
+class RouterConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int64), ("top_k", ctypes.c_int64),
+                ("num_groups", ctypes.c_int64), ("topk_groups", ctypes.c_int64),
+                ("score", ctypes.c_int64), ("normalize", ctypes.c_int64),
+                ("dtype", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
+SCORE_CODES = {"softmax": 0, "sigmoid": 1}
 
 
 class Handle(ctypes.Structure):
@@ -96,6 +107,15 @@ def _load(path=None):
         "ep_rank_major_combine": ([Handle, p, i64, p, p], st),
         "ep_rank_major_combine_bwd": ([Handle, p, i64, p, p], st),
         "ep_rank_major_dispatch_bwd": ([Handle, p, p, i64, p, p, p], st),
+        "ep_expert_gemm": ([Handle, p, p, i64, i64, p, p], st),
+        "ep_expert_gemm_swiglu": ([Handle, p, p, i64, i64, p, p, p], st),
+        "ep_expert_dgrad": ([Handle, p, p, i64, i64, p, p], st),
+        "ep_expert_dgrad_swiglu": ([Handle, p, p, p, i64, i64, p, p], st),
+        "ep_expert_wgrad": ([Handle, p, p, i64, i64, p, i64, ctypes.c_int, p], st),
+        "ep_expert_gemv_w4": ([Handle, p, p, p, i64, i64, i64, p, p], st),
+        "ep_expert_gemv_w4_swiglu": ([Handle, p, p, p, i64, i64, i64, p, p], st),
+        "ep_router": ([RouterConfig, p, p, i64, p, p, p], st),
+        "ep_router_bwd": ([RouterConfig, p, p, p, i64, p, p], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -112,7 +132,9 @@ SYMBOLS = ("ep_abi_version", "ep_last_error", "ep_launch_count", "ep_register_la
            "ep_shard_combine", "ep_shard_combine_bwd", "ep_shard_dispatch_bwd", "ep_shard_token_owners",
            "ep_register_layer_rank_major", "ep_rank_major_count", "ep_rank_major_prepare",
            "ep_rank_major_dispatch", "ep_rank_major_combine", "ep_rank_major_combine_bwd",
-           "ep_rank_major_dispatch_bwd")
+           "ep_rank_major_dispatch_bwd",
+           "ep_expert_gemm", "ep_expert_gemm_swiglu", "ep_expert_dgrad", "ep_expert_dgrad_swiglu",
+           "ep_expert_wgrad", "ep_expert_gemv_w4", "ep_expert_gemv_w4_swiglu", "ep_router", "ep_router_bwd")
 
 
 def lib():
@@ -187,6 +209,7 @@ def ep_register_layer(num_experts: int, top_k: int, hidden: int, max_tokens: int
     size = ctypes.c_size_t(0)
     _check(_lib.ep_register_layer(cfg, ctypes.byref(lid), ctypes.byref(size)))
     _layer_dtype[int(lid.value)] = TORCH_DTYPES[code]
+    _layer_experts[int(lid.value)] = (num_experts, ep_recv_capacity(int(lid.value)))
     return int(lid.value), int(size.value)
 
 
@@ -202,6 +225,7 @@ def ep_register_layer_sharded(num_experts: int, top_k: int, hidden: int, max_tok
     size = ctypes.c_size_t(0)
     _check(_lib.ep_register_layer_sharded(cfg, num_ranks, rank, ctypes.byref(lid), ctypes.byref(size)))
     _layer_dtype[int(lid.value)] = TORCH_DTYPES[code]
+    _layer_experts[int(lid.value)] = (num_experts // num_ranks, ep_recv_capacity(int(lid.value)))
     return int(lid.value), int(size.value)
 
 
@@ -472,3 +496,172 @@ def ep_rank_major_dispatch_bwd(h: EpHandle, grad_recv: torch.Tensor,
                                            _ptr(grad_tokens, _payload(h), "grad_tokens"),
                                            _ptr(grad_topk_weights, torch.float32, "grad_topk_weights"),
                                            _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# Expert products on the receive rows of a prepared handle
+# ----------------------------------------------------------------------------
+
+def _rows(h: EpHandle, t: torch.Tensor, width: int, name: str) -> int:
+    """A receive-row buffer: at least the layer's capacity of rows of `width`
+    payload elements."""
+    p = _ptr(t, _payload(h), name)
+    capacity = _layer_experts.get(h.id, (0, 0))[1]
+    if t.dim() != 2 or t.shape[1] != width or t.shape[0] < capacity:
+        raise ValueError("%s must be [>= %d rows, %d], got %s" % (name, capacity, width, tuple(t.shape)))
+    return p
+
+
+def _expert_weights(h: EpHandle, t: torch.Tensor, name: str, dtype=None):
+    """A per-expert array [E, n, k]: pointer and the two sizes."""
+    p = _ptr(t, dtype if dtype is not None else _payload(h), name)
+    experts = _layer_experts.get(h.id, (t.shape[0], 0))[0]
+    if t.dim() != 3 or t.shape[0] != experts:
+        raise ValueError("%s must be [%d experts, out, in], got %s" % (name, experts, tuple(t.shape)))
+    return p, t.shape[1], t.shape[2]
+
+
+def _gated(n: int, name: str) -> int:
+    if n % 2:
+        raise ValueError("%s must hold as many gate rows as up rows, got %d" % (name, n))
+    return n // 2
+
+
+def ep_expert_gemm(h: EpHandle, x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, stream=None):
+    """y[r] = w[e] x[r] for the rows of each expert e; w [E, out, in]."""
+    wp, n, k = _expert_weights(h, w, "w")
+    _check(_lib.ep_expert_gemm(h.c, _rows(h, x, k, "x"), wp, n, k, _rows(h, y, n, "y"), _stream(stream)))
+
+
+def ep_expert_gemm_swiglu(h: EpHandle, x: torch.Tensor, w: torch.Tensor, act: torch.Tensor,
+                          pre: Optional[torch.Tensor] = None, stream=None):
+    """act[r] = silu(gate) * up of w[e] x[r]; w [E, 2*ffn, in], gate rows
+    first.  pre, when given, keeps the unactivated [R, 2*ffn]."""
+    wp, n, k = _expert_weights(h, w, "w")
+    f = _gated(n, "w")
+    _check(_lib.ep_expert_gemm_swiglu(h.c, _rows(h, x, k, "x"), wp, f, k,
+                                      None if pre is None else _rows(h, pre, n, "pre"),
+                                      _rows(h, act, f, "act"), _stream(stream)))
+
+
+def ep_expert_dgrad(h: EpHandle, dy: torch.Tensor, w: torch.Tensor, dx: torch.Tensor, stream=None):
+    """dx[r] = transpose(w[e]) dy[r]."""
+    wp, n, k = _expert_weights(h, w, "w")
+    _check(_lib.ep_expert_dgrad(h.c, _rows(h, dy, n, "dy"), wp, n, k, _rows(h, dx, k, "dx"), _stream(stream)))
+
+
+def ep_expert_dgrad_swiglu(h: EpHandle, dy: torch.Tensor, w: torch.Tensor, pre: torch.Tensor,
+                           dpre: torch.Tensor, stream=None):
+    """transpose(w[e]) dy[r] taken through the gated activation; pre and
+    dpre [R, 2*ffn], w [E, out, ffn]."""
+    wp, n, f = _expert_weights(h, w, "w")
+    _check(_lib.ep_expert_dgrad_swiglu(h.c, _rows(h, dy, n, "dy"), wp, _rows(h, pre, 2 * f, "pre"), n, f,
+                                       _rows(h, dpre, 2 * f, "dpre"), _stream(stream)))
+
+
+def ep_expert_wgrad(h: EpHandle, dy: torch.Tensor, x: torch.Tensor, dw: torch.Tensor,
+                    accumulate: bool = False, stream=None):
+    """dw[e] = (dw[e] +) sum over the expert's rows of dy[r] x[r]^T; dw
+    [E, out, in] of the payload type or float32."""
+    if dw.dtype not in (torch.float32, _payload(h)):
+        raise TypeError("dw must be float32 or %s, got %s" % (_payload(h), dw.dtype))
+    wp, n, k = _expert_weights(h, dw, "dw", dw.dtype)
+    code = DTYPE_CODES["fp32"] if dw.dtype == torch.float32 else _dtype_code(dw.dtype)
+    _check(_lib.ep_expert_wgrad(h.c, _rows(h, dy, n, "dy"), _rows(h, x, k, "x"), n, k, wp, code,
+                                1 if accumulate else 0, _stream(stream)))
+
+
+def _w4(h: EpHandle, wq: torch.Tensor, scales: torch.Tensor):
+    wp, n, half = _expert_weights(h, wq, "wq", torch.uint8)
+    sp, sn, groups = _expert_weights(h, scales, "scales")
+    if sn != n or groups < 1 or (2 * half) % groups:
+        raise ValueError("scales must be [%d, %d, in/group], got %s" % (wq.shape[0], n, tuple(scales.shape)))
+    return wp, sp, n, 2 * half, 2 * half // groups
+
+
+def ep_expert_gemv_w4(h: EpHandle, x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
+                      y: torch.Tensor, stream=None):
+    """y[r] = w[e] x[r] with 4-bit weights: wq uint8 [E, out, in/2] (see
+    pack_w4), scales [E, out, in/group] of the payload type."""
+    wp, sp, n, k, group = _w4(h, wq, scales)
+    _check(_lib.ep_expert_gemv_w4(h.c, _rows(h, x, k, "x"), wp, sp, n, k, group, _rows(h, y, n, "y"),
+                                  _stream(stream)))
+
+
+def ep_expert_gemv_w4_swiglu(h: EpHandle, x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
+                             act: torch.Tensor, stream=None):
+    """act[r] = silu(gate) * up with 4-bit weights: wq [E, 2*ffn, in/2]."""
+    wp, sp, n, k, group = _w4(h, wq, scales)
+    f = _gated(n, "wq")
+    _check(_lib.ep_expert_gemv_w4_swiglu(h.c, _rows(h, x, k, "x"), wp, sp, f, k, group,
+                                         _rows(h, act, f, "act"), _stream(stream)))
+
+
+def pack_w4(w: torch.Tensor, group: int):
+    """Round weights [E, out, in] to 4 bits with one scale per `group` of the
+    input features: (wq uint8 [E, out, in/2], scales [E, out, in/group] of
+    w's type).  Laid out once, when weights are loaded; plain torch."""
+    E, n, k = w.shape
+    if group < 1 or k % group or k % 2:
+        raise ValueError("in_features %d must be even and a multiple of the group %d" % (k, group))
+    g = w.float().view(E, n, k // group, group)
+    scales = (g.abs().amax(dim=3) / 7).to(w.dtype)
+    s = scales.float().unsqueeze(3)
+    q = torch.where(s > 0, torch.round(g / torch.where(s > 0, s, torch.ones_like(s))), torch.zeros_like(g))
+    q = (q.clamp(-8, 7) + 8).to(torch.uint8).view(E, n, k)
+    return (q[..., 0::2] | (q[..., 1::2] << 4)).contiguous(), scales.contiguous()
+
+
+# ----------------------------------------------------------------------------
+# Router
+# ----------------------------------------------------------------------------
+
+def _router_config(logits, top_k, num_groups, topk_groups, score, normalize, scale) -> RouterConfig:
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens, experts], got %s" % (tuple(logits.shape),))
+    if score not in SCORE_CODES:
+        raise ValueError("score must be softmax or sigmoid, got %s" % score)
+    return RouterConfig(logits.shape[1], top_k, num_groups, topk_groups, SCORE_CODES[score],
+                        1 if normalize else 0, _dtype_code(logits.dtype), scale)
+
+
+def _routes(t: torch.Tensor, T: int, K: int, name: str):
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != K:
+        raise ValueError("%s must be [%d, %d], got %s" % (name, T, K, tuple(t.shape)))
+
+
+def ep_router(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+              bias: Optional[torch.Tensor] = None, score: str = "softmax", normalize: bool = True,
+              num_groups: int = 1, topk_groups: int = 1, scale: float = 1.0, stream=None):
+    """The chosen experts and their weights, from logits [T, E]: topk_idx
+    int64 [T, K] and topk_weights float32 [T, K] as ep_prepare and
+    ep_dispatch take them."""
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [tokens, top_k], got %s" % (tuple(topk_idx.shape),))
+    cfg = _router_config(logits, topk_idx.shape[1], num_groups, topk_groups, score, normalize, scale)
+    T, K = logits.shape[0], topk_idx.shape[1]
+    _routes(topk_idx, T, K, "topk_idx")
+    _routes(topk_weights, T, K, "topk_weights")
+    if bias is not None and tuple(bias.shape) != (logits.shape[1],):
+        raise ValueError("bias must be [%d], got %s" % (logits.shape[1], tuple(bias.shape)))
+    _check(_lib.ep_router(cfg, _ptr(logits, None, "logits"), _ptr(bias, torch.float32, "bias"), T,
+                          _ptr(topk_idx, torch.int64, "topk_idx"),
+                          _ptr(topk_weights, torch.float32, "topk_weights"), _stream(stream)))
+
+
+def ep_router_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, grad_topk_weights: torch.Tensor,
+                  grad_logits: torch.Tensor, score: str = "softmax", normalize: bool = True,
+                  scale: float = 1.0, stream=None):
+    """grad_logits [T, E] (every element written) from the weights' gradient
+    (ep_dispatch_bwd's grad_topk_weights), the choice held fixed."""
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [tokens, top_k], got %s" % (tuple(topk_idx.shape),))
+    cfg = _router_config(logits, topk_idx.shape[1], 1, 1, score, normalize, scale)
+    T, K = logits.shape[0], topk_idx.shape[1]
+    _routes(topk_idx, T, K, "topk_idx")
+    _routes(grad_topk_weights, T, K, "grad_topk_weights")
+    if grad_logits.shape != logits.shape:
+        raise ValueError("grad_logits must be %s, got %s" % (tuple(logits.shape), tuple(grad_logits.shape)))
+    _check(_lib.ep_router_bwd(cfg, _ptr(logits, None, "logits"), _ptr(topk_idx, torch.int64, "topk_idx"),
+                              _ptr(grad_topk_weights, torch.float32, "grad_topk_weights"), T,
+                              _ptr(grad_logits, logits.dtype, "grad_logits"), _stream(stream)))

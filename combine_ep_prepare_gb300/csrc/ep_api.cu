@@ -14,7 +14,7 @@
 #include <mutex>
 #include <string>
 
-#include "ep_internal.cuh"
+#include "ep_experts.cuh"
 
 namespace ep {
 cudaError_t probe_kernel_image();
@@ -1101,3 +1101,25 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t h, const void* const* grad_re
 }
 
 }  // extern "C"
+
+// The library's state, for the calls of ep_experts_api.cu.
+namespace ep {
+
+ep_status_t api_fail(ep_status_t code, const char* msg) { return fail(code, "%s", msg); }
+
+ep_status_t api_cuda_fail(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+
+ep_status_t api_expert_layer(const ep_handle_t& h, const LayerInfo** out) {
+  const ep_status_t st = lookup(h, out, 2);
+  if (st != EP_OK) return st;
+  if ((*out)->rank_major)
+    return fail(EP_ERR_INVALID_ARG, "layer %llu is rank-major: the experts' rows are the owner's single-buffer layer's",
+                (unsigned long long)h.id);
+  return EP_OK;
+}
+
+ep_status_t api_device(int* num_sms) { return check_device(num_sms); }
+
+void api_count_launches(int n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
+
+}  // namespace ep

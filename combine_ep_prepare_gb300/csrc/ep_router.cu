@@ -1,0 +1,268 @@
+// ep_router.cu -- the router in front of prepare, and its gradient.
+//
+// Per token with logits z[0..E): selection values v_e = z_e (softmax) or
+// sigmoid(z_e) + bias_e (sigmoid).  With groups, a group's rank is the sum of
+// its two largest v and only the `kept` best groups' experts stay.  The K
+// largest v are chosen in descending order, ties to the lowest index.  A
+// logit or value that is -inf or NaN is never chosen; where fewer than K
+// are left, the remaining ids are -1 and their weights 0.
+//
+// One warp per token: lane l holds the values of experts l, l + 32, ... as
+// order-preserving unsigned keys (0 = cannot be chosen), so that a round of
+// the selection is one redux.sync maximum over the lanes' best keys and one
+// redux.sync minimum over the indices that hold it.
+#include "ep_experts.cuh"
+
+namespace ep {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 8;
+
+template <typename T>
+__device__ __forceinline__ float logit(const void* p, long long i) { return to_f32(static_cast<const T*>(p)[i]); }
+
+// Unsigned key in the order of v; 0 for -inf and NaN.  Adding +0 makes -0 and
+// +0 the same key.
+__device__ __forceinline__ unsigned key_of(float v) {
+  if (!(v > -INFINITY)) return 0;
+  const unsigned u = __float_as_uint(v + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(unsigned key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+__device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+// exp(z - m), 0 where the logit cannot be chosen.
+__device__ __forceinline__ float exp_or_0(float z, float m) { return z > -INFINITY ? expf(z - m) : 0.0f; }
+
+template <typename T, int J>
+__global__ void __launch_bounds__(kWarps * 32) ep_router_kernel(const RouterParams p) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const long long row = static_cast<long long>(t) * p.E;
+  unsigned key[J];
+  float z[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane + 32 * j;
+    z[j] = e < p.E ? logit<T>(p.logits, row + e) : -INFINITY;
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane + 32 * j;
+    float v = z[j];
+    if (p.sigmoid) {
+      v = sigmoidf(z[j]);
+      if (p.bias != nullptr && e < p.E) v += p.bias[e];
+    }
+    key[j] = z[j] > -INFINITY ? key_of(v) : 0;
+  }
+  // Softmax over all experts: the largest logit and the sum of exponentials.
+  float zmax = 0.0f, zsum = 1.0f;
+  if (!p.sigmoid && !p.normalize) {
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) m = max(m, key[j]);
+    m = __reduce_max_sync(kAll, m);
+    zmax = m ? value_of(m) : 0.0f;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) s += exp_or_0(z[j], zmax);
+    zsum = warp_sum(s);
+  }
+  if (p.groups > 1) {
+    const int per = p.E / p.groups;
+    unsigned gkey = 0;  // lane g: group g's rank
+    for (int g = 0; g < p.groups; ++g) {
+      unsigned a = 0, b = 0;  // this lane's two best of group g
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int e = lane + 32 * j;
+        if (e >= g * per && e < (g + 1) * per) {
+          const unsigned k = key[j];
+          b = max(b, min(a, k));
+          a = max(a, k);
+        }
+      }
+      const unsigned best = __reduce_max_sync(kAll, a);
+      const unsigned holders = __ballot_sync(kAll, a == best);
+      // The second best: the best again where two lanes hold it, else the
+      // best of the other lanes' first and the holder's second.
+      const unsigned second = __reduce_max_sync(
+          kAll, (holders & (holders - 1)) ? best : (a == best ? b : a));
+      // Half the sum of the two: the same order, and two logits at the type's
+      // lowest value do not overflow to -inf.
+      if (lane == g && best != 0) {
+        const float f = value_of(best);
+        gkey = key_of(0.5f * f + 0.5f * (second != 0 ? value_of(second) : f));
+      }
+    }
+    unsigned keep = 0;
+    for (int i = 0; i < p.kept; ++i) {
+      const unsigned best = __reduce_max_sync(kAll, gkey);
+      if (best == 0) break;
+      const int g = __ffs(__ballot_sync(kAll, gkey == best)) - 1;
+      keep |= 1u << g;
+      if (lane == g) gkey = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = lane + 32 * j;
+      if (e < p.E && !((keep >> (e / per)) & 1)) key[j] = 0;
+    }
+  }
+  int mine = -1;  // lane k: the k-th choice
+  for (int k = 0; k < p.K; ++k) {
+    unsigned best = 0;
+    int at = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j;
+      }
+    const unsigned top = __reduce_max_sync(kAll, best);
+    if (top == 0) break;
+    const unsigned e = __reduce_min_sync(kAll, best == top ? static_cast<unsigned>(lane + 32 * at) : 0x7fffffffu);
+    if (lane == k) mine = static_cast<int>(e);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (static_cast<unsigned>(lane + 32 * j) == e) key[j] = 0;
+  }
+  // Weights: lane k has the k-th choice's.
+  const float zk = mine >= 0 ? logit<T>(p.logits, row + mine) : -INFINITY;
+  float w;
+  if (p.sigmoid) {
+    w = mine >= 0 ? sigmoidf(zk) : 0.0f;
+    if (p.normalize) {
+      const float total = warp_sum(w);
+      w = total > 0.0f ? w / total : 0.0f;
+    }
+  } else if (p.normalize) {
+    const float m = __shfl_sync(kAll, zk, 0);  // the first choice has the largest logit
+    w = exp_or_0(zk, m);
+    const float total = warp_sum(w);
+    w = total > 0.0f ? w / total : 0.0f;
+  } else {
+    w = exp_or_0(zk, zmax) / (zsum > 0.0f ? zsum : 1.0f);
+  }
+  if (lane < p.K) {
+    p.idx[static_cast<long long>(t) * p.K + lane] = mine;
+    p.w[static_cast<long long>(t) * p.K + lane] = w * p.scale;
+  }
+}
+
+// d loss / d logits, the choice held fixed.  With s_k the chosen scores, S
+// their sum and g the gradient of the weights (times `scale`):
+//   sigmoid              ds_k = g_k                 (dz = ds s (1 - s))
+//   sigmoid, normalised  ds_k = (g_k - sum g s / S) / S
+//   softmax, normalised  dz_k = w_k (g_k - sum g w)
+//   softmax              dz_e = p_e ([e chosen] g_e - sum_k g_k p_k), every e
+// The row is written once densely and the K chosen entries after it: bound by
+// the write of [T][E].
+template <typename T, int J>
+__global__ void __launch_bounds__(kWarps * 32) ep_router_bwd_kernel(const RouterParams p) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const long long row = static_cast<long long>(t) * p.E, krow = static_cast<long long>(t) * p.K;
+  T* out = static_cast<T*>(p.grad_logits) + row;
+  long long e = lane < p.K ? p.idx[krow + lane] : -1;
+  if (e < 0 || e >= p.E) e = -1;
+  const float g = e >= 0 ? p.grad[krow + lane] * p.scale : 0.0f;
+  const float ze = e >= 0 ? logit<T>(p.logits, row + e) : -INFINITY;
+  float d;
+  if (p.sigmoid || p.normalize) {
+    if (p.sigmoid) {
+      const float s = e >= 0 ? sigmoidf(ze) : 0.0f;
+      float ds = g;
+      if (p.normalize) {
+        const float S = warp_sum(s), gs = warp_sum(g * s);
+        ds = S > 0.0f ? (g - gs / S) / S : 0.0f;
+      }
+      d = ds * s * (1.0f - s);
+    } else {
+      const unsigned m = __reduce_max_sync(kAll, key_of(ze));
+      const float x = exp_or_0(ze, m ? value_of(m) : 0.0f);
+      const float S = warp_sum(x);
+      const float w = S > 0.0f ? x / S : 0.0f;
+      d = w * (g - warp_sum(g * w));
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (lane + 32 * j < p.E) out[lane + 32 * j] = from_f32<T>(0.0f);
+  } else {
+    float z[J];
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      z[j] = lane + 32 * j < p.E ? logit<T>(p.logits, row + lane + 32 * j) : -INFINITY;
+      m = max(m, key_of(z[j]));
+    }
+    m = __reduce_max_sync(kAll, m);
+    const float zmax = m ? value_of(m) : 0.0f;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      z[j] = exp_or_0(z[j], zmax);
+      s += z[j];
+    }
+    s = warp_sum(s);
+    const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+    const float pe = exp_or_0(ze, zmax) * inv;
+    const float inner = warp_sum(g * pe);
+    d = pe * (g - inner);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (lane + 32 * j < p.E) out[lane + 32 * j] = from_f32<T>(z[j] * inv * -inner);
+  }
+  __syncwarp();  // orders the dense writes before the chosen entries'
+  if (e >= 0) out[e] = from_f32<T>(d);
+}
+
+template <typename T, bool bwd>
+cudaError_t launch_typed(const RouterParams& p, cudaStream_t s) {
+  const dim3 grid((p.T + kWarps - 1) / kWarps), block(kWarps * 32);
+  const int j = (p.E + 31) / 32;
+#define EP_ROUTER(JJ)                                                                   \
+  if (j <= JJ) {                                                                        \
+    if constexpr (bwd) return launch_pdl(ep_router_bwd_kernel<T, JJ>, grid, block, 0, s, 0, p); \
+    else return launch_pdl(ep_router_kernel<T, JJ>, grid, block, 0, s, 0, p);           \
+  }
+  EP_ROUTER(1)
+  EP_ROUTER(2)
+  EP_ROUTER(4)
+  EP_ROUTER(8)
+  EP_ROUTER(16)
+  EP_ROUTER(32)
+#undef EP_ROUTER
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_router(const RouterParams& p, int, cudaStream_t s) {
+  if (p.dtype == EP_DTYPE_FP32) return launch_typed<float, false>(p, s);
+  if (p.dtype == EP_DTYPE_FP16) return launch_typed<__half, false>(p, s);
+  return launch_typed<__nv_bfloat16, false>(p, s);
+}
+
+cudaError_t launch_router_bwd(const RouterParams& p, int, cudaStream_t s) {
+  if (p.dtype == EP_DTYPE_FP32) return launch_typed<float, true>(p, s);
+  if (p.dtype == EP_DTYPE_FP16) return launch_typed<__half, true>(p, s);
+  return launch_typed<__nv_bfloat16, true>(p, s);
+}
+
+}  // namespace ep

@@ -456,6 +456,123 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t handle, const void* const* gr
                                        const float* const* g_recv_topk_weights, int64_t num_tokens,
                                        void* grad_tokens, float* grad_topk_weights, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Expert products: what runs on the receive rows between dispatch and
+ * combine, and its backward pass, on a prepared handle.
+ *
+ * Experts.  A single-buffer layer's E experts, or a sharded layer's own E/N
+ * (a rank-major layer is refused: use the owner's single-buffer layer).  With
+ * c_e, p_e and off_e of the handle's last prepare, expert e's rows are
+ * [off_e, off_e + c_e).  Only those are read.  Row outputs are written in
+ * [off_e, off_e + p_e), zeros in the padding rows whatever the inputs hold
+ * there; rows from P on are left alone.  On a handle without a prepare, or
+ * after one that overflowed (or, sharded, disagreed with the gathered
+ * counts), nothing is read or written.  The rows stay on the device: no call
+ * needs the counts on the host.
+ *
+ * Types.  Row buffers (R rows), weights and row outputs hold the layer's
+ * payload type.  Sums are float32, rounded once at the end, so the activation
+ * is applied to unrounded sums.  Feature counts are multiples of 8 up to 2^20
+ * and need not match the layer's hidden.  Pointers are 16-byte aligned;
+ * outputs must not overlap inputs.  The order of a sum is fixed by the sizes
+ * and the counts: the same inputs give the same bits.
+ *
+ * Weights are [E][out_features][in_features], row-major.  A gated layer keeps
+ * its two input matrices in one [E][2*ffn_features][in_features]: gate rows
+ * first, then up rows; act = silu(gate) * up.
+ * ------------------------------------------------------------------------ */
+
+/* y[r] = w[e] x[r].   x [R, in], w [E, out, in], y [R, out] out. */
+ep_status_t ep_expert_gemm(ep_handle_t handle, const void* x, const void* w, int64_t out_features,
+                           int64_t in_features, void* y, void* stream);
+
+/* pre[r] = w[e] x[r] (gate, then up), act[r] = silu(gate) * up.
+ *   x [R, in], w [E, 2*ffn, in], pre [R, 2*ffn] out or NULL (not kept),
+ *   act [R, ffn] out. */
+ep_status_t ep_expert_gemm_swiglu(ep_handle_t handle, const void* x, const void* w, int64_t ffn_features,
+                                  int64_t in_features, void* pre, void* act, void* stream);
+
+/* Input gradient of ep_expert_gemm: dx[r] = transpose(w[e]) dy[r].
+ *   dy [R, out], w [E, out, in], dx [R, in] out. */
+ep_status_t ep_expert_dgrad(ep_handle_t handle, const void* dy, const void* w, int64_t out_features,
+                            int64_t in_features, void* dx, void* stream);
+
+/* Input gradient of a product whose input is act, taken through the
+ * activation: da = transpose(w[e]) dy[r] (not stored), then with s =
+ * sigmoid(gate)
+ *   dpre gate half = da * up * s * (1 + gate * (1 - s)),
+ *   dpre up half   = da * gate * s.
+ *   dy [R, out], w [E, out, ffn], pre [R, 2*ffn], dpre [R, 2*ffn] out. */
+ep_status_t ep_expert_dgrad_swiglu(ep_handle_t handle, const void* dy, const void* w, const void* pre,
+                                   int64_t out_features, int64_t ffn_features, void* dpre, void* stream);
+
+/* Weight gradient: dw[e][n][k] = sum over the expert's rows of dy[r][n] x[r][k];
+ * accumulate = 1 adds it to dw (one float32 addition per element, then the
+ * rounding to dw's type).  An expert without rows gets zeros, or keeps its
+ * dw.   dy [R, out], x [R, in], dw [E, out, in] out, of the payload type or
+ * float32 (dw_dtype). */
+ep_status_t ep_expert_wgrad(ep_handle_t handle, const void* dy, const void* x, int64_t out_features,
+                            int64_t in_features, void* dw, int64_t dw_dtype, int accumulate, void* stream);
+
+/* Products of a few rows per expert with 4-bit weights (serving; bf16 and
+ * fp16 layers).  w[e][n][k] = scales[e][n][k / group] * (q - 8), q the
+ * unsigned nibble k of a row: low half of byte k/2 for even k, high half for
+ * odd k.  The sum over a group is taken on the integers, then multiplied by
+ * its scale in float32.
+ *   x [R, in], wq uint8 [E, out, in/2], scales [E, out, in/group] of the
+ *   payload type, y [R, out] out; group 32, 64 or 128, dividing in. */
+ep_status_t ep_expert_gemv_w4(ep_handle_t handle, const void* x, const uint8_t* wq, const void* scales,
+                              int64_t out_features, int64_t in_features, int64_t group, void* y, void* stream);
+
+/* The gated pair of it: act[r] = silu(gate) * up.
+ *   wq [E, 2*ffn, in/2], scales [E, 2*ffn, in/group], act [R, ffn] out. */
+ep_status_t ep_expert_gemv_w4_swiglu(ep_handle_t handle, const void* x, const uint8_t* wq, const void* scales,
+                                     int64_t ffn_features, int64_t in_features, int64_t group, void* act,
+                                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * Router: from a gate's logits to the topk_idx and topk_weights that prepare
+ * and dispatch take, and back.  Needs no layer and no handle.
+ *
+ * Selection values: v = logit (softmax), or sigmoid(logit) + bias (sigmoid;
+ * the bias steers the choice and does not enter the weights).  With
+ * num_groups > 1 the experts form groups of E/num_groups consecutive ones, a
+ * group's rank is the sum of its two largest v (twice the largest where only
+ * one can be chosen) and only the topk_groups highest groups' experts stay.
+ * The top_k largest v are chosen, in descending order; ties go to the lower
+ * index, between groups too.  An expert whose logit or v is -infinity or NaN
+ * is never chosen; where fewer than top_k can be chosen the remaining ids are
+ * -1 with weight 0, which the expert-parallel calls take as masked routes.
+ *
+ * Weights: the chosen experts' scores (softmax over all logits that can be
+ * chosen, whether their group stayed or not; or sigmoid), with normalize = 1
+ * divided by their sum (0 where that sum is 0), times scale.  All arithmetic
+ * is float32.
+ * ------------------------------------------------------------------------ */
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t;
+
+typedef struct {
+  int64_t num_experts;  /* E, 1 .. EP_MAX_EXPERTS */
+  int64_t top_k;        /* K, 1 .. min(EP_MAX_TOPK, E) */
+  int64_t num_groups;   /* 1 .. 32, divides E */
+  int64_t topk_groups;  /* 1 .. num_groups */
+  int64_t score;        /* ep_score_t */
+  int64_t normalize;    /* 0 or 1 */
+  int64_t dtype;        /* ep_dtype_t of logits and their gradient */
+  float scale;          /* finite */
+} ep_router_config_t;
+
+/* logits [T, E], bias float32 [E] or NULL (sigmoid only), topk_idx int64
+ * [T, K] out, topk_weights float32 [T, K] out. */
+ep_status_t ep_router(ep_router_config_t config, const void* logits, const float* bias, int64_t num_tokens,
+                      int64_t* topk_idx, float* topk_weights, void* stream);
+
+/* Gradient of the weights with the choice held fixed: grad_logits [T, E] out
+ * (every element written) from grad_topk_weights float32 [T, K], the choice
+ * topk_idx and the logits given to ep_router.  Masked routes have no part. */
+ep_status_t ep_router_bwd(ep_router_config_t config, const void* logits, const int64_t* topk_idx,
+                          const float* grad_topk_weights, int64_t num_tokens, void* grad_logits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
