@@ -16,7 +16,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
-SOURCES = ["ep_api.cu", "ep_route.cu", "ep_rows.cu", "ep_experts_api.cu", "ep_products.cu", "ep_w4.cu",
+SOURCES = ["ep_api.cu", "ep_route.cu", "ep_rows.cu", "ep_experts_api.cu", "ep_products.cu", "ep_products_tc.cu", "ep_w4.cu",
            "ep_router.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

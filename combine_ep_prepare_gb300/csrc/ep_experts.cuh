@@ -116,6 +116,8 @@ __device__ __forceinline__ void swiglu_bwd(float gate, float up, float da, float
 
 // Plain products on the CUDA cores (every type).
 cudaError_t launch_product_simt(const ProductParams& p, int num_sms, cudaStream_t s);
+// The same on the tensor cores (bf16, fp16).
+cudaError_t launch_product_tc(const ProductParams& p, int num_sms, cudaStream_t s);
 
 struct W4Params {
   int* hdr;

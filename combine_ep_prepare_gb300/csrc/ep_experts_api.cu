@@ -65,7 +65,8 @@ ep_status_t enqueue(const ep::ProductParams& p, const char* where, void* stream)
   ep_status_t st = ep::api_device(&sms);
   if (st != EP_OK) return st;
   if (p.R == 0 && p.kind != ep::kProdWgrad) return EP_OK;
-  const cudaError_t e = ep::launch_product_simt(p, sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = p.dtype == EP_DTYPE_FP32 ? ep::launch_product_simt(p, sms, static_cast<cudaStream_t>(stream))
+                                                 : ep::launch_product_tc(p, sms, static_cast<cudaStream_t>(stream));
   ep::api_count_launches(1);
   if (e != cudaSuccess) return ep::api_cuda_fail(e, where);
   return EP_OK;

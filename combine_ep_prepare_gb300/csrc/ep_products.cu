@@ -285,9 +285,7 @@ cudaError_t launch_typed(const ProductParams& p, int num_sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_product_simt(const ProductParams& p, int num_sms, cudaStream_t s) {
-  if (p.dtype == EP_DTYPE_FP32) return launch_typed<float>(p, num_sms, s);
-  if (p.dtype == EP_DTYPE_FP16) return launch_typed<__half>(p, num_sms, s);
-  return launch_typed<__nv_bfloat16>(p, num_sms, s);
+  return launch_typed<float>(p, num_sms, s);
 }
 
 }  // namespace ep

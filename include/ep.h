@@ -480,6 +480,11 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t handle, const void* const* gr
  * Weights are [E][out_features][in_features], row-major.  A gated layer keeps
  * its two input matrices in one [E][2*ffn_features][in_features]: gate rows
  * first, then up rows; act = silu(gate) * up.
+ *
+ * bf16 and fp16 products run on the tensor cores.  Their waits on copies and
+ * on the tensor core are bounded: one that runs out ends the kernel, leaves
+ * the call's outputs incomplete and adds EP_ST_TIMEOUT to the status word,
+ * without EP_ST_NOT_PREPARED; the next prepare clears it.
  * ------------------------------------------------------------------------ */
 
 /* y[r] = w[e] x[r].   x [R, in], w [E, out, in], y [R, out] out. */
