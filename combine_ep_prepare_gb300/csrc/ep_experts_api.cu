@@ -86,7 +86,7 @@ ep_status_t w4(ep_handle_t h, bool gated, const void* x, const uint8_t* wq, cons
   if (K % group != 0) return fail(EP_ERR_SHAPE, "%s: in_features %lld is not a multiple of the group", where, (long long)K);
   if ((st = check_ptr(x, "x")) != EP_OK) return st;
   if ((st = check_ptr(wq, "wq")) != EP_OK) return st;
-  if ((st = check_ptr(scales, "scales", 2)) != EP_OK) return st;
+  if ((st = check_ptr(scales, "scales")) != EP_OK) return st;
   if ((st = check_ptr(out, "out")) != EP_OK) return st;
   int sms = 0;
   if ((st = ep::api_device(&sms)) != EP_OK) return st;

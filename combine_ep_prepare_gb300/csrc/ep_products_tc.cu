@@ -102,6 +102,7 @@ struct Walk {
       o->n = ((o->cnt + nb - 1) / nb + 31) & ~31;
       o->r0 = b * o->n;
       o->last = b + 1 == nb;
+      if (o->last) o->n = (o->cnt - o->r0 + 31) & ~31;
       o->slabs = ((kind == kProdFwd || kind == kProdFwdSwiglu ? p.K : p.N) + kSlab - 1) / kSlab;
     }
   }
@@ -151,11 +152,13 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// Outputs are stored as streaming data, first to leave L2, which the operands
+// need: dgrad of 16,384 rows x 4096 -> 7168 took 634 us without, 558 us with.
 template <typename T>
-__device__ __forceinline__ void store2(T* p, float x, float y) { *reinterpret_cast<uint32_t*>(p) = pack2<T>(x, y); }
+__device__ __forceinline__ void store2(T* p, float x, float y) { __stcs(reinterpret_cast<uint32_t*>(p), pack2<T>(x, y)); }
 template <typename T>
 __device__ __forceinline__ void store4(T* p, const float4& v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+  __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w)));
 }
 template <typename T>
 __device__ __forceinline__ float4 unpack4(uint2 u) {
@@ -186,7 +189,7 @@ constexpr int kRows = 16;  // tile rows per step of the epilogue
 // four warps put their 32 features side by side into shared memory and read
 // the rows back, four rows and all 128 features a warp.  A store then covers
 // whole 128-byte lines of one row.
-template <typename T, int kind>
+template <typename T, int kind, typename O>
 struct Rows {
   const ProductParams& p;
   const Tile& t;
@@ -208,8 +211,7 @@ struct Rows {
   // Adds what wgrad's output holds.
   __device__ __forceinline__ void add_old(int r, float4* x) const {
     const long long i = at + static_cast<long long>(r) * cols;
-    const float4 y = p.out_f32 ? *reinterpret_cast<const float4*>(static_cast<const float*>(p.out) + i)
-                               : load4(static_cast<const T*>(p.out) + i);
+    const float4 y = load4(static_cast<const T*>(p.out) + i);
     *x = make_float4(x->x + y.x, x->y + y.y, x->z + y.z, x->w + y.w);
   }
   // Row r of the tile from the sums x (gated: gate and up of two features).
@@ -229,7 +231,7 @@ struct Rows {
       store4(out, make_float4(x.x * u.x * s0 * (1.0f + g.x * (1.0f - s0)), x.y * u.y * s1 * (1.0f + g.y * (1.0f - s1)),
                               x.z * u.z * s2 * (1.0f + g.z * (1.0f - s2)), x.w * u.w * s3 * (1.0f + g.w * (1.0f - s3))));
       store4(out + p.K, make_float4(x.x * g.x * s0, x.y * g.y * s1, x.z * g.z * s2, x.w * g.w * s3));
-    } else if (kind == kProdWgrad && p.out_f32) {
+    } else if constexpr (sizeof(O) == 4) {
       *reinterpret_cast<float4*>(static_cast<float*>(p.out) + i) = x;
     } else {
       store4(out, x);
@@ -237,10 +239,42 @@ struct Rows {
   }
 };
 
-template <typename T, int kind>
+template <typename T, int kind, typename O>
 __device__ __forceinline__ void write_half(const ProductParams& p, const Tile& t, uint32_t acc, int rank, int w, int half,
                                            int lane, float* stage) {
-  const Rows<T, kind> rows(p, t, rank, lane);
+  if constexpr (sizeof(O) == 4) {
+    // float32 gradients: a lane's feature of one row from 32 lanes is a whole
+    // line as it is.
+    const int f = t.f0 + rank * kHalfM + w * 32 + lane, stop = f < p.K ? p.N - t.r0 : 0;
+    float* out = static_cast<float*>(p.out) + (static_cast<long long>(t.e) * p.N + t.r0) * p.K + f;
+#pragma unroll 1
+    for (int c = 32 * half; c < t.n; c += 64) {
+      float v[32];
+      __syncwarp();
+      tc::tmem_ld32(acc + c, v);
+      tc::tmem_ld_wait();
+      float* o = out + static_cast<long long>(c) * p.K;
+      if (c + 32 <= stop) {
+        if (p.accumulate) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += o[static_cast<long long>(j) * p.K];
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) __stcs(o + static_cast<long long>(j) * p.K, v[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c + j < stop) o[static_cast<long long>(j) * p.K] = p.accumulate ? v[j] + o[static_cast<long long>(j) * p.K] : v[j];
+      }
+    }
+    return;
+  }
+  const Rows<T, kind, O> rows(p, t, rank, lane);
+  constexpr bool gated = kind == kProdFwdSwiglu || kind == kProdDgradSwiglu;
+  // What needs no arithmetic after the sum is rounded before it is put: a
+  // word holds two rows' values of a feature, and shared memory, which the
+  // tensor core reads its operands from meanwhile, moves half the bytes.
+  constexpr bool packed = !gated;
   uint2 raw[2][4] = {};  // dgrad through the activation: gate and up values, read a step ahead of their use
   auto load_pre = [&](int r0) {
 #pragma unroll
@@ -252,53 +286,92 @@ __device__ __forceinline__ void write_half(const ProductParams& p, const Tile& t
   };
   if constexpr (kind == kProdDgradSwiglu) load_pre(kRows * half + 4 * w);
   float* put = stage + w * 32 + lane;
-  const float* get = stage + 4 * w * kHalfM + (kind == kProdFwdSwiglu ? (lane >> 3) * 32 + 2 * (lane & 7) : 4 * lane);
+  const float* get = stage + (packed ? 2 : 4) * w * kHalfM + (kind == kProdFwdSwiglu ? (lane >> 3) * 32 + 2 * (lane & 7) : 4 * lane);
 #pragma unroll 1
   for (int c = kRows * half; c < t.n; c += 2 * kRows) {
     float v[kRows];
     __syncwarp();
     tc::tmem_ld16(acc + c, v);
     tc::tmem_ld_wait();
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) put[j * kHalfM] = v[j];
-    half_sync(half);
-    float4 x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (kind == kProdFwdSwiglu) {
-        // gate features 16 q + m sit at 32 q + m, their up rows 16 further on
-        const float2 g = *reinterpret_cast<const float2*>(get + i * kHalfM);
-        const float2 u = *reinterpret_cast<const float2*>(get + i * kHalfM + 16);
-        x[i] = make_float4(g.x, g.y, u.x, u.y);
-      } else {
-        x[i] = *reinterpret_cast<const float4*>(get + i * kHalfM);
-      }
-    }
-    half_sync(half);  // read: the next rows may be put
     const int r0 = c + 4 * w;
-    if (r0 + 3 < rows.stop) {
-      if (kind == kProdWgrad && p.accumulate) {
+    if (kind == kProdWgrad && p.accumulate) {
+      // The old values are added in float32, before the rounding: the rows
+      // go through shared memory unrounded, eight at a time.
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rows.add_old(r0 + i, &x[i]);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) put[j * kHalfM] = v[8 * h + j];
+        half_sync(half);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float4 x = *reinterpret_cast<const float4*>(stage + (2 * w + i) * kHalfM + 4 * lane);
+          const int r = c + 8 * h + 2 * w + i;
+          if (r < rows.stop) {
+            rows.add_old(r, &x);
+            rows.put(r, x, raw[0][0], raw[1][0]);
+          }
+        }
+        half_sync(half);
       }
+      continue;
+    }
+    if constexpr (packed) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rows.put(r0 + i, x[i], raw[0][i], raw[1][i]);
+      for (int j = 0; j < kRows; j += 2) put[j / 2 * kHalfM] = __uint_as_float(pack2<T>(v[j], v[j + 1]));
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (r0 + i < rows.stop) {
-          if (kind == kProdWgrad && p.accumulate) rows.add_old(r0 + i, &x[i]);
-          rows.put(r0 + i, x[i], raw[0][i], raw[1][i]);
-        }
+      for (int j = 0; j < kRows; ++j) put[j * kHalfM] = v[j];
     }
-    if constexpr (kind == kProdDgradSwiglu) load_pre(r0 + 2 * kRows);
+    half_sync(half);
+    if constexpr (packed) {
+      uint2 y[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 q = *reinterpret_cast<const uint4*>(get + i * kHalfM);
+        y[2 * i] = make_uint2(__byte_perm(q.x, q.y, 0x5410), __byte_perm(q.z, q.w, 0x5410));
+        y[2 * i + 1] = make_uint2(__byte_perm(q.x, q.y, 0x7632), __byte_perm(q.z, q.w, 0x7632));
+      }
+      half_sync(half);  // read: the next rows may be put
+      T* out = static_cast<T*>(p.out) + rows.at + static_cast<long long>(r0) * rows.cols;
+      if (r0 + 3 < rows.stop) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __stcs(reinterpret_cast<uint2*>(out + static_cast<long long>(i) * rows.cols), y[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r0 + i < rows.stop) *reinterpret_cast<uint2*>(out + static_cast<long long>(i) * rows.cols) = y[i];
+      }
+    } else {
+      float4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (kind == kProdFwdSwiglu) {
+          // gate features 16 q + m sit at 32 q + m, their up rows 16 further on
+          const float2 g = *reinterpret_cast<const float2*>(get + i * kHalfM);
+          const float2 u = *reinterpret_cast<const float2*>(get + i * kHalfM + 16);
+          x[i] = make_float4(g.x, g.y, u.x, u.y);
+        } else {
+          x[i] = *reinterpret_cast<const float4*>(get + i * kHalfM);
+        }
+      }
+      half_sync(half);
+      if (r0 + 3 < rows.stop) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows.put(r0 + i, x[i], raw[0][i], raw[1][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r0 + i < rows.stop) rows.put(r0 + i, x[i], raw[0][i], raw[1][i]);
+      }
+      if constexpr (kind == kProdDgradSwiglu) load_pre(r0 + 2 * kRows);
+    }
   }
 }
 
 // Rows [begin, end) of the tile (counted from its first) become zeros.
-template <typename T, int kind>
+template <typename T, int kind, typename O>
 __device__ __forceinline__ void zero_rows(const ProductParams& p, const Tile& t, int rank, int lane, int begin, int end) {
-  const Rows<T, kind> rows(p, t, rank, lane);
+  const Rows<T, kind, O> rows(p, t, rank, lane);
   if (rows.stop == 0) return;
   // A zero gate and a zero sum make every output zero.
   for (int r = begin; r < end; r += kEpilogueWarps)
@@ -322,7 +395,7 @@ struct Shared {
 constexpr size_t kSmemBytes =
     static_cast<size_t>(kStages) * (kABytes + kBBytes) + 2 * kRows * kHalfM * sizeof(float) + 1024 + sizeof(Shared);
 
-template <typename T, int kind>
+template <typename T, int kind, typename O>
 __global__ void __launch_bounds__(kThreads, 1)
     ep_product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                          const __grid_constant__ CUtensorMap map_b64, const __grid_constant__ CUtensorMap map_b32,
@@ -341,9 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tma_prefetch_desc(&map_b);
     tc::tma_prefetch_desc(&map_b16);
     for (int i = 0; i < kStages; ++i) {
-      // The first block's two loading warps account for both blocks' copies;
-      // in wgrad each block's loading warps, or its zeroing warp twice, do.
-      tc::mbar_init(tc::smem_addr(&s.full[i]), kind == kProdWgrad ? 4 : 2);
+      // The first block's two loaders account for both blocks' copies.  A
+      // ragged slab of wgrad lands in each block by itself, and each block's
+      // zeroing warp then arrives.
+      tc::mbar_init(tc::smem_addr(&s.full[i]), 2);
       tc::mbar_init(tc::smem_addr(&s.landed[i]), 2);
       tc::mbar_init(tc::smem_addr(&s.empty[i]), 1);
     }
@@ -387,15 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < t.slabs; ++k) {
             if (!tc::mbar_wait(tc::smem_addr(&s.empty[stage]), phase ^ 1, gave_up)) break;
             const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * (kABytes + kBBytes)), b = a + kABytes;
-            uint32_t bar = rank == 0 && kind != kProdWgrad ? tc::smem_addr(&s.full[stage])
-                                                           : tc::in_block(tc::smem_addr(&s.full[stage]), 0);
+            uint32_t bar = rank == 0 ? tc::smem_addr(&s.full[stage]) : tc::in_block(tc::smem_addr(&s.full[stage]), 0);
             if (kind == kProdWgrad && (t.cnt - k * kSlab) < kSlab && ((t.cnt - k * kSlab) & 15)) {
               bar = tc::smem_addr(&s.landed[stage]);  // its rows past the end are zeroed before `full`
               tc::mbar_expect(bar, bytes);
-            } else if (kind == kProdWgrad) {
-              tc::mbar_expect_cluster(bar, bytes);
             } else if (rank == 0) {
-              tc::mbar_expect(bar, 2 * bytes);
+              tc::mbar_expect(bar, 2 * bytes);  // the other block's copies too
             }
             const int x = k * kSlab;
             if (load_a) {
@@ -505,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(slab + j / chunks * kBoxBytes + left * 128 + j % chunks * 16) = make_uint4(0, 0, 0, 0);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane < 2) tc::mbar_publish_cluster(tc::in_block(tc::smem_addr(&s.full[at]), 0));
+        if (lane == 0) tc::mbar_publish_cluster(tc::in_block(tc::smem_addr(&s.full[at]), 0));
       }
     } else if (warp >= 4) {
       int buf = 0;
@@ -523,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;  // an expert without rows keeps its gradient
         }
         if (has) {
-          write_half<T, kind>(p, t, tmem + buf * kTileN + (static_cast<uint32_t>(w * 32) << 16), rank, w, half, lane,
+          write_half<T, kind, O>(p, t, tmem + buf * kTileN + (static_cast<uint32_t>(w * 32) << 16), rank, w, half, lane,
                               rows_out + half * kRows * kHalfM);
           tc::fence_before();
           __syncwarp();
@@ -535,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Padding rows; wgrad: the gradient of an expert without rows.
         if (kind == kProdWgrad ? !has : t.last)
-          zero_rows<T, kind>(p, t, rank, lane, (kind == kProdWgrad ? 0 : t.cnt - t.r0) + warp - 4,
+          zero_rows<T, kind, O>(p, t, rank, lane, (kind == kProdWgrad ? 0 : t.cnt - t.r0) + warp - 4,
                              kind == kProdWgrad ? min(t.n, p.N - t.r0) : t.rows - t.r0);
       }
     }
@@ -583,7 +654,7 @@ bool gated_map(CUtensorMap* m, const ProductParams& p) {
 
 // Pairs of blocks that fit on the current device at once (0: the query
 // failed); the kernel's shared memory is raised on the way.  Once per device.
-template <typename T, int kind>
+template <typename T, int kind, typename O>
 int resident_pairs(int num_sms) {
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices];
@@ -591,7 +662,7 @@ int resident_pairs(int num_sms) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   int pairs = known[dev].load(std::memory_order_acquire);
   if (pairs == 0) {
-    const auto kern = ep_product_tc_kernel<T, kind>;
+    const auto kern = ep_product_tc_kernel<T, kind, O>;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes)) != cudaSuccess)
       return 0;
@@ -612,7 +683,7 @@ int resident_pairs(int num_sms) {
   return pairs;
 }
 
-template <typename T, int kind>
+template <typename T, int kind, typename O = T>
 cudaError_t launch_kind(const ProductParams& p, int num_sms, cudaStream_t s) {
   CUtensorMap a, b, b64, b32, b16;
   const long long R = p.R > 0 ? p.R : 1;  // without rows nothing is read through the maps
@@ -627,9 +698,9 @@ cudaError_t launch_kind(const ProductParams& p, int num_sms, cudaStream_t s) {
          rows_map(&b32, p.a, p.dtype, fwd ? p.K : p.N, R, 32) && rows_map(&b16, p.a, p.dtype, fwd ? p.K : p.N, R, 16);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const int pairs = resident_pairs<T, kind>(num_sms);
+  const int pairs = resident_pairs<T, kind, O>(num_sms);
   if (pairs == 0) return cudaErrorLaunchOutOfResources;
-  return launch_pdl(ep_product_tc_kernel<T, kind>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, 2, a, b, b64, b32, b16, p);
+  return launch_pdl(ep_product_tc_kernel<T, kind, O>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, 2, a, b, b64, b32, b16, p);
 }
 
 template <typename T>
@@ -639,7 +710,7 @@ cudaError_t launch_typed(const ProductParams& p, int num_sms, cudaStream_t s) {
     case kProdFwdSwiglu: return launch_kind<T, kProdFwdSwiglu>(p, num_sms, s);
     case kProdDgrad: return launch_kind<T, kProdDgrad>(p, num_sms, s);
     case kProdDgradSwiglu: return launch_kind<T, kProdDgradSwiglu>(p, num_sms, s);
-    default: return launch_kind<T, kProdWgrad>(p, num_sms, s);
+    default: return p.out_f32 ? launch_kind<T, kProdWgrad, float>(p, num_sms, s) : launch_kind<T, kProdWgrad>(p, num_sms, s);
   }
 }
 

@@ -107,7 +107,8 @@ struct Shared {
   int cum[EP_MAX_EXPERTS + 1];
 };
 constexpr int kRedBytes = 16 * 1024;
-constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kRedBytes + 1024 + sizeof(Shared);
+constexpr int kScaleBytes = kWarps * kBoxRows * 8 * 2;
+constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kRedBytes + kScaleBytes + 1024 + sizeof(Shared);
 
 // cum[e] = units of the experts before e when the reduction is split KW ways.
 __device__ __forceinline__ void scan_units(const W4Params& p, int KW, Shared& s) {
@@ -147,42 +148,49 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;
 // One unit of a consumer warp; stage and phase follow the ring.  False when a
 // wait gave up.
 template <typename T, int G, bool gated, int NT>
-__device__ __forceinline__ bool unit_sums(const W4Params& p, const Unit& u, unsigned char* ring, Shared& s, int* stage,
-                                          uint32_t* phase, float (&total)[2][NT][4]) {
+__device__ __forceinline__ bool unit_sums(const W4Params& p, const Unit& u, unsigned char* ring, T* scale_buf, Shared& s,
+                                          int* stage, uint32_t* phase, float (&total)[2][NT][4]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int sub = warp % u.kw, group = warp / u.kw;
-  constexpr int kGroups = kChunk / G;  // scales per weight row and stage
+  constexpr int kGroups = kChunk / G;    // scales per weight row and stage
+  constexpr int kPeriod = 8 / kGroups;   // stages that eight scales of a row last
   const int ngroups = p.K / G;
   const int chunks = (p.K + kChunk - 1) / kChunk, iters = (chunks + u.kw - 1) / u.kw;
-  // Weight rows of this lane: fragment f's rows g and g + 8 (gated: the gate
-  // row and the up row of one feature), clamped into the expert.
+  // Box rows of this lane's fragments: fragment f's rows g and g + 8 (gated:
+  // the gate row and the up row of one feature).
   int box_row[2][2];
-  const T* scale_row[2][2];
 #pragma unroll
   for (int f = 0; f < 2; ++f)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      box_row[f][h] = gated ? h * 16 + f * 8 + g : f * 16 + h * 8 + g;
-      int n;
-      if (gated) {
-        const int F = p.N / 2, j = u.n0 / 2 + group * 16 + f * 8 + g;
-        n = (j < F ? j : F - 1) + h * F;
-      } else {
-        n = u.n0 + group * kBoxRows + box_row[f][h];
-        n = n < p.N ? n : p.N - 1;
-      }
-      scale_row[f][h] = static_cast<const T*>(p.scales) + (static_cast<long long>(u.e) * p.N + n) * ngroups;
+    for (int h = 0; h < 2; ++h) box_row[f][h] = gated ? h * 16 + f * 8 + g : f * 16 + h * 8 + g;
+  // Scales: lane l brings eight of box row l, a period ahead, and the warp
+  // shares them through shared memory.
+  int n;  // this lane's weight row, clamped into the expert
+  if (gated) {
+    const int F = p.N / 2, j = u.n0 / 2 + group * 16 + (lane & 15);
+    n = (j < F ? j : F - 1) + (lane >> 4) * F;
+  } else {
+    n = u.n0 + group * kBoxRows + lane;
+    n = n < p.N ? n : p.N - 1;
+  }
+  const T* scale_row = static_cast<const T*>(p.scales) + (static_cast<long long>(u.e) * p.N + n) * ngroups;
+  const bool wide = (ngroups & 7) == 0 && ((sub * iters * kGroups) & 7) == 0;
+  auto load_scales = [&](int period) {
+    const int g0 = sub * iters * kGroups + period * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (wide) {
+      if (g0 < ngroups) v = __ldg(reinterpret_cast<const uint4*>(scale_row + g0));
+    } else {
+      unsigned short h[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        h[q] = g0 + q < ngroups ? __ldg(reinterpret_cast<const unsigned short*>(scale_row) + g0 + q) : 0;
+      v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     }
-  float sc[2][2][kGroups], next[2][2][kGroups];
-  auto load_scales = [&](int it, float (&d)[2][2][kGroups]) {
-    const int g0 = (it * u.kw + sub) * kGroups;
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int q = 0; q < kGroups; ++q) d[f][h][q] = g0 + q < ngroups ? to_f32(__ldg(scale_row[f][h] + g0 + q)) : 0.0f;
+    return v;
   };
+  T* scales = scale_buf + warp * (kBoxRows * 8);
+  uint4 next = load_scales(0);
   float acc[2][NT][4];
 #pragma unroll
   for (int f = 0; f < 2; ++f)
@@ -190,16 +198,15 @@ __device__ __forceinline__ bool unit_sums(const W4Params& p, const Unit& u, unsi
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) total[f][i][j] = acc[f][i][j] = 0.0f;
-  load_scales(0, next);
   bool fine = true;
   for (int it = 0; it < iters; ++it) {
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int q = 0; q < kGroups; ++q) sc[f][h][q] = next[f][h][q];
-    if (it + 1 < iters) load_scales(it + 1, next);
+    if (it % kPeriod == 0) {
+      __syncwarp();
+      *reinterpret_cast<uint4*>(scales + lane * 8) = next;
+      __syncwarp();
+      if (it + kPeriod < iters) next = load_scales(it / kPeriod + 1);
+    }
+    const T* sc = scales + it % kPeriod * kGroups;
     fine = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_addr(&s.full[*stage]), *phase, &s.gave_up));
     if (!fine) break;
     const unsigned char* st = ring + static_cast<size_t>(*stage) * kStageBytes;
@@ -229,14 +236,16 @@ __device__ __forceinline__ bool unit_sums(const W4Params& p, const Unit& u, unsi
       if ((kb + 1) * 32 % G == 0) {
         const int q = kb * 32 / G;
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int f = 0; f < 2; ++f) {
+          const float s0 = to_f32(sc[box_row[f][0] * 8 + q]), s1 = to_f32(sc[box_row[f][1] * 8 + q]);
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              total[f][i][j] = fmaf(sc[f][j >> 1][q], acc[f][i][j], total[f][i][j]);
+              total[f][i][j] = fmaf(j < 2 ? s0 : s1, acc[f][i][j], total[f][i][j]);
               acc[f][i][j] = 0.0f;
             }
+        }
       }
     }
     __syncwarp();
@@ -302,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Aligned by an offset, so that accesses stay known as shared-memory ones.
   unsigned char* ring = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
   float* red = reinterpret_cast<float*>(ring + static_cast<size_t>(kStages) * kStageBytes);
-  Shared& s = *reinterpret_cast<Shared*>(ring + static_cast<size_t>(kStages) * kStageBytes + kRedBytes);
+  T* scale_buf = reinterpret_cast<T*>(ring + static_cast<size_t>(kStages) * kStageBytes + kRedBytes);
+  Shared& s = *reinterpret_cast<Shared*>(ring + static_cast<size_t>(kStages) * kStageBytes + kRedBytes + kScaleBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tc::tma_prefetch_desc(&map_w);
@@ -336,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int issued = 0;
     for (int i = blockIdx.x; i < total_units && !*gave_up; i += gridDim.x) {
       unit_at(p, s, i, &e, &u);
-      // The unit's scales into L2: the consumers read them a stage ahead.
+      // The unit's scales into L2: the consumers read them two to eight stages ahead.
       const long long scale_bytes = static_cast<long long>(p.K / G) * 2;
       for (int r = lane; r < kWarps * kBoxRows / u.kw; r += 32) {
         const int half = kWarps * kBoxRows / u.kw / 2;
@@ -356,13 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < (gated ? 2 * kWarps : kWarps)) {
           const int cw = gated ? lane >> 1 : lane, half = gated ? lane & 1 : 0;
           const int row = gated ? half * (p.N / 2) + u.n0 / 2 + cw / u.kw * 16 : u.n0 + cw / u.kw * kBoxRows;
-          tc::tma_load_3d(w + cw * kBoxBytes + half * (kBoxBytes / 2), &map_w, full, (it * u.kw + cw % u.kw) * (kChunk / 2),
+          tc::tma_load_3d(w + cw * kBoxBytes + half * (kBoxBytes / 2), &map_w, full, (cw % u.kw * iters + it) * (kChunk / 2),
                           row, u.e);
         }
         // A slab of 8 rows x kChunk as four boxes of 8 rows x 32 elements.
         if (lane < u.kw * u.nt * 4) {
           const int slab = lane >> 2, kb = lane & 3;
-          tc::tma_load_2d(x + lane * 512, &map_x, full, (it * u.kw + slab / u.nt) * kChunk + kb * 32,
+          tc::tma_load_2d(x + lane * 512, &map_x, full, (slab / u.nt * iters + it) * kChunk + kb * 32,
                           u.off + u.r0 + slab % u.nt * 8);
         }
         __syncwarp();
@@ -392,15 +402,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool fine;
       if (u.nt == 1) {
         float total[2][1][4];
-        fine = unit_sums<T, G, gated, 1>(p, u, ring, s, &stage, &phase, total);
+        fine = unit_sums<T, G, gated, 1>(p, u, ring, scale_buf, s, &stage, &phase, total);
         if (fine || u.kw > 1) unit_write<T, gated, 1>(p, u, red, total);
       } else if (u.nt == 2) {
         float total[2][2][4];
-        fine = unit_sums<T, G, gated, 2>(p, u, ring, s, &stage, &phase, total);
+        fine = unit_sums<T, G, gated, 2>(p, u, ring, scale_buf, s, &stage, &phase, total);
         if (fine || u.kw > 1) unit_write<T, gated, 2>(p, u, red, total);
       } else {
         float total[2][4][4];
-        fine = unit_sums<T, G, gated, 4>(p, u, ring, s, &stage, &phase, total);
+        fine = unit_sums<T, G, gated, 4>(p, u, ring, scale_buf, s, &stage, &phase, total);
         if (fine || u.kw > 1) unit_write<T, gated, 4>(p, u, red, total);
       }
       if (KW > 1) {
