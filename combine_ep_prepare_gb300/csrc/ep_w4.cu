@@ -4,97 +4,112 @@
 // row n (low nibble of a byte: even k).  out[r][n] = sum_k x[r][k] w[e][n][k]
 // for the rows of expert e, or silu(gate) * up of the two halves of n.
 //
-// Bound by the weights' bytes.  A persistent block per SM walks units of 256,
-// 128, 64 or 32 weight rows of one expert.  One warp keeps a ring of stages
-// filled by TMA, running ahead across units, so that about 100 KB of weights
-// per SM are in flight whatever the units' length; eight warps unpack and
-// multiply.  A warp owns 32 weight rows and a share of the reduction; where
-// there are few units, 2, 4 or 8 warps share 32 rows and split the reduction,
-// joined through shared memory in a fixed order.
+// Bound by the weights' bytes, and close behind by the logic unit, which
+// unpacks them.  A persistent block per SM walks units of 256 down to 32
+// weight rows of one expert: one warp keeps a ring of four stages of 32 KB
+// filled by TMA (and the receive rows' share with them), running ahead across
+// units; of eight others each owns 32 weight rows and a share of the reduction.  Where there are few units, 2 or
+// 4 warps share 32 rows and split the reduction, joined through shared
+// memory in a fixed order.  A stage is 256 rows of 128 bytes (256 weights):
+// the copies cost a block about two clocks a row, so 64-byte rows would not
+// keep up with memory, and copies of 16 or 32 rows for each warp cost 90
+// clocks each to issue.  (Such boxes, 20 to 32 a stage, took 83 us for one
+// token's up products of 8 experts, 7168 -> 2 x 2048; cp.async by the warps
+// themselves, 40% more instructions, 53 us.)
 //
 // The receive rows are the narrow side of mma.m16n8k16 (weights 16 x 16,
-// receive rows 16 x 8): 8, 16 or 32 rows share one pass over the weights.  A
-// nibble becomes 128 + q (bf16) or 1024 + q (fp16) by placing it in the
-// mantissa, one packed subtraction gives q - 8 exactly, and the integers' sum
-// over a group is exact up to the float32 accumulation of q x; the scale
-// multiplies that sum in float32, so no weight is ever rounded.
-#include <cuda.h>
-
+// receive rows 16 x 8): up to 16 rows share one pass over the weights.  A
+// nibble becomes an integer plus a constant by being placed in the mantissa
+// of a 16-bit number, one packed operation gives q - 8 exactly, and the
+// integers' sum over a group is exact up to the float32 accumulation of q x;
+// the scale multiplies that sum in float32, so no weight is ever rounded.
 #include "ep_experts.cuh"
 #include "ep_tc.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kWarps = 8;                    // consumers; one more warp loads
+constexpr int kWarps = 8;                     // consumers; one more warp loads
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kBoxRows = 32, kChunk = 128;   // a warp's weight rows and reduction elements per stage
-constexpr int kBoxBytes = kBoxRows * kChunk / 2;
-constexpr int kWBytes = kWarps * kBoxBytes;  // 16 KB
-constexpr int kXBytes = 16 * 1024;           // row slabs of up to 8 (8 rows x kChunk) each
-constexpr int kStageBytes = kWBytes + kXBytes;
-constexpr int kStages = 6;
+constexpr int kBoxRows = 32, kChunk = 256;    // a warp's weight rows and reduction elements per stage
+constexpr int kRowBytes = kChunk / 2;
+constexpr int kBoxBytes = kBoxRows * kRowBytes;
+constexpr int kWBytes = kWarps * kBoxBytes;
+constexpr int kSlabBytes = 8 * kChunk * 2;    // eight receive rows' share of a stage
+constexpr int kMaxSlabs = 4;                  // shares times blocks of eight rows
+constexpr int kStageBytes = kWBytes + kMaxSlabs * kSlabBytes;
+constexpr int kStages = 4;
+constexpr int kSteps = kChunk / 32;           // steps of 32 reduction elements
+constexpr int kUnitRows = kWarps * kBoxRows;
+constexpr int kMaxSplit = 4;
 
+// The eight nibbles of a word, as the pairs (0,4) (1,5) (2,6) (3,7) of q - 8:
+// nibbles i and i + 4 lie 16 bits apart, so one shift and one mask place both.
+// The logic unit, which takes an instruction every other clock, has most of
+// the kernel's work here.  (Shifts by the multipliers' upper halves instead
+// took 190 us for 173 on a decode batch's down products.)
 template <typename T>
 struct Nib;
 template <>
 struct Nib<__nv_bfloat16> {
-  static constexpr unsigned kMagic = 0x43004300u;   // 128
-  static constexpr unsigned kOffset = 0xc308c308u;  // -136
-  static __device__ __forceinline__ unsigned add(unsigned a, unsigned b) {
-    unsigned r;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+  // 128 + q, less 136
+  static __device__ __forceinline__ void unpack(unsigned w, unsigned (&out)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+      asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(v), "r"(0xc308c308u));
+    }
+  }
+  // c = a b
+  static __device__ __forceinline__ void mma0(float* c, const unsigned* a, unsigned b0, unsigned b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
   }
   static __device__ __forceinline__ void mma(float* c, const unsigned* a, unsigned b0, unsigned b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 };
 template <>
 struct Nib<__half> {
-  static constexpr unsigned kMagic = 0x64006400u;   // 1024
-  static constexpr unsigned kOffset = 0xe408e408u;  // -1032
-  static __device__ __forceinline__ unsigned add(unsigned a, unsigned b) {
-    unsigned r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+  // Even nibbles as 1024 + q, less 1032; odd ones where they are, 1024 + 16 q,
+  // over 16 less 72: exact, and without a shift.
+  static __device__ __forceinline__ void unpack(unsigned w, unsigned (&out)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const unsigned s = w >> (4 * i);
+      const unsigned even = (s & 0x000f000fu) | 0x64006400u, odd = (s & 0x00f000f0u) | 0x64006400u;
+      asm("add.rn.f16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(even), "r"(0xe408e408u));
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(out[i + 1]) : "r"(odd), "r"(0x2c002c00u), "r"(0xd480d480u));
+    }
+  }
+  // c = a b
+  static __device__ __forceinline__ void mma0(float* c, const unsigned* a, unsigned b0, unsigned b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
   }
   static __device__ __forceinline__ void mma(float* c, const unsigned* a, unsigned b0, unsigned b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 };
 
-// The eight nibbles of a word as the pairs (0,1) (2,3) (4,5) (6,7) of q - 8.
-template <typename T>
-__device__ __forceinline__ void unpack8(unsigned w, unsigned* out) {
-  const unsigned hi = w >> 4;
-#pragma unroll
-  for (unsigned i = 0; i < 4; ++i) {
-    const unsigned p = __byte_perm(w, hi, i | i << 4 | (4 + i) << 8 | (4 + i) << 12);
-    out[i] = Nib<T>::add((p & 0x000f000fu) | Nib<T>::kMagic, Nib<T>::kOffset);
-  }
-}
-
-// A unit: 256 / kw weight rows of an expert times a block of 8 nt rows.
+// A unit: kUnitRows / KW weight rows of an expert times a block of 8 nt rows.
 struct Unit {
-  int e, n0, r0, cnt, off, rows, nt, kw;
+  int e, n0, r0, cnt, off, nt, kw;
   bool last;  // the expert's last row block: zeroes the padding rows
 };
-
-__device__ __forceinline__ int row_tiles(int cnt) { return cnt <= 8 ? 1 : cnt <= 16 ? 2 : 4; }
 
 struct Blocks {
   int nt, kw, nblk, tblk;
   __device__ __forceinline__ Blocks(const W4Params& p, int cnt, int KW) {
-    nt = row_tiles(cnt);
-    kw = KW < 8 / nt ? KW : 8 / nt;
-    const int rows = kWarps * kBoxRows / kw;
+    nt = cnt <= 8 ? 1 : 2;
+    kw = KW < kMaxSlabs / nt ? KW : kMaxSlabs / nt;
+    const int rows = kUnitRows / kw;
     nblk = (p.N + rows - 1) / rows;  // gated: N / 2 features over rows / 2
     tblk = (cnt + 8 * nt - 1) / (8 * nt);
   }
@@ -102,13 +117,14 @@ struct Blocks {
 
 struct Shared {
   uint64_t full[kStages], empty[kStages];
-  int gave_up, ok, stop, kw;
+  int gave_up, ok, stop;
   int part[32];
-  int cum[EP_MAX_EXPERTS + 1];
+  int cum[EP_MAX_EXPERTS + 1];  // units of the experts before e
 };
-constexpr int kRedBytes = 16 * 1024;
-constexpr int kScaleBytes = kWarps * kBoxRows * 8 * 2;
-constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kRedBytes + kScaleBytes + 1024 + sizeof(Shared);
+constexpr int kScaleBytes = kWarps * kBoxRows * 16;              // 256 / 32 scales of every box row
+constexpr int kRedBytes = kWarps / kMaxSplit * (kMaxSplit - 1) * 32 * 8 * 4;  // sums of 8 rows of all but one share
+constexpr size_t kSmemBytes =
+    static_cast<size_t>(kStages) * kStageBytes + kScaleBytes + kRedBytes + 1024 + sizeof(Shared);
 
 // cum[e] = units of the experts before e when the reduction is split KW ways.
 __device__ __forceinline__ void scan_units(const W4Params& p, int KW, Shared& s) {
@@ -128,195 +144,256 @@ __device__ __forceinline__ void scan_units(const W4Params& p, int KW, Shared& s)
   __syncthreads();
 }
 
-__device__ __forceinline__ void unit_at(const W4Params& p, const Shared& s, int u, int* e, Unit* o) {
-  while (u >= s.cum[*e + 1]) ++*e;
-  o->e = *e;
-  o->cnt = p.counts[*e];
-  o->off = p.offsets[*e];
-  o->rows = p.offsets[*e + 1] - o->off;
-  const Blocks b(p, o->cnt, s.kw);
-  const int in = u - s.cum[*e], tb = in % b.tblk;
+// o->e: the expert to search from.
+__device__ __forceinline__ void unit_at(const W4Params& p, const Shared& s, int KW, int u, Unit* o) {
+  while (u >= s.cum[o->e + 1]) ++o->e;
+  o->cnt = p.counts[o->e];
+  o->off = p.offsets[o->e];
+  const Blocks b(p, o->cnt, KW);
+  const int in = u - s.cum[o->e], tb = in % b.tblk;
   o->nt = b.nt;
   o->kw = b.kw;
-  o->n0 = in / b.tblk * (kWarps * kBoxRows / b.kw);
+  o->n0 = in / b.tblk * (kUnitRows / b.kw);
   o->r0 = tb * 8 * b.nt;
   o->last = tb + 1 == b.tblk;
 }
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
-// One unit of a consumer warp; stage and phase follow the ring.  False when a
-// wait gave up.
-template <typename T, int G, bool gated, int NT>
-__device__ __forceinline__ bool unit_sums(const W4Params& p, const Unit& u, unsigned char* ring, T* scale_buf, Shared& s,
-                                          int* stage, uint32_t* phase, float (&total)[2][NT][4]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int sub = warp % u.kw, group = warp / u.kw;
-  constexpr int kGroups = kChunk / G;    // scales per weight row and stage
-  constexpr int kPeriod = 8 / kGroups;   // stages that eight scales of a row last
-  const int ngroups = p.K / G;
-  const int chunks = (p.K + kChunk - 1) / kChunk, iters = (chunks + u.kw - 1) / u.kw;
-  // Box rows of this lane's fragments: fragment f's rows g and g + 8 (gated:
-  // the gate row and the up row of one feature).
-  int box_row[2][2];
-#pragma unroll
-  for (int f = 0; f < 2; ++f)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) box_row[f][h] = gated ? h * 16 + f * 8 + g : f * 16 + h * 8 + g;
-  // Scales: lane l brings eight of box row l, a period ahead, and the warp
-  // shares them through shared memory.
-  int n;  // this lane's weight row, clamped into the expert
-  if (gated) {
-    const int F = p.N / 2, j = u.n0 / 2 + group * 16 + (lane & 15);
-    n = (j < F ? j : F - 1) + (lane >> 4) * F;
-  } else {
-    n = u.n0 + group * kBoxRows + lane;
-    n = n < p.N ? n : p.N - 1;
-  }
-  const T* scale_row = static_cast<const T*>(p.scales) + (static_cast<long long>(u.e) * p.N + n) * ngroups;
-  const bool wide = (ngroups & 7) == 0 && ((sub * iters * kGroups) & 7) == 0;
-  auto load_scales = [&](int period) {
-    const int g0 = sub * iters * kGroups + period * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (wide) {
-      if (g0 < ngroups) v = __ldg(reinterpret_cast<const uint4*>(scale_row + g0));
-    } else {
-      unsigned short h[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        h[q] = g0 + q < ngroups ? __ldg(reinterpret_cast<const unsigned short*>(scale_row) + g0 + q) : 0;
-      v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+// Shared memory from its first 1024-byte boundary.
+__device__ __forceinline__ unsigned char* block_smem() {
+  extern __shared__ unsigned char raw[];
+  return raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
+}
+
+// What a consumer warp keeps over the units.
+template <typename T, int G, bool gated>
+struct Consumer {
+  const W4Params& p;
+  Shared& s;
+  int chunks, warp, lane;
+  int stage;
+  uint32_t phase;
+
+  // One unit's sums.  False when a wait gave up.
+  template <int NT>
+  __device__ __forceinline__ bool sums(const Unit& u, float (&total)[2][NT][4]) {
+    const int g = lane >> 2, t = lane & 3, KW = u.kw, sub = warp % KW, group = warp / KW;
+    const int iters = (chunks + KW - 1) / KW;
+    constexpr int kGroups = kChunk / G;
+    int left = min(p.K - sub * iters * kChunk, iters * kChunk);  // elements of the warp's share
+    // Scales: lane l brings a stage's scales of box row l, a stage ahead, and
+    // the warp shares them through shared memory, eight words' space a row.
+    const T* scale;
+    int groups_left = p.K / G - sub * iters * kGroups;
+    {
+      int n;  // weight row of box row `lane`, clamped into the expert
+      if (gated) {
+        const int F = p.N / 2;
+        n = min(u.n0 / 2 + group * 16 + (lane & 15), F - 1) + (lane >> 4) * F;
+      } else {
+        n = min(u.n0 + group * kBoxRows + lane, p.N - 1);
+      }
+      scale = static_cast<const T*>(p.scales) + (static_cast<long long>(u.e) * p.N + n) * (p.K / G) + sub * iters * kGroups;
     }
-    return v;
-  };
-  T* scales = scale_buf + warp * (kBoxRows * 8);
-  uint4 next = load_scales(0);
-  float acc[2][NT][4];
+    const bool wide = p.K % kChunk == 0;  // rows of whole stages: a stage's scales lie on their own alignment
+    uint32_t next[kGroups / 2];
+    auto load_scales = [&]() {
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+      for (int i = 0; i < kGroups / 2; ++i) next[i] = 0;
+      if (wide && groups_left > 0) {
+        if constexpr (kGroups == 2) {
+          next[0] = __ldg(reinterpret_cast<const uint32_t*>(scale));
+        } else if constexpr (kGroups == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(scale));
+          next[0] = v.x;
+          next[1] = v.y;
+        } else {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(scale));
+          next[0] = v.x;
+          next[1] = v.y;
+          next[2] = v.z;
+          next[3] = v.w;
+        }
+      } else {
+        const unsigned short* h = reinterpret_cast<const unsigned short*>(scale);
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+        for (int q = 0; q < kGroups; ++q)
+          if (q < groups_left) next[q / 2] |= static_cast<uint32_t>(__ldg(h + q)) << (16 * (q & 1));
+      }
+      scale += kGroups;
+      groups_left -= kGroups;
+    };
+    unsigned char* smem = block_smem();
+    unsigned char* scales = smem + kStages * kStageBytes + warp * (kBoxRows * 16);
+    load_scales();
+    // The sums of the present group and of the one before, whose scales are
+    // applied only after the present group's mma have been issued: to wait
+    // for a group's last mma each time took a third of the kernel's time.
+    float acc[2][2][NT][4], sc[2][2][2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) total[f][i][j] = acc[f][i][j] = 0.0f;
-  bool fine = true;
-  for (int it = 0; it < iters; ++it) {
-    if (it % kPeriod == 0) {
-      __syncwarp();
-      *reinterpret_cast<uint4*>(scales + lane * 8) = next;
-      __syncwarp();
-      if (it + kPeriod < iters) next = load_scales(it / kPeriod + 1);
-    }
-    const T* sc = scales + it % kPeriod * kGroups;
-    fine = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_addr(&s.full[*stage]), *phase, &s.gave_up));
-    if (!fine) break;
-    const unsigned char* st = ring + static_cast<size_t>(*stage) * kStageBytes;
-    const unsigned char* wbox = st + warp * kBoxBytes;
-    const unsigned char* xbox = st + kWBytes + sub * NT * (8 * kChunk * 2);
-#pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
-      uint4 x[NT];
+    for (int f = 0; f < 2; ++f) {
+      sc[1][f][0] = sc[1][f][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        x[i] = *reinterpret_cast<const uint4*>(xbox + i * (8 * kChunk * 2) + kb * 512 + g * 64 + ((t ^ ((g >> 1) & 3)) << 4));
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        unsigned a[2][4];
+        for (int j = 0; j < 4; ++j) total[f][i][j] = acc[1][f][i][j] = 0.0f;
+    }
+    auto apply = [&](int q) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = box_row[f][h];
-          unpack8<T>(*reinterpret_cast<const unsigned*>(wbox + r * 64 + ((kb ^ ((r >> 1) & 3)) << 4) + t * 4), a[h]);
-        }
-        const unsigned lo[4] = {a[0][0], a[1][0], a[0][1], a[1][1]}, hi[4] = {a[0][2], a[1][2], a[0][3], a[1][3]};
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) total[f][i][j] = fmaf(sc[q][f][j >> 1], acc[q][f][i][j], total[f][i][j]);
+    };
+    // Fragment f's rows g and g + 8 (gated: the gate row and the up row of one
+    // feature) in the stage: this warp's rows of its share's box; the gate
+    // rows of a box come before its up rows.
+    const int sub_bytes = kWBytes / KW;
+    const uint32_t word_at = sub * sub_bytes + group * (gated ? 16 : kBoxRows) * kRowBytes + g * kRowBytes + t * 4;
+    const uint32_t h_bytes = gated ? sub_bytes / 2 : 8 * kRowBytes;
+    constexpr int kFBytes = (gated ? 8 : 16) * kRowBytes;
+    constexpr int kScaleF = (gated ? 8 : 16) * 16, kScaleH = (gated ? 16 : 8) * 16;  // box rows in the scales' order
+    for (int it = 0; it < iters; ++it) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kGroups / 2; ++i) reinterpret_cast<uint32_t*>(scales + lane * 16)[i] = next[i];
+      if (it + 1 < iters) load_scales();
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(tc::smem_addr(&s.full[stage]), phase, &s.gave_up))) return false;
+      const unsigned char* words = smem + stage * kStageBytes + word_at;
+      const unsigned char* slab = smem + stage * kStageBytes + kWBytes + sub * NT * kSlabBytes + g * (kChunk * 2);
+#pragma unroll
+      for (int kb = 0; kb < kSteps; ++kb) {
+        // Rows' elements in the order of the nibble pairs: lane (g, t) has
+        // eight from t * 8 of this run of 32 of row g of a slab.
+        unsigned b[NT][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          Nib<T>::mma(acc[f][i], lo, x[i].x, x[i].y);
-          Nib<T>::mma(acc[f][i], hi, x[i].z, x[i].w);
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              slab + i * kSlabBytes + kb * 64 + ((t ^ (kb >> 1)) << 4));
+          b[i][0] = __byte_perm(v.x, v.z, 0x5410);
+          b[i][1] = __byte_perm(v.x, v.z, 0x7632);
+          b[i][2] = __byte_perm(v.y, v.w, 0x5410);
+          b[i][3] = __byte_perm(v.y, v.w, 0x7632);
         }
-      }
-      if ((kb + 1) * 32 % G == 0) {
-        const int q = kb * 32 / G;
+        const unsigned char* w0 = words + ((kb ^ g) << 4);
+        const int q = kb * 32 / G & 1;
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const float s0 = to_f32(sc[box_row[f][0] * 8 + q]), s1 = to_f32(sc[box_row[f][1] * 8 + q]);
+          unsigned a[2][4];
+          Nib<T>::unpack(*reinterpret_cast<const unsigned*>(w0 + f * kFBytes), a[0]);
+          Nib<T>::unpack(*reinterpret_cast<const unsigned*>(w0 + h_bytes + f * kFBytes), a[1]);
+          const unsigned lo[4] = {a[0][0], a[1][0], a[0][1], a[1][1]}, hi[4] = {a[0][2], a[1][2], a[0][3], a[1][3]};
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int i = 0; i < NT; ++i) {
+            if (kb * 32 % G == 0) Nib<T>::mma0(acc[q][f][i], lo, b[i][0], b[i][1]);
+            else Nib<T>::mma(acc[q][f][i], lo, b[i][0], b[i][1]);
+            Nib<T>::mma(acc[q][f][i], hi, b[i][2], b[i][3]);
+          }
+        }
+        if ((kb + 1) * 32 % G == 0) {
+          const T* at_g = reinterpret_cast<const T*>(scales + g * 16) + kb * 32 / G;
+          apply(q ^ 1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              total[f][i][j] = fmaf(j < 2 ? s0 : s1, acc[f][i][j], total[f][i][j]);
-              acc[f][i][j] = 0.0f;
-            }
+          for (int f = 0; f < 2; ++f) {
+            sc[q][f][0] = to_f32(at_g[f * kScaleF / 2]);
+            sc[q][f][1] = to_f32(at_g[(f * kScaleF + kScaleH) / 2]);
+          }
+          if (kb * 32 >= left) {
+            // Past the share's end: another share's rows, or none.
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[q][f][i][j] = 0.0f;
+          }
         }
       }
+      left -= kChunk;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_addr(&s.empty[stage]));
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(tc::smem_addr(&s.empty[*stage]));
-    if (++*stage == kStages) {
-      *stage = 0;
-      *phase ^= 1;
-    }
+    apply(1);  // a stage has an even number of groups
+    return true;
   }
-  return fine;
-}
 
-// Joins the reduction's shares (in ascending order) and writes the unit's output.
-template <typename T, bool gated, int NT>
-__device__ __forceinline__ void unit_write(const W4Params& p, const Unit& u, float* red, float (&total)[2][NT][4]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int sub = warp % u.kw, group = warp / u.kw;
-  if (u.kw > 1) {
-    if (sub > 0) {
-      float* d = red + (group * (u.kw - 1) + sub - 1) * (32 * 8 * NT);
+  // Joins the reduction's shares (in ascending order, eight rows at a time)
+  // and writes the unit's output.
+  template <int NT>
+  __device__ __forceinline__ void write(const Unit& u, float (&total)[2][NT][4]) {
+    const int g = lane >> 2, t = lane & 3, KW = u.kw, sub = warp % KW, group = warp / KW;
+    if (KW > 1) {
+      float* red = reinterpret_cast<float*>(block_smem() + kStages * kStageBytes + kScaleBytes) + group * (KW - 1) * 256;
 #pragma unroll
-      for (int j = 0; j < 8 * NT; ++j) d[j * 32 + lane] = total[j / (4 * NT)][j / 4 % NT][j % 4];
-    }
-    consumers_sync();
-    if (sub > 0) return;
-    for (int k = 0; k + 1 < u.kw; ++k) {
-      const float* d = red + (group * (u.kw - 1) + k) * (32 * 8 * NT);
+      for (int i = 0; i < NT; ++i) {
+        if (sub > 0) {
 #pragma unroll
-      for (int j = 0; j < 8 * NT; ++j) total[j / (4 * NT)][j / 4 % NT][j % 4] += d[j * 32 + lane];
-    }
-  }
-  const int cols = gated ? p.N / 2 : p.N;
-  T* out = static_cast<T*>(p.out) + static_cast<long long>(u.off) * cols;
-  const int c0 = gated ? u.n0 / 2 + group * 16 : u.n0 + group * kBoxRows;
-#pragma unroll
-  for (int f = 0; f < 2; ++f)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = u.r0 + i * 8 + 2 * t + j;
-        if (r >= u.cnt) continue;
-        if (gated) {
-          const int c = c0 + f * 8 + g;
-          if (c < cols) out[static_cast<long long>(r) * cols + c] = from_f32<T>(swiglu(total[f][i][j], total[f][i][2 + j]));
-        } else {
-          const int c = c0 + f * 16 + g;
-          if (c < cols) out[static_cast<long long>(r) * cols + c] = from_f32<T>(total[f][i][j]);
-          if (c + 8 < cols) out[static_cast<long long>(r) * cols + c + 8] = from_f32<T>(total[f][i][2 + j]);
+          for (int j = 0; j < 8; ++j) red[(sub - 1) * 256 + j * 32 + lane] = total[j / 4][i][j % 4];
         }
+        consumers_sync();
+        if (sub == 0)
+          for (int k = 0; k + 1 < KW; ++k) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) total[j / 4][i][j % 4] += red[k * 256 + j * 32 + lane];
+          }
+        consumers_sync();
       }
-  if (u.last) {
-    const int c = c0 + lane;
-    if (c < cols && lane < (gated ? 16 : kBoxRows))
-      for (int r = u.cnt; r < u.rows; ++r) out[static_cast<long long>(r) * cols + c] = from_f32<T>(0.0f);
+      if (sub > 0) return;
+    }
+    const int cols = gated ? p.N / 2 : p.N;
+    T* out = static_cast<T*>(p.out) + static_cast<long long>(u.off) * cols;
+    const int c0 = gated ? u.n0 / 2 + group * 16 : u.n0 + group * kBoxRows;
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = u.r0 + i * 8 + 2 * t + j;
+          if (r >= u.cnt) continue;
+          if (gated) {
+            const int c = c0 + f * 8 + g;
+            if (c < cols) out[static_cast<long long>(r) * cols + c] = from_f32<T>(swiglu(total[f][i][j], total[f][i][2 + j]));
+          } else {
+            const int c = c0 + f * 16 + g;
+            if (c < cols) out[static_cast<long long>(r) * cols + c] = from_f32<T>(total[f][i][j]);
+            if (c + 8 < cols) out[static_cast<long long>(r) * cols + c + 8] = from_f32<T>(total[f][i][2 + j]);
+          }
+        }
+    if (u.last) {
+      const int c = c0 + lane;
+      if (c < cols && lane < (gated ? 16 : kBoxRows))
+        for (int r = u.cnt, rows = p.offsets[u.e + 1] - u.off; r < rows; ++r)
+          out[static_cast<long long>(r) * cols + c] = from_f32<T>(0.0f);
+    }
   }
-}
+
+  template <int NT>
+  __device__ __forceinline__ bool unit(const Unit& u) {
+    float total[2][NT][4];
+    const bool fine = sums<NT>(u, total);
+    if (fine || u.kw > 1) write<NT>(u, total);  // a split unit's barriers want every warp
+    return fine;
+  }
+};
+
+struct Maps {
+  CUtensorMap box[3];  // weights in boxes of kUnitRows, / 2 or / 4 rows of kRowBytes (gated: half of each)
+  CUtensorMap rows;    // receive rows, boxes of 8 rows x kChunk
+};
 
 template <typename T, int G, bool gated>
-__global__ void __launch_bounds__(kThreads, 1)
-    ep_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const W4Params p) {
-  extern __shared__ unsigned char raw[];
-  // Aligned by an offset, so that accesses stay known as shared-memory ones.
-  unsigned char* ring = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
-  float* red = reinterpret_cast<float*>(ring + static_cast<size_t>(kStages) * kStageBytes);
-  T* scale_buf = reinterpret_cast<T*>(ring + static_cast<size_t>(kStages) * kStageBytes + kRedBytes);
-  Shared& s = *reinterpret_cast<Shared*>(ring + static_cast<size_t>(kStages) * kStageBytes + kRedBytes + kScaleBytes);
+__global__ void __launch_bounds__(kThreads, 1) ep_w4_kernel(const __grid_constant__ Maps maps, const W4Params p) {
+  unsigned char* smem = block_smem();
+  Shared& s = *reinterpret_cast<Shared*>(smem + kStages * kStageBytes + kScaleBytes + kRedBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    tc::tma_prefetch_desc(&map_w);
-    tc::tma_prefetch_desc(&map_x);
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(tc::smem_addr(&s.full[i]), 1);
       tc::mbar_init(tc::smem_addr(&s.empty[i]), kWarps);
@@ -333,88 +410,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int chunks = (p.K + kChunk - 1) / kChunk;
   scan_units(p, 1, s);
   int KW = 1;
-  while (KW < 8 && 2 * KW <= chunks && s.cum[p.E] * KW < 2 * static_cast<int>(gridDim.x)) KW *= 2;
-  if (threadIdx.x == 0) s.kw = KW;
+  while (KW < kMaxSplit && 2 * KW <= chunks && s.cum[p.E] * KW < 2 * static_cast<int>(gridDim.x)) KW *= 2;
   __syncthreads();
   if (KW > 1) scan_units(p, KW, s);
   const int total_units = s.cum[p.E];
-  int e = 0, stage = 0;
-  uint32_t phase = 0;
   Unit u;
+  u.e = 0;
   volatile int* gave_up = &s.gave_up;
   if (warp == kWarps) {
-    int issued = 0;
-    for (int i = blockIdx.x; i < total_units && !*gave_up; i += gridDim.x) {
-      unit_at(p, s, i, &e, &u);
-      // The unit's scales into L2: the consumers read them two to eight stages ahead.
-      const long long scale_bytes = static_cast<long long>(p.K / G) * 2;
-      for (int r = lane; r < kWarps * kBoxRows / u.kw; r += 32) {
-        const int half = kWarps * kBoxRows / u.kw / 2;
-        const int n = gated ? u.n0 / 2 + (r < half ? r : p.N / 2 + r - half) : u.n0 + r;
-        if (n < p.N) {
-          const char* at = static_cast<const char*>(p.scales) + (static_cast<long long>(u.e) * p.N + n) * scale_bytes;
-          for (long long b = 0; b < scale_bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int i = blockIdx.x; i < total_units && !*gave_up; i += gridDim.x) {
+        unit_at(p, s, KW, i, &u);
+        // A share's weight rows of a stage are one copy; gated two, gate rows first.
+        const int boxes = (gated ? 2 : 1) * u.kw, rows = kUnitRows / boxes, iters = (chunks + u.kw - 1) / u.kw;
+        const CUtensorMap* map = &maps.box[31 - __clz(u.kw)];
+        for (int it = 0; it < iters; ++it) {
+          if (!tc::mbar_wait(tc::smem_addr(&s.empty[stage]), phase ^ 1, gave_up)) break;
+          const uint32_t full = tc::smem_addr(&s.full[stage]), dst = tc::smem_addr(smem + stage * kStageBytes);
+          tc::mbar_expect(full, kWBytes + u.kw * u.nt * kSlabBytes);
+          for (int b = 0; b < boxes; ++b) {
+            const int share = gated ? b / 2 : b;
+            const int row = gated ? (b & 1) * (p.N / 2) + u.n0 / 2 : u.n0;
+            tc::tma_load_3d(dst + b * rows * kRowBytes, map, full, (share * iters + it) * kRowBytes, row, u.e);
+          }
+          for (int b = 0; b < u.kw * u.nt; ++b)
+            tc::tma_load_3d(dst + kWBytes + b * kSlabBytes, &maps.rows, full, 0, (b / u.nt * iters + it) * kSteps,
+                            u.off + u.r0 + b % u.nt * 8);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
-      const int iters = (chunks + u.kw - 1) / u.kw;
-      for (int it = 0; it < iters; ++it) {
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(tc::smem_addr(&s.empty[stage]), phase ^ 1, gave_up))) break;
-        const uint32_t full = tc::smem_addr(&s.full[stage]);
-        const uint32_t w = tc::smem_addr(ring + static_cast<size_t>(stage) * kStageBytes), x = w + kWBytes;
-        if (lane == 0) tc::mbar_expect(full, kWBytes + u.kw * u.nt * (8 * kChunk * 2));
-        __syncwarp();
-        if (lane < (gated ? 2 * kWarps : kWarps)) {
-          const int cw = gated ? lane >> 1 : lane, half = gated ? lane & 1 : 0;
-          const int row = gated ? half * (p.N / 2) + u.n0 / 2 + cw / u.kw * 16 : u.n0 + cw / u.kw * kBoxRows;
-          tc::tma_load_3d(w + cw * kBoxBytes + half * (kBoxBytes / 2), &map_w, full, (cw % u.kw * iters + it) * (kChunk / 2),
-                          row, u.e);
+      if (*gave_up) {
+        // The copies in flight land before the block's shared memory goes; a
+        // copy takes microseconds.
+        const unsigned long long start = tc::now_ns();
+        while (tc::now_ns() - start < tc::kWaitNs / 100) {
         }
-        // A slab of 8 rows x kChunk as four boxes of 8 rows x 32 elements.
-        if (lane < u.kw * u.nt * 4) {
-          const int slab = lane >> 2, kb = lane & 3;
-          tc::tma_load_2d(x + lane * 512, &map_x, full, (slab / u.nt * iters + it) * kChunk + kb * 32,
-                          u.off + u.r0 + slab % u.nt * 8);
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
+        atomicOr(&p.hdr[kHdrStatus], static_cast<int>(EP_ST_TIMEOUT));
       }
-    }
-    if (*gave_up) {
-      // The copies in flight land before the block's shared memory goes.
-      const unsigned long long start = tc::now_ns();
-      for (int j = issued < kStages ? issued : kStages; j > 0; --j) {
-        if (--stage < 0) {
-          stage = kStages - 1;
-          phase ^= 1;
-        }
-        while (!tc::mbar_try(tc::smem_addr(&s.full[stage]), phase) && tc::now_ns() - start < tc::kWaitNs) {
-        }
-      }
-      if (lane == 0) atomicOr(&p.hdr[kHdrStatus], static_cast<int>(EP_ST_TIMEOUT));
     }
   } else {
+    Consumer<T, G, gated> c{p, s, chunks, warp, lane, 0, 0};
     for (int i = blockIdx.x; i < total_units; i += gridDim.x) {
-      unit_at(p, s, i, &e, &u);
-      bool fine;
-      if (u.nt == 1) {
-        float total[2][1][4];
-        fine = unit_sums<T, G, gated, 1>(p, u, ring, scale_buf, s, &stage, &phase, total);
-        if (fine || u.kw > 1) unit_write<T, gated, 1>(p, u, red, total);
-      } else if (u.nt == 2) {
-        float total[2][2][4];
-        fine = unit_sums<T, G, gated, 2>(p, u, ring, scale_buf, s, &stage, &phase, total);
-        if (fine || u.kw > 1) unit_write<T, gated, 2>(p, u, red, total);
-      } else {
-        float total[2][4][4];
-        fine = unit_sums<T, G, gated, 4>(p, u, ring, scale_buf, s, &stage, &phase, total);
-        if (fine || u.kw > 1) unit_write<T, gated, 4>(p, u, red, total);
-      }
+      unit_at(p, s, KW, i, &u);
+      const bool fine = u.nt == 1 ? c.template unit<1>(u) : c.template unit<2>(u);
       if (KW > 1) {
-        // All warps leave together, or the next unit's barrier would wait for one that left.
+        // All warps leave together, or the next unit's barriers would wait for one that left.
         if (threadIdx.x == 0) s.stop = *gave_up;
         consumers_sync();
         if (s.stop) break;
@@ -426,22 +471,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename T, int G, bool gated>
-cudaError_t launch_one(const W4Params& p, const CUtensorMap& w, const CUtensorMap& x, int num_sms, cudaStream_t s) {
+cudaError_t launch_one(const W4Params& p, const Maps& maps, int num_sms, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(ep_w4_kernel<T, G, gated>),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
   if (e != cudaSuccess) return e;
-  return launch_pdl(ep_w4_kernel<T, G, gated>, dim3(num_sms), dim3(kThreads), kSmemBytes, s, 0, w, x, p);
+  return launch_pdl(ep_w4_kernel<T, G, gated>, dim3(num_sms), dim3(kThreads), kSmemBytes, s, 0, maps, p);
 }
 
 template <typename T>
-cudaError_t launch_typed(const W4Params& p, const CUtensorMap& w, const CUtensorMap& x, int num_sms, cudaStream_t s) {
+cudaError_t launch_typed(const W4Params& p, const Maps& maps, int num_sms, cudaStream_t s) {
   if (p.swiglu)
-    return p.group == 32   ? launch_one<T, 32, true>(p, w, x, num_sms, s)
-           : p.group == 64 ? launch_one<T, 64, true>(p, w, x, num_sms, s)
-                           : launch_one<T, 128, true>(p, w, x, num_sms, s);
-  return p.group == 32   ? launch_one<T, 32, false>(p, w, x, num_sms, s)
-         : p.group == 64 ? launch_one<T, 64, false>(p, w, x, num_sms, s)
-                         : launch_one<T, 128, false>(p, w, x, num_sms, s);
+    return p.group == 32   ? launch_one<T, 32, true>(p, maps, num_sms, s)
+           : p.group == 64 ? launch_one<T, 64, true>(p, maps, num_sms, s)
+                           : launch_one<T, 128, true>(p, maps, num_sms, s);
+  return p.group == 32   ? launch_one<T, 32, false>(p, maps, num_sms, s)
+         : p.group == 64 ? launch_one<T, 64, false>(p, maps, num_sms, s)
+                         : launch_one<T, 128, false>(p, maps, num_sms, s);
 }
 
 }  // namespace
@@ -449,24 +494,28 @@ cudaError_t launch_typed(const W4Params& p, const CUtensorMap& w, const CUtensor
 cudaError_t launch_w4(const W4Params& p, int num_sms, cudaStream_t s) {
   const tc::EncodeFn f = tc::tensor_map_encoder();
   if (f == nullptr) return cudaErrorNotSupported;
-  CUtensorMap w, x;
+  // Weights as bytes [E][N][K/2].
+  Maps maps;
   const cuuint32_t one[3] = {1, 1, 1};
-  // weights as bytes [E][N][K/2]
-  const cuuint64_t wsize[3] = {static_cast<cuuint64_t>(p.K / 2), static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.E)};
-  const cuuint64_t wstride[2] = {wsize[0], wsize[0] * wsize[1]};
-  const cuuint32_t wbox[3] = {kChunk / 2, static_cast<cuuint32_t>(p.swiglu ? kBoxRows / 2 : kBoxRows), 1};
-  const cuuint64_t xsize[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.R)};
-  const cuuint64_t xstride[1] = {static_cast<cuuint64_t>(p.K) * 2};
-  const cuuint32_t xbox[2] = {32, 8};
-  if (f(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.wq), wsize, wstride, wbox, one,
-        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-      f(&x, p.dtype == EP_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+  const cuuint64_t size[3] = {static_cast<cuuint64_t>(p.K / 2), static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.E)};
+  const cuuint64_t stride[2] = {size[0], size[0] * size[1]};
+  for (int i = 0; i < 3; ++i) {
+    const cuuint32_t box[3] = {kRowBytes, static_cast<cuuint32_t>((p.swiglu ? kUnitRows / 2 : kUnitRows) >> i), 1};
+    if (f(&maps.box[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.wq), size, stride, box, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  // Receive rows as [R][K/32][32]: a row's runs of 32 side by side, whatever
+  // part of the last 256 there is.
+  const cuuint64_t xsize[3] = {32, static_cast<cuuint64_t>(p.K / 32), static_cast<cuuint64_t>(p.R)};
+  const cuuint64_t xstride[2] = {64, static_cast<cuuint64_t>(p.K) * 2};
+  const cuuint32_t xbox[3] = {32, kSteps, 8};
+  if (f(&maps.rows, p.dtype == EP_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
         const_cast<void*>(p.x), xsize, xstride, xbox, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  return p.dtype == EP_DTYPE_FP16 ? launch_typed<__half>(p, w, x, num_sms, s)
-                                  : launch_typed<__nv_bfloat16>(p, w, x, num_sms, s);
+  return p.dtype == EP_DTYPE_FP16 ? launch_typed<__half>(p, maps, num_sms, s) : launch_typed<__nv_bfloat16>(p, maps, num_sms, s);
 }
 
 }  // namespace ep
