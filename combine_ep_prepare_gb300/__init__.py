@@ -35,5 +35,7 @@ _BINDING_NAMES = {
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import _libep
-        return getattr(_libep, name)
+        value = getattr(_libep, name)
+        globals()[name] = value  # later uses find it without this call
+        return value
     raise AttributeError(name)

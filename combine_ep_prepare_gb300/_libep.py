@@ -146,8 +146,16 @@ def _check(code: int):
         raise EpError(code, _lib.ep_last_error().decode())
 
 
+# The current stream's handle without a Stream object: building one costs more
+# than a small kernel takes.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -161,7 +169,7 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name="tensor") -> Optional[int]:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     return t.data_ptr() or None
 
@@ -191,9 +199,12 @@ def ep_launch_count() -> int:
     return int(_lib.ep_launch_count())
 
 
+_DTYPE_NAMES = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
+
+
 def _dtype_code(dtype) -> int:
     if not isinstance(dtype, str):
-        dtype = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}.get(dtype, str(dtype))
+        dtype = _DTYPE_NAMES.get(dtype, str(dtype))
     if dtype not in DTYPE_CODES:
         raise TypeError("payload dtype must be bf16, fp16 or fp32, got %s" % dtype)
     return DTYPE_CODES[dtype]
@@ -616,13 +627,22 @@ def pack_w4(w: torch.Tensor, group: int):
 # Router
 # ----------------------------------------------------------------------------
 
+_router_configs = {}  # arguments -> RouterConfig
+
+
 def _router_config(logits, top_k, num_groups, topk_groups, score, normalize, scale) -> RouterConfig:
     if logits.dim() != 2:
         raise ValueError("logits must be [tokens, experts], got %s" % (tuple(logits.shape),))
-    if score not in SCORE_CODES:
-        raise ValueError("score must be softmax or sigmoid, got %s" % score)
-    return RouterConfig(logits.shape[1], top_k, num_groups, topk_groups, SCORE_CODES[score],
-                        1 if normalize else 0, _dtype_code(logits.dtype), scale)
+    key = (logits.shape[1], top_k, num_groups, topk_groups, score, bool(normalize), logits.dtype, scale)
+    cfg = _router_configs.get(key)
+    if cfg is None:
+        if score not in SCORE_CODES:
+            raise ValueError("score must be softmax or sigmoid, got %s" % score)
+        cfg = RouterConfig(logits.shape[1], top_k, num_groups, topk_groups, SCORE_CODES[score],
+                           1 if normalize else 0, _dtype_code(logits.dtype), scale)
+        if len(_router_configs) < 1024:
+            _router_configs[key] = cfg
+    return cfg
 
 
 def _routes(t: torch.Tensor, T: int, K: int, name: str):

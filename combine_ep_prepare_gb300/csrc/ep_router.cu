@@ -7,17 +7,20 @@
 // logit or value that is -inf or NaN is never chosen; where fewer than K
 // are left, the remaining ids are -1 and their weights 0.
 //
-// One warp per token: lane l holds the values of experts l, l + 32, ... as
-// order-preserving unsigned keys (0 = cannot be chosen), so that a round of
-// the selection is one redux.sync maximum over the lanes' best keys and one
-// redux.sync minimum over the indices that hold it.
+// One warp per token: lane l holds the values of J experts from l J on as
+// order-preserving unsigned keys (0 = cannot be chosen).  A round of the
+// selection is one redux.sync maximum over the lanes' best keys; the lowest
+// lane that holds it has the lowest index, since lanes hold runs of experts.
+// The instructions of the rounds and of the exact sigmoids bound the kernel:
+// 16,384 tokens x 256 experts, 8 groups, 8 choices take ROUTER_US us where
+// the bytes alone would take 2.7.
 #include "ep_experts.cuh"
 
 namespace ep {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;  // one for each of an SM's schedulers
 
 template <typename T>
 __device__ __forceinline__ float logit(const void* p, long long i) { return to_f32(static_cast<const T*>(p)[i]); }
@@ -33,7 +36,8 @@ __device__ __forceinline__ float value_of(unsigned key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-__device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + expf(-z)); }
+// 1 / (1 + exp(-z)), the reciprocal rounded correctly, as a division would be.
+__device__ __forceinline__ float sigmoidf(float z) { return __frcp_rn(1.0f + expf(-z)); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -44,6 +48,39 @@ __device__ __forceinline__ float warp_sum(float v) {
 // exp(z - m), 0 where the logit cannot be chosen.
 __device__ __forceinline__ float exp_or_0(float z, float m) { return z > -INFINITY ? expf(z - m) : 0.0f; }
 
+// This lane's J logits from expert lane J on; -inf past the last.
+template <typename T, int J>
+__device__ __forceinline__ void load_run(const RouterParams& p, long long row, int lane, float (&z)[J]) {
+  constexpr int kVec = 16 / sizeof(T) < J ? 16 / sizeof(T) : J;  // elements per load
+  const T* at = static_cast<const T*>(p.logits) + row + lane * J;
+  if (kVec > 1 && p.E % kVec == 0 && reinterpret_cast<uintptr_t>(p.logits) % (kVec * sizeof(T)) == 0) {
+#pragma unroll
+    for (int j = 0; j < J; j += kVec) {
+      alignas(16) T v[kVec];
+      if (lane * J + j < p.E) {
+        if constexpr (kVec * sizeof(T) == 16) *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(at + j));
+        else if constexpr (kVec * sizeof(T) == 8) *reinterpret_cast<uint2*>(v) = __ldg(reinterpret_cast<const uint2*>(at + j));
+        else if constexpr (kVec * sizeof(T) == 4) *reinterpret_cast<uint32_t*>(v) = __ldg(reinterpret_cast<const uint32_t*>(at + j));
+        else v[0] = at[j];
+      }
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) z[j + i] = lane * J + j < p.E ? to_f32(v[i]) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j) z[j] = lane * J + j < p.E ? to_f32(at[j]) : -INFINITY;
+  }
+}
+
+// A group's rank from its two largest keys (0: none).  Half the sum of the
+// two: the same order, and two logits at the type's lowest value do not
+// overflow to -inf.
+__device__ __forceinline__ unsigned group_key(unsigned best, unsigned second) {
+  if (best == 0) return 0;
+  const float f = value_of(best);
+  return key_of(0.5f * f + 0.5f * (second != 0 ? value_of(second) : f));
+}
+
 template <typename T, int J>
 __global__ void __launch_bounds__(kWarps * 32) ep_router_kernel(const RouterParams p) {
   pdl_wait();
@@ -52,93 +89,112 @@ __global__ void __launch_bounds__(kWarps * 32) ep_router_kernel(const RouterPara
   if (t >= p.T) return;
   const long long row = static_cast<long long>(t) * p.E;
   unsigned key[J];
-  float z[J];
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = lane + 32 * j;
-    z[j] = e < p.E ? logit<T>(p.logits, row + e) : -INFINITY;
-  }
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = lane + 32 * j;
-    float v = z[j];
-    if (p.sigmoid) {
-      v = sigmoidf(z[j]);
-      if (p.bias != nullptr && e < p.E) v += p.bias[e];
-    }
-    key[j] = z[j] > -INFINITY ? key_of(v) : 0;
-  }
   // Softmax over all experts: the largest logit and the sum of exponentials.
   float zmax = 0.0f, zsum = 1.0f;
-  if (!p.sigmoid && !p.normalize) {
-    unsigned m = 0;
+  {
+    float z[J];
+    load_run<T, J>(p, row, lane, z);
 #pragma unroll
-    for (int j = 0; j < J; ++j) m = max(m, key[j]);
-    m = __reduce_max_sync(kAll, m);
-    zmax = m ? value_of(m) : 0.0f;
-    float s = 0.0f;
+    for (int j = 0; j < J; ++j) {
+      float v = z[j];
+      if (p.sigmoid) {
+        v = sigmoidf(z[j]);
+        const int e = lane * J + j;
+        if (p.bias != nullptr && e < p.E) v += __ldg(p.bias + e);
+      }
+      key[j] = z[j] > -INFINITY ? key_of(v) : 0;
+    }
+    if (!p.sigmoid && !p.normalize) {
+      unsigned m = 0;
 #pragma unroll
-    for (int j = 0; j < J; ++j) s += exp_or_0(z[j], zmax);
-    zsum = warp_sum(s);
+      for (int j = 0; j < J; ++j) m = max(m, key[j]);
+      m = __reduce_max_sync(kAll, m);
+      zmax = m ? value_of(m) : 0.0f;
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) s += exp_or_0(z[j], zmax);
+      zsum = warp_sum(s);
+    }
   }
   if (p.groups > 1) {
     const int per = p.E / p.groups;
-    unsigned gkey = 0;  // lane g: group g's rank
-    for (int g = 0; g < p.groups; ++g) {
-      unsigned a = 0, b = 0;  // this lane's two best of group g
+    const int span = per / J;  // lanes of a group, where groups are runs of whole lanes
+    unsigned gkey = 0;         // one lane of each group: its rank
+    int g_of = 0;              // the group of that lane
+    if (per % J == 0 && (span & (span - 1)) == 0) {
+      unsigned a = 0, b = 0;  // the two best
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const int e = lane + 32 * j;
-        if (e >= g * per && e < (g + 1) * per) {
-          const unsigned k = key[j];
-          b = max(b, min(a, k));
-          a = max(a, k);
+        b = max(b, min(a, key[j]));
+        a = max(a, key[j]);
+      }
+      for (int d = 1; d < span; d <<= 1) {
+        const unsigned oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
+        b = max(min(a, oa), max(b, ob));
+        a = max(a, oa);
+      }
+      g_of = lane / span;
+      if (lane % span == 0) gkey = group_key(a, b);
+    } else {
+      for (int g = 0; g < p.groups; ++g) {
+        unsigned a = 0, b = 0;  // this lane's two best of group g
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int e = lane * J + j;
+          if (e >= g * per && e < (g + 1) * per) {
+            b = max(b, min(a, key[j]));
+            a = max(a, key[j]);
+          }
         }
+        const unsigned best = __reduce_max_sync(kAll, a);
+        const unsigned holders = __ballot_sync(kAll, a == best);
+        // The second best: the best again where two lanes hold it, else the
+        // best of the other lanes' first and the holder's second.
+        const unsigned second = __reduce_max_sync(kAll, (holders & (holders - 1)) ? best : (a == best ? b : a));
+        if (lane == g) gkey = group_key(best, second);
       }
-      const unsigned best = __reduce_max_sync(kAll, a);
-      const unsigned holders = __ballot_sync(kAll, a == best);
-      // The second best: the best again where two lanes hold it, else the
-      // best of the other lanes' first and the holder's second.
-      const unsigned second = __reduce_max_sync(
-          kAll, (holders & (holders - 1)) ? best : (a == best ? b : a));
-      // Half the sum of the two: the same order, and two logits at the type's
-      // lowest value do not overflow to -inf.
-      if (lane == g && best != 0) {
-        const float f = value_of(best);
-        gkey = key_of(0.5f * f + 0.5f * (second != 0 ? value_of(second) : f));
-      }
+      g_of = lane;
     }
+    // The lanes' groups ascend, so the lowest lane of equal ranks has the lowest group.
     unsigned keep = 0;
     for (int i = 0; i < p.kept; ++i) {
       const unsigned best = __reduce_max_sync(kAll, gkey);
       if (best == 0) break;
-      const int g = __ffs(__ballot_sync(kAll, gkey == best)) - 1;
-      keep |= 1u << g;
-      if (lane == g) gkey = 0;
+      const int l = __ffs(__ballot_sync(kAll, gkey == best)) - 1;
+      keep |= 1u << __shfl_sync(kAll, g_of, l);
+      if (lane == l) gkey = 0;
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int e = lane + 32 * j;
+      const int e = lane * J + j;
       if (e < p.E && !((keep >> (e / per)) & 1)) key[j] = 0;
     }
   }
+  unsigned best = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) best = max(best, key[j]);
   int mine = -1;  // lane k: the k-th choice
   for (int k = 0; k < p.K; ++k) {
-    unsigned best = 0;
-    int at = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        at = j;
-      }
     const unsigned top = __reduce_max_sync(kAll, best);
     if (top == 0) break;
-    const unsigned e = __reduce_min_sync(kAll, best == top ? static_cast<unsigned>(lane + 32 * at) : 0x7fffffffu);
-    if (lane == k) mine = static_cast<int>(e);
+    const int l = __ffs(__ballot_sync(kAll, best == top)) - 1;
+    int e = 0;
+    if (lane == l) {
+      // The first of the run that holds it leaves.
+      bool found = false;
+      best = 0;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (static_cast<unsigned>(lane + 32 * j) == e) key[j] = 0;
+      for (int j = 0; j < J; ++j) {
+        if (!found && key[j] == top) {
+          found = true;
+          e = lane * J + j;
+          key[j] = 0;
+        }
+        best = max(best, key[j]);
+      }
+    }
+    e = __shfl_sync(kAll, e, l);
+    if (lane == k) mine = e;
   }
   // Weights: lane k has the k-th choice's.
   const float zk = mine >= 0 ? logit<T>(p.logits, row + mine) : -INFINITY;
@@ -200,9 +256,12 @@ __global__ void __launch_bounds__(kWarps * 32) ep_router_bwd_kernel(const Router
       const float w = S > 0.0f ? x / S : 0.0f;
       d = w * (g - warp_sum(g * w));
     }
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (lane + 32 * j < p.E) out[lane + 32 * j] = from_f32<T>(0.0f);
+    constexpr int kVec = 16 / sizeof(T);
+    if (p.E % kVec == 0 && reinterpret_cast<uintptr_t>(p.grad_logits) % 16 == 0) {
+      for (int i = lane * kVec; i < p.E; i += 32 * kVec) *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int i = lane; i < p.E; i += 32) out[i] = from_f32<T>(0.0f);
+    }
   } else {
     float z[J];
     unsigned m = 0;

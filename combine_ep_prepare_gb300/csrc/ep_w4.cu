@@ -4,18 +4,23 @@
 // row n (low nibble of a byte: even k).  out[r][n] = sum_k x[r][k] w[e][n][k]
 // for the rows of expert e, or silu(gate) * up of the two halves of n.
 //
-// Bound by the weights' bytes, and close behind by the logic unit, which
-// unpacks them.  A persistent block per SM walks units of 256 down to 32
-// weight rows of one expert: one warp keeps a ring of four stages of 32 KB
-// filled by TMA (and the receive rows' share with them), running ahead across
-// units; of eight others each owns 32 weight rows and a share of the reduction.  Where there are few units, 2 or
-// 4 warps share 32 rows and split the reduction, joined through shared
-// memory in a fixed order.  A stage is 256 rows of 128 bytes (256 weights):
-// the copies cost a block about two clocks a row, so 64-byte rows would not
-// keep up with memory, and copies of 16 or 32 rows for each warp cost 90
-// clocks each to issue.  (Such boxes, 20 to 32 a stage, took 83 us for one
-// token's up products of 8 experts, 7168 -> 2 x 2048; cp.async by the warps
-// themselves, 40% more instructions, 53 us.)
+// Bound by the logic unit, which unpacks the weights, and not far behind by
+// their bytes: without the unpacking a decode batch's down products (64
+// experts, 8 rows each, 2048 -> 7168) take 90 us, with it 136; memory alone
+// would take 73.  (Without the copies it takes 131.)
+//
+// Two persistent blocks per SM walk units of 256 down to 64 weight rows of one
+// expert: one warp keeps a ring of two 32 KB stages filled by TMA (and the
+// receive rows' share with them), running ahead across units; of eight others
+// each owns 32 weight rows and a share of the reduction.  Where there are few
+// units, 2 or 4 warps share 32 rows and split the reduction, joined through
+// shared memory in a fixed order.  One block of eight consumers per SM took
+// 148 us for those down products: two warps a scheduler do not hide each
+// other's latencies.  A stage is 256 rows of 128 bytes (256 weights): the
+// copies cost a block about two clocks a row, so 64-byte rows would not keep
+// up with memory, and copies of 16 or 32 rows for each warp cost 90 clocks
+// each to issue (20 to 32 of them a stage: 188 us).  cp.async by the consumers
+// themselves costs 40% more instructions (169 us).
 //
 // The receive rows are the narrow side of mma.m16n8k16 (weights 16 x 16,
 // receive rows 16 x 8): up to 16 rows share one pass over the weights.  A
@@ -38,7 +43,7 @@ constexpr int kWBytes = kWarps * kBoxBytes;
 constexpr int kSlabBytes = 8 * kChunk * 2;    // eight receive rows' share of a stage
 constexpr int kMaxSlabs = 4;                  // shares times blocks of eight rows
 constexpr int kStageBytes = kWBytes + kMaxSlabs * kSlabBytes;
-constexpr int kStages = 4;
+constexpr int kStages = 2;
 constexpr int kSteps = kChunk / 32;           // steps of 32 reduction elements
 constexpr int kUnitRows = kWarps * kBoxRows;
 constexpr int kMaxSplit = 4;
@@ -227,25 +232,21 @@ struct Consumer {
     unsigned char* smem = block_smem();
     unsigned char* scales = smem + kStages * kStageBytes + warp * (kBoxRows * 16);
     load_scales();
-    // The sums of the present group and of the one before, whose scales are
-    // applied only after the present group's mma have been issued: to wait
-    // for a group's last mma each time took a third of the kernel's time.
-    float acc[2][2][NT][4], sc[2][2][2];
+    float acc[2][NT][4], sc[2][2];
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      sc[1][f][0] = sc[1][f][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) total[f][i][j] = acc[1][f][i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) total[f][i][j] = 0.0f;
     }
-    auto apply = [&](int q) {
+    auto apply = [&]() {
 #pragma unroll
       for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) total[f][i][j] = fmaf(sc[q][f][j >> 1], acc[q][f][i][j], total[f][i][j]);
+          for (int j = 0; j < 4; ++j) total[f][i][j] = fmaf(sc[f][j >> 1], acc[f][i][j], total[f][i][j]);
     };
     // Fragment f's rows g and g + 8 (gated: the gate row and the up row of one
     // feature) in the stage: this warp's rows of its share's box; the gate
@@ -278,7 +279,6 @@ struct Consumer {
           b[i][3] = __byte_perm(v.y, v.w, 0x7632);
         }
         const unsigned char* w0 = words + ((kb ^ g) << 4);
-        const int q = kb * 32 / G & 1;
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           unsigned a[2][4];
@@ -287,28 +287,19 @@ struct Consumer {
           const unsigned lo[4] = {a[0][0], a[1][0], a[0][1], a[1][1]}, hi[4] = {a[0][2], a[1][2], a[0][3], a[1][3]};
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            if (kb * 32 % G == 0) Nib<T>::mma0(acc[q][f][i], lo, b[i][0], b[i][1]);
-            else Nib<T>::mma(acc[q][f][i], lo, b[i][0], b[i][1]);
-            Nib<T>::mma(acc[q][f][i], hi, b[i][2], b[i][3]);
+            if (kb * 32 % G == 0) Nib<T>::mma0(acc[f][i], lo, b[i][0], b[i][1]);
+            else Nib<T>::mma(acc[f][i], lo, b[i][0], b[i][1]);
+            Nib<T>::mma(acc[f][i], hi, b[i][2], b[i][3]);
           }
         }
         if ((kb + 1) * 32 % G == 0) {
           const T* at_g = reinterpret_cast<const T*>(scales + g * 16) + kb * 32 / G;
-          apply(q ^ 1);
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            sc[q][f][0] = to_f32(at_g[f * kScaleF / 2]);
-            sc[q][f][1] = to_f32(at_g[(f * kScaleF + kScaleH) / 2]);
+            sc[f][0] = to_f32(at_g[f * kScaleF / 2]);
+            sc[f][1] = to_f32(at_g[(f * kScaleF + kScaleH) / 2]);
           }
-          if (kb * 32 >= left) {
-            // Past the share's end: another share's rows, or none.
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-              for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[q][f][i][j] = 0.0f;
-          }
+          if (kb * 32 < left) apply();  // past the share's end: another share's rows, or none
         }
       }
       left -= kChunk;
@@ -319,7 +310,6 @@ struct Consumer {
         phase ^= 1;
       }
     }
-    apply(1);  // a stage has an even number of groups
     return true;
   }
 
@@ -389,7 +379,7 @@ struct Maps {
 };
 
 template <typename T, int G, bool gated>
-__global__ void __launch_bounds__(kThreads, 1) ep_w4_kernel(const __grid_constant__ Maps maps, const W4Params p) {
+__global__ void __launch_bounds__(kThreads, 2) ep_w4_kernel(const __grid_constant__ Maps maps, const W4Params p) {
   unsigned char* smem = block_smem();
   Shared& s = *reinterpret_cast<Shared*>(smem + kStages * kStageBytes + kScaleBytes + kRedBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -406,11 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1) ep_w4_kernel(const __grid_constan
   if (threadIdx.x == 0) s.ok = blocks_ok(p.hdr, p.R);
   __syncthreads();
   if (!s.ok) return;
-  // The reduction is split until there are two units per block.
+  // The reduction is split until there is a unit for every block.
   const int chunks = (p.K + kChunk - 1) / kChunk;
   scan_units(p, 1, s);
   int KW = 1;
-  while (KW < kMaxSplit && 2 * KW <= chunks && s.cum[p.E] * KW < 2 * static_cast<int>(gridDim.x)) KW *= 2;
+  while (KW < kMaxSplit && 2 * KW <= chunks && s.cum[p.E] * KW < static_cast<int>(gridDim.x)) KW *= 2;
   __syncthreads();
   if (KW > 1) scan_units(p, KW, s);
   const int total_units = s.cum[p.E];
@@ -475,7 +465,7 @@ cudaError_t launch_one(const W4Params& p, const Maps& maps, int num_sms, cudaStr
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(ep_w4_kernel<T, G, gated>),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
   if (e != cudaSuccess) return e;
-  return launch_pdl(ep_w4_kernel<T, G, gated>, dim3(num_sms), dim3(kThreads), kSmemBytes, s, 0, maps, p);
+  return launch_pdl(ep_w4_kernel<T, G, gated>, dim3(2 * num_sms), dim3(kThreads), kSmemBytes, s, 0, maps, p);
 }
 
 template <typename T>
