@@ -30,7 +30,7 @@ __device__ __forceinline__ float logit(const void* p, long long i) { return to_f
 __device__ __forceinline__ unsigned key_of(float v) {
   if (!(v > -INFINITY)) return 0;
   const unsigned u = __float_as_uint(v + 0.0f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  return u ^ (static_cast<unsigned>(static_cast<int>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(unsigned key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
@@ -116,85 +116,99 @@ __global__ void __launch_bounds__(kWarps * 32) ep_router_kernel(const RouterPara
       zsum = warp_sum(s);
     }
   }
+  // This lane's best two (of equal ones the lower index first); more are
+  // looked for only when a lane has had two chosen.
+  unsigned a = 0, b = 0;
+  int at = 0, bt = 0;
+  auto best_two = [&]() {
+    a = b = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const bool over_a = key[j] > a, over_b = key[j] > b;
+      b = over_a ? a : over_b ? key[j] : b;
+      bt = over_a ? at : over_b ? j : bt;
+      a = over_a ? key[j] : a;
+      at = over_a ? j : at;
+    }
+  };
+  best_two();
   if (p.groups > 1) {
     const int per = p.E / p.groups;
     const int span = per / J;  // lanes of a group, where groups are runs of whole lanes
-    unsigned gkey = 0;         // one lane of each group: its rank
-    int g_of = 0;              // the group of that lane
-    if (per % J == 0 && (span & (span - 1)) == 0) {
-      unsigned a = 0, b = 0;  // the two best
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        b = max(b, min(a, key[j]));
-        a = max(a, key[j]);
+    unsigned gkey = 0;         // one lane of each group, ascending: its rank
+    int shift = 0;             // log2 of the lanes between those
+    const bool whole = per % J == 0 && (span & (span - 1)) == 0;
+    if (whole) {
+      unsigned x = a, y = b;
+      for (int d = 1; d < span; d <<= 1, ++shift) {
+        const unsigned ox = __shfl_xor_sync(kAll, x, d), oy = __shfl_xor_sync(kAll, y, d);
+        y = max(min(x, ox), max(y, oy));
+        x = max(x, ox);
       }
-      for (int d = 1; d < span; d <<= 1) {
-        const unsigned oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
-        b = max(min(a, oa), max(b, ob));
-        a = max(a, oa);
-      }
-      g_of = lane / span;
-      if (lane % span == 0) gkey = group_key(a, b);
+      if ((lane & (span - 1)) == 0) gkey = group_key(x, y);
     } else {
       for (int g = 0; g < p.groups; ++g) {
-        unsigned a = 0, b = 0;  // this lane's two best of group g
+        unsigned x = 0, y = 0;  // this lane's two best of group g
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const int e = lane * J + j;
           if (e >= g * per && e < (g + 1) * per) {
-            b = max(b, min(a, key[j]));
-            a = max(a, key[j]);
+            y = max(y, min(x, key[j]));
+            x = max(x, key[j]);
           }
         }
-        const unsigned best = __reduce_max_sync(kAll, a);
-        const unsigned holders = __ballot_sync(kAll, a == best);
+        const unsigned best = __reduce_max_sync(kAll, x);
+        const unsigned holders = __ballot_sync(kAll, x == best);
         // The second best: the best again where two lanes hold it, else the
         // best of the other lanes' first and the holder's second.
-        const unsigned second = __reduce_max_sync(kAll, (holders & (holders - 1)) ? best : (a == best ? b : a));
+        const unsigned second = __reduce_max_sync(kAll, (holders & (holders - 1)) ? best : (x == best ? y : x));
         if (lane == g) gkey = group_key(best, second);
       }
-      g_of = lane;
     }
-    // The lanes' groups ascend, so the lowest lane of equal ranks has the lowest group.
-    unsigned keep = 0;
+    unsigned keep = 0;  // bit of each kept group's lane; of equal ranks the lowest
     for (int i = 0; i < p.kept; ++i) {
       const unsigned best = __reduce_max_sync(kAll, gkey);
       if (best == 0) break;
-      const int l = __ffs(__ballot_sync(kAll, gkey == best)) - 1;
-      keep |= 1u << __shfl_sync(kAll, g_of, l);
-      if (lane == l) gkey = 0;
+      const unsigned holders = __ballot_sync(kAll, gkey == best), lowest = holders & (0u - holders);
+      keep |= lowest;
+      if (lowest >> lane & 1) gkey = 0;
     }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int e = lane * J + j;
-      if (e < p.E && !((keep >> (e / per)) & 1)) key[j] = 0;
-    }
-  }
-  unsigned best = 0;
-#pragma unroll
-  for (int j = 0; j < J; ++j) best = max(best, key[j]);
-  int mine = -1;  // lane k: the k-th choice
-  for (int k = 0; k < p.K; ++k) {
-    const unsigned top = __reduce_max_sync(kAll, best);
-    if (top == 0) break;
-    const int l = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    int e = 0;
-    if (lane == l) {
-      // The first of the run that holds it leaves.
-      bool found = false;
-      best = 0;
+    if (whole) {
+      if (!(keep >> (lane >> shift << shift) & 1)) a = b = 0;
+    } else {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        if (!found && key[j] == top) {
-          found = true;
-          e = lane * J + j;
-          key[j] = 0;
+        const int e = lane * J + j;
+        if (e < p.E && !(keep >> (e / per) & 1)) key[j] = 0;
+      }
+      best_two();
+    }
+  }
+  int mine = -1, had = 0;  // lane k: the k-th choice; how many of this lane's were chosen
+  for (int k = 0; k < p.K; ++k) {
+    const unsigned top = __reduce_max_sync(kAll, a);
+    if (top == 0) break;
+    const int l = __ffs(__ballot_sync(kAll, a == top)) - 1;
+    const int e = l * J + __shfl_sync(kAll, at, l);
+    if (lane == k) mine = e;
+    if (lane == l) {
+      if (++had == 1) {
+        a = b;
+        at = bt;
+      } else {
+        // The best after (top, at) in the order of the choice.
+        const int last = at;
+        a = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const bool left = key[j] < top || (key[j] == top && j > last);
+          if (left && key[j] > a) {
+            a = key[j];
+            at = j;
+          }
         }
-        best = max(best, key[j]);
       }
     }
-    e = __shfl_sync(kAll, e, l);
-    if (lane == k) mine = e;
   }
   // Weights: lane k has the k-th choice's.
   const float zk = mine >= 0 ? logit<T>(p.logits, row + mine) : -INFINITY;
