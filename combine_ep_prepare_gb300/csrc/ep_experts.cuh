@@ -114,9 +114,9 @@ __device__ __forceinline__ void swiglu_bwd(float gate, float up, float da, float
   *dup = da * gate * sg;
 }
 
-// Plain products on the CUDA cores (every type).
+// Products of float32 rows on the CUDA cores.
 cudaError_t launch_product_simt(const ProductParams& p, int num_sms, cudaStream_t s);
-// The same on the tensor cores (bf16, fp16).
+// Products of bf16 and fp16 rows on the tensor cores.
 cudaError_t launch_product_tc(const ProductParams& p, int num_sms, cudaStream_t s);
 
 struct W4Params {

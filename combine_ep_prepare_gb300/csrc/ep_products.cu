@@ -1,92 +1,82 @@
-// ep_products.cu -- products grouped by expert on the CUDA cores.
+// ep_products.cu -- products grouped by expert of float32 rows, on the CUDA
+// cores (the tensor cores have no float32 operands).
 //
 // For every expert e with rows [off_e, off_e + c_e):
 //   forward   out[r][n] = sum_k a[r][k] w[e][n][k]
 //   dgrad     out[r][k] = sum_n a[r][n] w[e][n][k]
 //   wgrad     out[e][n][k] (+)= sum_r a[r][n] b[r][k]
 // with the gated activation silu(gate) * up, or its derivative, applied to the
-// float32 sums before the one rounding.  Sums are float32 fused multiply-adds
-// in ascending order of the reduction.
+// sums.  Sums are float32 fused multiply-adds in ascending order of the
+// reduction.
 #include "ep_experts.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kTile = 128;   // output tile, rows and columns
-constexpr int kStep = 16;    // reduction elements per step
-constexpr int kThreads = 256;
-constexpr int kPad = 4;      // shared-memory row padding against bank conflicts
+constexpr int kPad = 4;  // shared-memory row padding against bank conflicts
 
-// Eight consecutive elements as float32.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* v) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    const T* e = reinterpret_cast<const T*>(&x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
-  }
+// Output tiles of TILE x TILE, 8 x 8 sums per thread, STEP reduction elements
+// at a time: a thread moves eight elements of each operand per step.
+template <int TILE>
+struct Shape {
+  static constexpr int kThreads = (TILE / 8) * (TILE / 8);
+  static constexpr int kStep = kThreads * 8 / TILE;
+  using Row = float[TILE + kPad];
+};
+
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  *reinterpret_cast<float4*>(v) = reinterpret_cast<const float4*>(p)[0];
+  *reinterpret_cast<float4*>(v + 4) = reinterpret_cast<const float4*>(p)[1];
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const float* v) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    alignas(8) T e[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = from_f32<T>(v[i]);
-    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(e);
-  }
+// Two float32 multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(float2* c, const float2& a, const float2& b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;"
+      : "+l"(*reinterpret_cast<unsigned long long*>(c))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)), "l"(*reinterpret_cast<const unsigned long long*>(&b)));
 }
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, float* v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = to_f32(p[i]);
-}
-
-// One operand's share of a step: 8 elements per thread of a kTile x kStep slab.
-// kc: the reduction index is the contiguous one.
-template <typename T, bool kc>
+// One operand's share of a step.  kc: the reduction index is the contiguous one.
+template <int TILE, bool kc>
 struct Slab {
+  static constexpr int kParts = kc ? Shape<TILE>::kStep / 8 : TILE / 8;  // runs of eight in a contiguous row
   float v[8];
+  static __device__ __forceinline__ int mn() { return kc ? threadIdx.x / kParts : threadIdx.x % kParts * 8; }
+  static __device__ __forceinline__ int k() { return kc ? threadIdx.x % kParts * 8 : threadIdx.x / kParts; }
   // base: element (0, 0); ld: elements between rows; mn / k limits.
-  __device__ __forceinline__ void load(const T* base, long long ld, int mn_lim, int k0, int k_lim) {
-    const int t = threadIdx.x;
-    const int mn = kc ? t >> 1 : (t & 15) * 8;
-    const int k = k0 + (kc ? (t & 1) * 8 : t >> 4);
-    if (mn < mn_lim && k < k_lim) {
-      load8(kc ? base + mn * ld + k : base + k * ld + mn, v);
+  __device__ __forceinline__ void load(const float* base, long long ld, int mn_lim, int k0, int k_lim) {
+    const int m = mn(), kk = k0 + k();
+    if (m < mn_lim && kk < k_lim) {
+      load8(kc ? base + m * ld + kk : base + kk * ld + m, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
     }
   }
-  __device__ __forceinline__ void store(float (*s)[kTile + kPad]) const {
-    const int t = threadIdx.x;
+  __device__ __forceinline__ void store(typename Shape<TILE>::Row* s) const {
     if constexpr (kc) {
-      const int mn = t >> 1, k = (t & 1) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[k + i][mn] = v[i];
+      for (int i = 0; i < 8; ++i) s[k() + i][mn()] = v[i];
     } else {
-      const int mn = (t & 15) * 8, k = t >> 4;
-      *reinterpret_cast<float4*>(&s[k][mn]) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(&s[k][mn + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+      store4(&s[k()][mn()], v);
+      store4(&s[k()][mn() + 4], v + 4);
     }
   }
 };
 
-// A 128 x 128 tile per block, 8 x 8 sums per thread (rows and columns in two
-// runs of four, 64 apart, so that a warp's shared-memory reads of four floats
-// do not collide), the next step's loads in flight while the present one is
-// multiplied.  In the gated forward the tile's columns are 64 gate and 64 up
-// columns of the same features, so that one thread holds both.
-template <typename T, int kind>
-__global__ void __launch_bounds__(kThreads) ep_product_simt_kernel(const ProductParams p) {
+// A tile per block, rows and columns of a thread in two runs of four, TILE / 2
+// apart, so that a warp's shared-memory reads of four floats do not collide;
+// the next step's loads are in flight while the present one is multiplied.  In
+// the gated forward one half of the tile's columns are gate columns and the
+// other the up columns of the same features, so that one thread holds both.
+// PER_SM: blocks per SM that the registers are to leave room for, 0 as the
+// compiler has it.
+template <int TILE, int PER_SM, int kind>
+__global__ void __launch_bounds__(Shape<TILE>::kThreads, PER_SM) ep_product_simt_kernel(const ProductParams p) {
+  constexpr int kThreads = Shape<TILE>::kThreads, kStep = Shape<TILE>::kStep, kTile = TILE, kHalf = TILE / 2;
   constexpr bool rows_out = kind != kProdWgrad;
   constexpr bool a_kc = rows_out;
   constexpr bool b_kc = kind == kProdFwd || kind == kProdFwdSwiglu;
@@ -96,9 +86,9 @@ __global__ void __launch_bounds__(kThreads) ep_product_simt_kernel(const Product
   __shared__ int part[32];
   pdl_wait();
   if (!blocks_ok(p.hdr, p.R)) return;
-  const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
-  const T* a = static_cast<const T*>(p.a);
-  const T* b = static_cast<const T*>(p.b);
+  const int t = threadIdx.x, tx = t % (TILE / 8), ty = t / (TILE / 8);
+  const float* a = static_cast<const float*>(p.a);
+  const float* b = static_cast<const float*>(p.b);
   const int F = p.N / 2;
   constexpr int cols_per_tile = kind == kProdFwdSwiglu ? kTile / 2 : kTile;
   const int cols = kind == kProdFwd ? p.N : kind == kProdFwdSwiglu ? F : p.K;
@@ -134,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) ep_product_simt_kernel(const Product
     }
     // Operands of this tile.
     const long long w0 = static_cast<long long>(e) * p.N * p.K;
-    const T *ab, *bb;
+    const float *ab, *bb;
     long long ald, bld;
     int a_lim, b_lim, red;
     if constexpr (rows_out) {
@@ -154,21 +144,21 @@ __global__ void __launch_bounds__(kThreads) ep_product_simt_kernel(const Product
       b_lim = p.K - c0;
       red = cnt;
     }
-    float acc[8][8];
+    alignas(8) float acc[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
 
-    Slab<T, a_kc> la;
-    Slab<T, b_kc> lb;
+    Slab<TILE, a_kc> la;
+    Slab<TILE, b_kc> lb;
     auto load = [&](int k0) {
       la.load(ab, ald, a_lim, k0, red);
       if constexpr (kind == kProdFwdSwiglu) {
-        // slab columns 0..63: gate features c0.., 64..127: up features c0..
-        const int half = t >> 7;
-        lb.load(bb + (half ? (static_cast<long long>(F) - 64) * bld : 0), bld,
-                half ? (b_lim < 64 ? b_lim : 64) + 64 : (b_lim < 64 ? b_lim : 64), k0, red);
+        // slab columns below kHalf: gate features from c0 on, the others: up features from c0 on
+        const int lim = b_lim < kHalf ? b_lim : kHalf;
+        const bool up = lb.mn() >= kHalf;
+        lb.load(bb + (up ? (static_cast<long long>(F) - kHalf) * bld : 0), bld, up ? kHalf + lim : lim, k0, red);
       } else {
         lb.load(bb, bld, b_lim, k0, red);
       }
@@ -184,15 +174,16 @@ __global__ void __launch_bounds__(kThreads) ep_product_simt_kernel(const Product
         if (more) load(k0 + kStep);
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
-          float ra[8], rb[8];
+          float ra[8];
+          alignas(16) float2 rb[4];
           *reinterpret_cast<float4*>(ra) = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 4]);
-          *reinterpret_cast<float4*>(ra + 4) = *reinterpret_cast<const float4*>(&sa[buf][k][64 + ty * 4]);
+          *reinterpret_cast<float4*>(ra + 4) = *reinterpret_cast<const float4*>(&sa[buf][k][kHalf + ty * 4]);
           *reinterpret_cast<float4*>(rb) = *reinterpret_cast<const float4*>(&sb[buf][k][tx * 4]);
-          *reinterpret_cast<float4*>(rb + 4) = *reinterpret_cast<const float4*>(&sb[buf][k][64 + tx * 4]);
+          *reinterpret_cast<float4*>(rb + 2) = *reinterpret_cast<const float4*>(&sb[buf][k][kHalf + tx * 4]);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(ra[i], rb[j], acc[i][j]);
+            for (int j = 0; j < 4; ++j) fma2(reinterpret_cast<float2*>(&acc[i][2 * j]), make_float2(ra[i], ra[i]), rb[j]);
         }
         if (more) {
           la.store(sa[buf ^ 1]);
@@ -202,13 +193,13 @@ __global__ void __launch_bounds__(kThreads) ep_product_simt_kernel(const Product
         buf ^= 1;
       }
     }
-    // Epilogue: rows m0 + {0, 64} + 4 ty + i.  A padding row's sums are +0
+    // Epilogue: rows m0 + {0, kHalf} + 4 ty + i.  A padding row's sums are +0
     // (its operand was not read), so it gets zeros without a case of its own,
     // except through the activation's derivative, which reads `pre`.
     const int m_lim = rows_out ? rows - m0 : p.N - m0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int m = (i >> 2) * 64 + ty * 4 + (i & 3);
+      const int m = (i >> 2) * kHalf + ty * 4 + (i & 3);
       if (m >= m_lim) continue;
       if constexpr (kind == kProdFwdSwiglu) {
         const int f = c0 + tx * 4;
@@ -217,51 +208,41 @@ __global__ void __launch_bounds__(kThreads) ep_product_simt_kernel(const Product
         float act[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) act[j] = swiglu(acc[i][j], acc[i][4 + j]);
-        store4(static_cast<T*>(p.out) + r * F + f, act);
+        store4(static_cast<float*>(p.out) + r * F + f, act);
         if (p.out2 != nullptr) {
-          T* pre = static_cast<T*>(p.out2) + r * p.N;
+          float* pre = static_cast<float*>(p.out2) + r * p.N;
           store4(pre + f, acc[i]);
           store4(pre + F + f, acc[i] + 4);
         }
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int c = c0 + h * 64 + tx * 4;
+          const int c = c0 + h * kHalf + tx * 4;
           if (c >= cols) continue;
           float* v = acc[i] + h * 4;
           if constexpr (kind == kProdDgradSwiglu) {
             const long long r = (static_cast<long long>(off) + m0 + m) * 2 * p.K;
             float dg[4], du[4];
             if (m0 + m < cnt) {
-              float g[4], u[4];
-              load4(static_cast<const T*>(p.pre) + r + c, g);
-              load4(static_cast<const T*>(p.pre) + r + p.K + c, u);
+              const float* g = static_cast<const float*>(p.pre) + r + c;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) swiglu_bwd(g[j], u[j], v[j], &dg[j], &du[j]);
+              for (int j = 0; j < 4; ++j) swiglu_bwd(g[j], g[p.K + j], v[j], &dg[j], &du[j]);
             } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j) dg[j] = du[j] = 0.0f;
             }
-            store4(static_cast<T*>(p.out) + r + c, dg);
-            store4(static_cast<T*>(p.out) + r + p.K + c, du);
+            store4(static_cast<float*>(p.out) + r + c, dg);
+            store4(static_cast<float*>(p.out) + r + p.K + c, du);
           } else if constexpr (kind == kProdWgrad) {
             const long long at = w0 + (static_cast<long long>(m0) + m) * p.K + c;
-            if (p.out_f32) {
-              float* o = static_cast<float*>(p.out) + at;
-              if (p.accumulate)
+            float* o = static_cast<float*>(p.out) + at;
+            if (p.accumulate) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] += o[j];
-              store4(o, v);
-            } else {
-              T* o = static_cast<T*>(p.out) + at;
-              if (p.accumulate) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] += to_f32(o[j]);
-              }
-              store4(o, v);
+              for (int j = 0; j < 4; ++j) v[j] += o[j];
             }
+            store4(o, v);
           } else {
-            store4(static_cast<T*>(p.out) + (static_cast<long long>(off) + m0 + m) * cols + c, v);
+            store4(static_cast<float*>(p.out) + (static_cast<long long>(off) + m0 + m) * cols + c, v);
           }
         }
       }
@@ -270,22 +251,32 @@ __global__ void __launch_bounds__(kThreads) ep_product_simt_kernel(const Product
   }
 }
 
-template <typename T>
-cudaError_t launch_typed(const ProductParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid(num_sms * 2), block(kThreads);
+template <int TILE, int PER_SM>
+cudaError_t launch_tile(const ProductParams& p, int num_sms, cudaStream_t s) {
+  const dim3 grid(2 * num_sms), block(Shape<TILE>::kThreads);
   switch (p.kind) {
-    case kProdFwd: return launch_pdl(ep_product_simt_kernel<T, kProdFwd>, grid, block, 0, s, 0, p);
-    case kProdFwdSwiglu: return launch_pdl(ep_product_simt_kernel<T, kProdFwdSwiglu>, grid, block, 0, s, 0, p);
-    case kProdDgrad: return launch_pdl(ep_product_simt_kernel<T, kProdDgrad>, grid, block, 0, s, 0, p);
-    case kProdDgradSwiglu: return launch_pdl(ep_product_simt_kernel<T, kProdDgradSwiglu>, grid, block, 0, s, 0, p);
-    default: return launch_pdl(ep_product_simt_kernel<T, kProdWgrad>, grid, block, 0, s, 0, p);
+    case kProdFwd: return launch_pdl(ep_product_simt_kernel<TILE, PER_SM, kProdFwd>, grid, block, 0, s, 0, p);
+    case kProdFwdSwiglu: return launch_pdl(ep_product_simt_kernel<TILE, PER_SM, kProdFwdSwiglu>, grid, block, 0, s, 0, p);
+    case kProdDgrad: return launch_pdl(ep_product_simt_kernel<TILE, PER_SM, kProdDgrad>, grid, block, 0, s, 0, p);
+    default: return launch_pdl(ep_product_simt_kernel<TILE, PER_SM, kProdDgradSwiglu>, grid, block, 0, s, 0, p);
   }
 }
 
 }  // namespace
 
+// Tiles of 128 x 128 read least.  Two blocks per SM hide each other's
+// latencies (dgrad of 8 x 1,024 rows x 2 x 1024 -> 2048 1.73 -> 1.42 ms), but
+// with hardly a tile per SM the device puts pairs of them on some SMs and none
+// on others (2,000 rows x 1024 -> 1024, 160 tiles: 105 -> 193 us), hence one
+// where the buffer's capacity of rows makes fewer than three tiles per SM.
+// wgrad, whose operands both lie along the tile's sides, takes 64 x 64 tiles:
+// 2.94 ms for 3.29 at 16 experts x 512 rows x 4096 x 2048.
 cudaError_t launch_product_simt(const ProductParams& p, int num_sms, cudaStream_t s) {
-  return launch_typed<float>(p, num_sms, s);
+  if (p.kind == kProdWgrad)
+    return launch_pdl(ep_product_simt_kernel<64, 8, kProdWgrad>, dim3(8 * num_sms), dim3(Shape<64>::kThreads), 0, s, 0, p);
+  const long long cols = p.kind == kProdFwd || p.kind == kProdFwdSwiglu ? p.N : p.K;
+  const long long tiles = (p.R / 128 + (p.E < p.R ? p.E : p.R)) * ((cols + 127) / 128);
+  return tiles < 3ll * num_sms ? launch_tile<128, 0>(p, num_sms, s) : launch_tile<128, 2>(p, num_sms, s);
 }
 
 }  // namespace ep
