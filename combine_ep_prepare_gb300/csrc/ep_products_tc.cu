@@ -49,6 +49,13 @@ constexpr int kHalfM = kTileM / 2;
 constexpr int kABytes = kHalfM * kSlab * 2, kBBytes = kTileN / 2 * kSlab * 2;
 constexpr int kStages = 6;
 constexpr int kBoxBytes = kSlab * 128;  // 64 rows of 64 elements
+// The accumulator in tensor memory is rounded toward zero with every mma: a
+// weight gradient of 512 rows is off by 4.7e-7 (of its norm), of 4,096 by
+// 4.4e-6, of 16,384 by 1.9e-5.  That drowns in a 16-bit result.  A float32
+// gradient is summed over segments of eight slabs (512 rows): each is added
+// to the output in float32, rounded to nearest, by the lanes that wrote the
+// one before, while it is still in L2.
+constexpr int kSegment = 8;
 
 // f0: first feature; r0, n: first row and row count (N, a multiple of 32) of
 // the pair's tile (wgrad: output features).
@@ -241,7 +248,7 @@ struct Rows {
 
 template <typename T, int kind, typename O>
 __device__ __forceinline__ void write_half(const ProductParams& p, const Tile& t, uint32_t acc, int rank, int w, int half,
-                                           int lane, float* stage) {
+                                           int lane, float* stage, bool add) {
   if constexpr (sizeof(O) == 4) {
     // float32 gradients: a lane's feature of one row from 32 lanes is a whole
     // line as it is.
@@ -255,7 +262,7 @@ __device__ __forceinline__ void write_half(const ProductParams& p, const Tile& t
       tc::tmem_ld_wait();
       float* o = out + static_cast<long long>(c) * p.K;
       if (c + 32 <= stop) {
-        if (p.accumulate) {
+        if (add) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] += o[static_cast<long long>(j) * p.K];
         }
@@ -264,7 +271,7 @@ __device__ __forceinline__ void write_half(const ProductParams& p, const Tile& t
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (c + j < stop) o[static_cast<long long>(j) * p.K] = p.accumulate ? v[j] + o[static_cast<long long>(j) * p.K] : v[j];
+          if (c + j < stop) o[static_cast<long long>(j) * p.K] = add ? v[j] + o[static_cast<long long>(j) * p.K] : v[j];
       }
     }
     return;
@@ -294,7 +301,7 @@ __device__ __forceinline__ void write_half(const ProductParams& p, const Tile& t
     tc::tmem_ld16(acc + c, v);
     tc::tmem_ld_wait();
     const int r0 = c + 4 * w;
-    if (kind == kProdWgrad && p.accumulate) {
+    if (kind == kProdWgrad && add) {
       // The old values are added in float32, before the rounding: the rows
       // go through shared memory unrounded, eight at a time.
 #pragma unroll
@@ -520,34 +527,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (long long i = first; i < walk.total && !lost; i += step) {
           walk.at(i, &t);
           if (t.slabs == 0) continue;
-          lost = !tc::mbar_wait(tc::smem_addr(&s.acc_empty[buf]), acc_phase ^ 1, gave_up);
-          if (lost) break;
-          tc::fence_after();
-          const uint32_t d = tmem + buf * kTileN;
           const uint32_t desc = tc::mma_desc(std::is_same<T, __nv_bfloat16>::value, a_mn, b_mn, kTileM, t.n);
-          for (int k = 0; k < t.slabs; ++k) {
-            lost = !tc::mbar_wait(tc::smem_addr(&s.full[stage]), phase, gave_up);
+          const int segment = sizeof(O) == 4 ? kSegment : t.slabs;
+          for (int k0 = 0; k0 < t.slabs && !lost; k0 += segment) {
+            lost = !tc::mbar_wait(tc::smem_addr(&s.acc_empty[buf]), acc_phase ^ 1, gave_up);
             if (lost) break;
             tc::fence_after();
-            const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * (kABytes + kBBytes)), b = a + kABytes;
-            const uint64_t da = a_mn ? tc::desc_mn_major(a, kBoxBytes) : tc::desc_k_major(a);
-            const uint64_t db = b_mn ? tc::desc_mn_major(b, kBoxBytes) : tc::desc_k_major(b);
-            const int left = kind == kProdWgrad ? t.cnt - k * kSlab : kSlab;
+            const uint32_t d = tmem + buf * kTileN;
+            const int k1 = min(t.slabs, k0 + segment);
+            for (int k = k0; k < k1; ++k) {
+              lost = !tc::mbar_wait(tc::smem_addr(&s.full[stage]), phase, gave_up);
+              if (lost) break;
+              tc::fence_after();
+              const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * (kABytes + kBBytes)), b = a + kABytes;
+              const uint64_t da = a_mn ? tc::desc_mn_major(a, kBoxBytes) : tc::desc_k_major(a);
+              const uint64_t db = b_mn ? tc::desc_mn_major(b, kBoxBytes) : tc::desc_k_major(b);
+              const int left = kind == kProdWgrad ? t.cnt - k * kSlab : kSlab;
 #pragma unroll
-            for (int q = 0; q < kSlab / 16; ++q)
-              if (q * 16 < left)
-                tc::mma_f16(d, da + q * (a_mn ? tc::kDescStepMn : tc::kDescStepK),
-                            db + q * (b_mn ? tc::kDescStepMn : tc::kDescStepK), desc, k > 0 || q > 0);
-            tc::mma_commit(tc::smem_addr(&s.empty[stage]));
-            if (k + 1 == t.slabs) tc::mma_commit(tc::smem_addr(&s.acc_full[buf]));
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1;
+              for (int q = 0; q < kSlab / 16; ++q)
+                if (q * 16 < left)
+                  tc::mma_f16(d, da + q * (a_mn ? tc::kDescStepMn : tc::kDescStepK),
+                              db + q * (b_mn ? tc::kDescStepMn : tc::kDescStepK), desc, k > k0 || q > 0);
+              tc::mma_commit(tc::smem_addr(&s.empty[stage]));
+              if (k + 1 == k1) tc::mma_commit(tc::smem_addr(&s.acc_full[buf]));
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+              }
             }
-          }
-          if (++buf == 2) {
-            buf = 0;
-            acc_phase ^= 1;
+            if (++buf == 2) {
+              buf = 0;
+              acc_phase ^= 1;
+            }
           }
         }
         if (lost) {
@@ -586,16 +597,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long i = first; i < walk.total; i += step) {
         walk.at(i, &t);
         const bool has = t.slabs > 0;
-        if (has) {
+        if (!has && p.accumulate) continue;  // an expert without rows keeps its gradient
+        auto wait = [&]() {
           // The four warps go on or leave together: write_half has barriers.
-          if (!half_all(half, tc::mbar_wait(tc::smem_addr(&s.acc_full[buf]), acc_phase, gave_up))) break;
+          const bool ok = half_all(half, tc::mbar_wait(tc::smem_addr(&s.acc_full[buf]), acc_phase, gave_up));
           tc::fence_after();
-        } else if (p.accumulate) {
-          continue;  // an expert without rows keeps its gradient
-        }
-        if (has) {
-          write_half<T, kind, O>(p, t, tmem + buf * kTileN + (static_cast<uint32_t>(w * 32) << 16), rank, w, half, lane,
-                              rows_out + half * kRows * kHalfM);
+          return ok;
+        };
+        auto release = [&]() {
           tc::fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive_cluster(tc::in_block(tc::smem_addr(&s.acc_empty[buf]), 0));
@@ -603,7 +612,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             buf = 0;
             acc_phase ^= 1;
           }
+        };
+        const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+        bool fine = true;
+        for (int k = 0; k < t.slabs && fine; k += sizeof(O) == 4 ? kSegment : t.slabs) {
+          fine = wait();
+          if (!fine) break;
+          write_half<T, kind, O>(p, t, tmem + buf * kTileN + lanes, rank, w, half, lane, rows_out + half * kRows * kHalfM,
+                                 p.accumulate || k > 0);
+          release();
         }
+        if (!fine) break;
         // Padding rows; wgrad: the gradient of an expert without rows.
         if (kind == kProdWgrad ? !has : t.last)
           zero_rows<T, kind, O>(p, t, rank, lane, (kind == kProdWgrad ? 0 : t.cnt - t.r0) + warp - 4,
