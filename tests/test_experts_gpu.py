@@ -204,10 +204,10 @@ def test_wgrad(ep, shape, dtype, wtype, accumulate):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_long_float32_gradients_keep_their_precision(ep, dtype, accumulate):
     """Weight gradients over thousands of rows in float32, against the norm of
-    the result.  The tensor core truncates: 32 accumulations (512 rows) of at
-    most 2^-23 each before a sum is added to a float32 that rounds to nearest,
-    at most 2^-24 for each of the 40 segments here: 6.2e-6.  (Truncated all the
-    way, 20,000 rows would be off by 2e-5.)"""
+    the result.  The tensor core truncates: 20,000 rows in one sum would be
+    off by 2e-5.  The tolerance is that of sums of 512 rows (32 accumulations,
+    at most 2^-23 each), the 40 of them added in float32 with rounding to
+    nearest (at most 2^-24 each): 6.2e-6."""
     s = Step(ep, 3, 1, 24000, 1, dtype, 13, p_mask=0.0, idx=(torch.arange(24000) % 12).clamp(max=2).view(-1, 1))
     assert s.counts == [2000, 2000, 20000]
     dy, x = s.rows(72, 71), s.rows(136, 72)
