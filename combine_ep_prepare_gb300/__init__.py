@@ -6,8 +6,11 @@ GB300, as hand-written sm_103a CUDA kernels behind a C ABI (libep).
     h = ep.alloc_handle(lid, size)
     ep.ep_prepare(h, topk_idx, token_counts, alignment)
     ep.ep_dispatch(h, topk_idx, tokens, topk_weights, recv_tokens, recv_topk_weights)
-    ... grouped expert GEMMs on recv_tokens ...
-    ep.ep_combine(h, expert_out, result)
+    ep.ep_expert_gemm_swiglu(h, recv_tokens, w13, act)
+    ep.ep_expert_gemm(h, act, w2, expert_out)
+    ep.ep_combine_weighted(h, expert_out, recv_topk_weights, result)
+
+``moe_layer`` runs a whole layer on these calls.
 
 The binding (``_libep``) is loaded on first use of an ``ep_*`` name, and
 raises ImportError when libep.so has not been built: there is no CPU path.

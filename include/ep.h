@@ -463,7 +463,7 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t handle, const void* const* gr
  * Experts.  A single-buffer layer's E experts, or a sharded layer's own E/N
  * (a rank-major layer is refused: use the owner's single-buffer layer).  With
  * c_e, p_e and off_e of the handle's last prepare, expert e's rows are
- * [off_e, off_e + c_e).  Only those are read.  Row outputs are written in
+ * [off_e, off_e + c_e).  Only those enter a result.  Row outputs are written in
  * [off_e, off_e + p_e), zeros in the padding rows whatever the inputs hold
  * there; rows from P on are left alone.  On a handle without a prepare, or
  * after one that overflowed (or, sharded, disagreed with the gathered
@@ -472,7 +472,9 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t handle, const void* const* gr
  *
  * Types.  Row buffers (R rows), weights and row outputs hold the layer's
  * payload type.  Sums are float32, rounded once at the end, so the activation
- * is applied to unrounded sums.  Feature counts are multiples of 8 up to 2^20
+ * is applied to unrounded sums; the tensor cores truncate as they add, which
+ * leaves a float32 weight gradient within 1e-6 of its norm (random rows, any
+ * number of them).  Feature counts are multiples of 8 up to 2^20
  * and need not match the layer's hidden.  Pointers are 16-byte aligned;
  * outputs must not overlap inputs.  The order of a sum is fixed by the sizes
  * and the counts: the same inputs give the same bits.
@@ -480,6 +482,9 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t handle, const void* const* gr
  * Weights are [E][out_features][in_features], row-major.  A gated layer keeps
  * its two input matrices in one [E][2*ffn_features][in_features]: gate rows
  * first, then up rows; act = silu(gate) * up.
+ *
+ * Like the others these calls can be captured in a CUDA graph; make the first
+ * call of each on a device before any capture (it sets up the kernel).
  *
  * bf16 and fp16 products run on the tensor cores.  Their waits on copies and
  * on the tensor core are bounded: one that runs out ends the kernel, leaves
