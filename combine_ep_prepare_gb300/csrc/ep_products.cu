@@ -6,28 +6,31 @@
 //   dgrad     out[r][k] = sum_n a[r][n] w[e][n][k]
 //   wgrad     out[e][n][k] (+)= sum_r a[r][n] b[r][k]
 // with the gated activation silu(gate) * up, or its derivative, applied to the
-// sums.  Sums are float32 fused multiply-adds in ascending order of the
-// reduction.
+// sums.  Sums are float32 fused multiply-adds, two chains in ascending order of
+// the reduction (elements 0 to 7 and 8 to 15 of every 16) added at the end.
 #include "ep_experts.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kPad = 4;  // shared-memory row padding against bank conflicts
+// Output tiles of 64 x 64, 8 x 8 sums per thread, 16 reduction elements at a
+// time, of which each of two groups of 64 threads multiplies eight.  What
+// bounds the kernel is the shared memory's reads, four of 16 bytes for the 64
+// multiply-adds of a thread and reduction element: 8,192 rows x 2048 -> 2 x
+// 1024 take 1.56 ms, 44 of the CUDA cores' 80 TFLOP/s.  Larger tiles save no
+// such reads.  128 x 128 by one group of 256 threads took the same there, but
+// leaves SMs without work where tiles are few (2,500 rows of 8 experts, 1024
+// -> 1024: 206 us for 137; one token's two rows: 98 for 38) and multiplies more
+// padding where experts have few rows (64 experts x 25 rows: 365 for 216).
+// 16 x 8 sums per thread read a quarter less and leave two warps per
+// scheduler, too few for the loads' latency (1.72 ms).
+constexpr int kTile = 64, kHalf = kTile / 2;
+constexpr int kGroup = (kTile / 8) * (kTile / 8), kThreads = 2 * kGroup;
+constexpr int kStep = 16;
+constexpr int kPerSm = 4;  // blocks that the registers leave room for
+constexpr int kPad = 4;    // shared-memory row padding against bank conflicts
+static_assert(kTile * kStep == 8 * kThreads, "a thread moves eight elements of each operand per step");
 
-// Output tiles of TILE x TILE, 8 x 8 sums per thread, STEP reduction elements
-// at a time: a thread moves eight elements of each operand per step.
-template <int TILE>
-struct Shape {
-  static constexpr int kThreads = (TILE / 8) * (TILE / 8);
-  static constexpr int kStep = kThreads * 8 / TILE;
-  using Row = float[TILE + kPad];
-};
-
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  *reinterpret_cast<float4*>(v) = reinterpret_cast<const float4*>(p)[0];
-  *reinterpret_cast<float4*>(v + 4) = reinterpret_cast<const float4*>(p)[1];
-}
 __device__ __forceinline__ void store4(float* p, const float* v) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -39,44 +42,46 @@ __device__ __forceinline__ void fma2(float2* c, const float2& a, const float2& b
       : "l"(*reinterpret_cast<const unsigned long long*>(&a)), "l"(*reinterpret_cast<const unsigned long long*>(&b)));
 }
 
-// One operand's share of a step.  kc: the reduction index is the contiguous one.
-template <int TILE, bool kc>
+// One operand's share of a step: two runs of four elements, half of a
+// contiguous row apart, so that the lanes of a warp write to different banks.
+// kc: the reduction index is the contiguous one.
+template <bool kc>
 struct Slab {
-  static constexpr int kParts = kc ? Shape<TILE>::kStep / 8 : TILE / 8;  // runs of eight in a contiguous row
-  float v[8];
-  static __device__ __forceinline__ int mn() { return kc ? threadIdx.x / kParts : threadIdx.x % kParts * 8; }
-  static __device__ __forceinline__ int k() { return kc ? threadIdx.x % kParts * 8 : threadIdx.x / kParts; }
+  static constexpr int kRow = kc ? kStep : kTile;
+  static constexpr int kParts = kRow / 8;
+  alignas(16) float v[2][4];
+  static __device__ __forceinline__ int at(int c) { return c * (kRow / 2) + threadIdx.x % kParts * 4; }
+  static __device__ __forceinline__ int row() { return threadIdx.x / kParts; }
   // base: element (0, 0); ld: elements between rows; mn / k limits.
   __device__ __forceinline__ void load(const float* base, long long ld, int mn_lim, int k0, int k_lim) {
-    const int m = mn(), kk = k0 + k();
-    if (m < mn_lim && kk < k_lim) {
-      load8(kc ? base + m * ld + kk : base + kk * ld + m, v);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    for (int c = 0; c < 2; ++c) {
+      const int m = kc ? row() : at(c), k = k0 + (kc ? at(c) : row());
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (m < mn_lim && k < k_lim) x = *reinterpret_cast<const float4*>(kc ? base + m * ld + k : base + k * ld + m);
+      *reinterpret_cast<float4*>(v[c]) = x;
     }
   }
-  __device__ __forceinline__ void store(typename Shape<TILE>::Row* s) const {
-    if constexpr (kc) {
+  __device__ __forceinline__ void store(float (*s)[kTile + kPad]) const {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[k() + i][mn()] = v[i];
-    } else {
-      store4(&s[k()][mn()], v);
-      store4(&s[k()][mn() + 4], v + 4);
+    for (int c = 0; c < 2; ++c) {
+      if constexpr (kc) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[at(c) + i][row()] = v[c][i];
+      } else {
+        store4(&s[row()][at(c)], v[c]);
+      }
     }
   }
 };
 
-// A tile per block, rows and columns of a thread in two runs of four, TILE / 2
+// A tile per block, rows and columns of a thread in two runs of four, kHalf
 // apart, so that a warp's shared-memory reads of four floats do not collide;
 // the next step's loads are in flight while the present one is multiplied.  In
 // the gated forward one half of the tile's columns are gate columns and the
 // other the up columns of the same features, so that one thread holds both.
-// PER_SM: blocks per SM that the registers are to leave room for, 0 as the
-// compiler has it.
-template <int TILE, int PER_SM, int kind>
-__global__ void __launch_bounds__(Shape<TILE>::kThreads, PER_SM) ep_product_simt_kernel(const ProductParams p) {
-  constexpr int kThreads = Shape<TILE>::kThreads, kStep = Shape<TILE>::kStep, kTile = TILE, kHalf = TILE / 2;
+template <int kind>
+__global__ void __launch_bounds__(kThreads, kPerSm) ep_product_simt_kernel(const ProductParams p) {
   constexpr bool rows_out = kind != kProdWgrad;
   constexpr bool a_kc = rows_out;
   constexpr bool b_kc = kind == kProdFwd || kind == kProdFwdSwiglu;
@@ -86,11 +91,11 @@ __global__ void __launch_bounds__(Shape<TILE>::kThreads, PER_SM) ep_product_simt
   __shared__ int part[32];
   pdl_wait();
   if (!blocks_ok(p.hdr, p.R)) return;
-  const int t = threadIdx.x, tx = t % (TILE / 8), ty = t / (TILE / 8);
+  const int group = threadIdx.x / kGroup, t = threadIdx.x % kGroup, tx = t % (kTile / 8), ty = t / (kTile / 8);
   const float* a = static_cast<const float*>(p.a);
   const float* b = static_cast<const float*>(p.b);
   const int F = p.N / 2;
-  constexpr int cols_per_tile = kind == kProdFwdSwiglu ? kTile / 2 : kTile;
+  constexpr int cols_per_tile = kind == kProdFwdSwiglu ? kHalf : kTile;
   const int cols = kind == kProdFwd ? p.N : kind == kProdFwdSwiglu ? F : p.K;
   const int ntiles = (cols + cols_per_tile - 1) / cols_per_tile;
   const int wrow_tiles = (p.N + kTile - 1) / kTile;  // wgrad
@@ -144,20 +149,20 @@ __global__ void __launch_bounds__(Shape<TILE>::kThreads, PER_SM) ep_product_simt
       b_lim = p.K - c0;
       red = cnt;
     }
-    alignas(8) float acc[8][8];
+    alignas(16) float acc[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
 
-    Slab<TILE, a_kc> la;
-    Slab<TILE, b_kc> lb;
+    Slab<a_kc> la;
+    Slab<b_kc> lb;
     auto load = [&](int k0) {
       la.load(ab, ald, a_lim, k0, red);
       if constexpr (kind == kProdFwdSwiglu) {
         // slab columns below kHalf: gate features from c0 on, the others: up features from c0 on
         const int lim = b_lim < kHalf ? b_lim : kHalf;
-        const bool up = lb.mn() >= kHalf;
+        const bool up = lb.row() >= kHalf;
         lb.load(bb + (up ? (static_cast<long long>(F) - kHalf) * bld : 0), bld, up ? kHalf + lim : lim, k0, red);
       } else {
         lb.load(bb, bld, b_lim, k0, red);
@@ -172,12 +177,14 @@ __global__ void __launch_bounds__(Shape<TILE>::kThreads, PER_SM) ep_product_simt
       for (int k0 = 0; k0 < red; k0 += kStep) {
         const bool more = k0 + kStep < red;
         if (more) load(k0 + kStep);
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          float ra[8];
+#pragma unroll 2
+        for (int ki = 0; ki < kStep / 2; ++ki) {
+          const int k = group * (kStep / 2) + ki;
+          alignas(16) float ra[8];
           alignas(16) float2 rb[4];
-          *reinterpret_cast<float4*>(ra) = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 4]);
-          *reinterpret_cast<float4*>(ra + 4) = *reinterpret_cast<const float4*>(&sa[buf][k][kHalf + ty * 4]);
+#pragma unroll
+          for (int i = 0; i < 8; i += 4)
+            *reinterpret_cast<float4*>(ra + i) = *reinterpret_cast<const float4*>(&sa[buf][k][i / 4 * kHalf + ty * 4]);
           *reinterpret_cast<float4*>(rb) = *reinterpret_cast<const float4*>(&sb[buf][k][tx * 4]);
           *reinterpret_cast<float4*>(rb + 2) = *reinterpret_cast<const float4*>(&sb[buf][k][kHalf + tx * 4]);
 #pragma unroll
@@ -193,14 +200,40 @@ __global__ void __launch_bounds__(Shape<TILE>::kThreads, PER_SM) ep_product_simt
         buf ^= 1;
       }
     }
-    // Epilogue: rows m0 + {0, kHalf} + 4 ty + i.  A padding row's sums are +0
-    // (its operand was not read), so it gets zeros without a case of its own,
-    // except through the activation's derivative, which reads `pre`.
+    // The groups' sums are added, group 0's first: group 0 finishes the rows of
+    // i < 4 (in acc[0..3]), group 1 the others.
+    static_assert(sizeof(sa) >= kGroup * 32 * sizeof(float), "half of a group's sums have room");
+    float4* sums = reinterpret_cast<float4*>(&sa[0][0][0]);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (group != g) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[i * kGroup + t] = reinterpret_cast<float4*>(acc[g * 4])[i];
+      }
+      __syncthreads();
+      if (group == g) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 o = sums[i * kGroup + t];
+          const float* mine = &acc[g * 4 + (i >> 1)][(i & 1) * 4];
+          float* v = &acc[i >> 1][(i & 1) * 4];
+          v[0] = mine[0] + o.x, v[1] = mine[1] + o.y, v[2] = mine[2] + o.z, v[3] = mine[3] + o.w;
+        }
+      }
+      __syncthreads();
+    }
+    // Epilogue: rows m0 + kHalf group + 4 ty + i.  A padding row's operand was
+    // not read but taken as zero, which an infinite weight makes NaN: its sums
+    // are set to zero.
     const int m_lim = rows_out ? rows - m0 : p.N - m0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int m = (i >> 2) * kHalf + ty * 4 + (i & 3);
+    for (int i = 0; i < 4; ++i) {
+      const int m = group * kHalf + ty * 4 + i;
       if (m >= m_lim) continue;
+      if (rows_out && m0 + m >= cnt) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+      }
       if constexpr (kind == kProdFwdSwiglu) {
         const int f = c0 + tx * 4;
         if (f >= F) continue;
@@ -251,32 +284,17 @@ __global__ void __launch_bounds__(Shape<TILE>::kThreads, PER_SM) ep_product_simt
   }
 }
 
-template <int TILE, int PER_SM>
-cudaError_t launch_tile(const ProductParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid(2 * num_sms), block(Shape<TILE>::kThreads);
-  switch (p.kind) {
-    case kProdFwd: return launch_pdl(ep_product_simt_kernel<TILE, PER_SM, kProdFwd>, grid, block, 0, s, 0, p);
-    case kProdFwdSwiglu: return launch_pdl(ep_product_simt_kernel<TILE, PER_SM, kProdFwdSwiglu>, grid, block, 0, s, 0, p);
-    case kProdDgrad: return launch_pdl(ep_product_simt_kernel<TILE, PER_SM, kProdDgrad>, grid, block, 0, s, 0, p);
-    default: return launch_pdl(ep_product_simt_kernel<TILE, PER_SM, kProdDgradSwiglu>, grid, block, 0, s, 0, p);
-  }
-}
-
 }  // namespace
 
-// Tiles of 128 x 128 read least.  Two blocks per SM hide each other's
-// latencies (dgrad of 8 x 1,024 rows x 2 x 1024 -> 2048 1.73 -> 1.42 ms), but
-// with hardly a tile per SM the device puts pairs of them on some SMs and none
-// on others (2,000 rows x 1024 -> 1024, 160 tiles: 105 -> 193 us), hence one
-// where the buffer's capacity of rows makes fewer than three tiles per SM.
-// wgrad, whose operands both lie along the tile's sides, takes 64 x 64 tiles:
-// 2.94 ms for 3.29 at 16 experts x 512 rows x 4096 x 2048.
 cudaError_t launch_product_simt(const ProductParams& p, int num_sms, cudaStream_t s) {
-  if (p.kind == kProdWgrad)
-    return launch_pdl(ep_product_simt_kernel<64, 8, kProdWgrad>, dim3(8 * num_sms), dim3(Shape<64>::kThreads), 0, s, 0, p);
-  const long long cols = p.kind == kProdFwd || p.kind == kProdFwdSwiglu ? p.N : p.K;
-  const long long tiles = (p.R / 128 + (p.E < p.R ? p.E : p.R)) * ((cols + 127) / 128);
-  return tiles < 3ll * num_sms ? launch_tile<128, 0>(p, num_sms, s) : launch_tile<128, 2>(p, num_sms, s);
+  const dim3 grid(kPerSm * num_sms), block(kThreads);
+  switch (p.kind) {
+    case kProdFwd: return launch_pdl(ep_product_simt_kernel<kProdFwd>, grid, block, 0, s, 0, p);
+    case kProdFwdSwiglu: return launch_pdl(ep_product_simt_kernel<kProdFwdSwiglu>, grid, block, 0, s, 0, p);
+    case kProdDgrad: return launch_pdl(ep_product_simt_kernel<kProdDgrad>, grid, block, 0, s, 0, p);
+    case kProdDgradSwiglu: return launch_pdl(ep_product_simt_kernel<kProdDgradSwiglu>, grid, block, 0, s, 0, p);
+    default: return launch_pdl(ep_product_simt_kernel<kProdWgrad>, grid, block, 0, s, 0, p);
+  }
 }
 
 }  // namespace ep

@@ -286,6 +286,31 @@ def test_nan_and_infinity_stay_with_their_expert(ep, dtype):
         assert bool(torch.isfinite(dw[e]).all()) != bad
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")], ids=["inf", "nan"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_padding_rows_are_zero_whatever_the_weights_hold(ep, dtype, value):
+    """0 * inf is NaN, so a padding row must not be what a product with its zeros gives."""
+    s = Step(ep, 5, 2, 70, 100, dtype, 81)
+    x, dy = s.rows(96, 82), s.rows(160, 83)
+    w, w13 = s.weights(160, 96, 84), s.weights(144, 96, 85)
+    w[:, 3, 5], w13[:, 7, 9], w13[:, 80, 11] = value, value, value
+    y, act, dx, dpre = s.out(160), s.out(72), s.out(96), s.out(192)
+    ep.ep_expert_gemm(s.h, x, w, y)
+    ep.ep_expert_gemm_swiglu(s.h, x, w13, act)
+    ep.ep_expert_dgrad(s.h, dy, w, dx)
+    ep.ep_expert_dgrad_swiglu(s.h, dy, w, s.rows(192, 86), dpre)
+    outs = [y, act, dx, dpre]
+    if dtype != "fp32":
+        wq, scales, _ = w4_weights(s, 80, 96, 32, 87)
+        scales[:, 2, 1] = value
+        outs.append(s.out(80))
+        ep.ep_expert_gemv_w4(s.h, x, wq, scales, outs[-1])
+    assert bool(s.pad.any())
+    for o in outs:
+        assert bool((o.cpu()[s.pad] == 0).all())
+        assert is_sentinel(o[s.P:])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_same_inputs_same_bits_and_other_stream(ep, dtype):
     s = Step(ep, 8, 2, 300, 16, dtype, 9)
