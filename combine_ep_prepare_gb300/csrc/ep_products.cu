@@ -7,7 +7,8 @@
 //   wgrad     out[e][n][k] (+)= sum_r a[r][n] b[r][k]
 // with the gated activation silu(gate) * up, or its derivative, applied to the
 // sums.  Sums are float32 fused multiply-adds, two chains in ascending order of
-// the reduction (elements 0 to 7 and 8 to 15 of every 16) added at the end.
+// the reduction (elements 0 to 7 and 8 to 15 of every 16) added at the end; in
+// tiles of eight rows or fewer, a chain per lane or thread and a tree.
 #include "ep_experts.cuh"
 
 namespace ep {
@@ -17,10 +18,10 @@ namespace {
 // time, of which each of two groups of 64 threads multiplies eight.  What
 // bounds the kernel is the shared memory's reads, four of 16 bytes for the 64
 // multiply-adds of a thread and reduction element: 8,192 rows x 2048 -> 2 x
-// 1024 take 1.56 ms, 44 of the CUDA cores' 80 TFLOP/s.  Larger tiles save no
+// 1024 take 1.59 ms, 43 of the CUDA cores' 80 TFLOP/s.  Larger tiles save no
 // such reads.  128 x 128 by one group of 256 threads took the same there, but
 // leaves SMs without work where tiles are few (2,500 rows of 8 experts, 1024
-// -> 1024: 206 us for 137; one token's two rows: 98 for 38) and multiplies more
+// -> 1024: 206 us for 137; 800 rows of 4: 106 for 63) and multiplies more
 // padding where experts have few rows (64 experts x 25 rows: 365 for 216).
 // 16 x 8 sums per thread read a quarter less and leave two warps per
 // scheduler, too few for the loads' latency (1.72 ms).
@@ -74,6 +75,93 @@ struct Slab {
     }
   }
 };
+
+// Tiles of a few rows are bound by the weights' bytes: their blocks read the
+// weights as they lie, straight into registers, and keep no operand in shared
+// memory.  16 tokens' top 2 of 32 experts, 1024 -> 4096: 139 us for 333 by the
+// way of full tiles; one token's top 2 of 8, 1024 -> 1024: 12.5 for 38.  Eight
+// rows by four columns are the sums that a thread has registers for beside the
+// loads.  wgrad is not treated so: sums straight from global memory gained 11%
+// with two rows to each expert and cost 2% with 512.  Sums go to
+// part[..][row][column].
+constexpr int kThin = 8;
+using Thin = float[kThin][kTile];
+
+// Four columns at a time per warp, the lanes along the reduction.  column(c):
+// the weights of the tile's column c, or nullptr.
+template <class Column>
+__device__ __forceinline__ void thin_along(const float* a, long long ald, int rows, int red, Column column, Thin& part) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (int c = warp * (kTile / 4); c < (warp + 1) * (kTile / 4); c += 4) {
+    const float* w = column(c);
+    if (w == nullptr) continue;
+    const long long ld = column(c + 1) - w;
+    float s[4 * kThin];  // [column][row]
+#pragma unroll
+    for (int i = 0; i < 4 * kThin; ++i) s[i] = 0.0f;
+#pragma unroll 1
+    for (int k = lane * 4; k < red; k += 128) {
+      float4 b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(w + j * ld + k);
+#pragma unroll
+      for (int r = 0; r < kThin; ++r) {
+        if (r < rows) {
+          const float4 x = *reinterpret_cast<const float4*>(a + r * ald + k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[j * kThin + r] = fmaf(x.w, b[j].w, fmaf(x.z, b[j].z, fmaf(x.y, b[j].y, fmaf(x.x, b[j].x, s[j * kThin + r]))));
+        }
+      }
+    }
+    // Lanes trade halves of what they hold until lane i has the whole sum i.
+#pragma unroll
+    for (int h = 2 * kThin; h > 0; h /= 2) {
+#pragma unroll
+      for (int i = 0; i < h; ++i) {
+        const float keep = lane & h ? s[i + h] : s[i], give = lane & h ? s[i] : s[i + h];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
+      }
+    }
+    part[lane % kThin][c + lane / kThin] = s[0];
+  }
+}
+
+// Four columns per thread, eight threads of each four along the reduction,
+// four elements at a time; the sums of a warp's two are added here.
+__device__ __forceinline__ void thin_across(const float* a, long long ald, int rows, const float* b, long long bld, int cols, int red,
+                                            Thin* part) {
+  const int lane = threadIdx.x % 32, c = threadIdx.x % 16 * 4;
+  float s[kThin][4];
+#pragma unroll
+  for (int r = 0; r < kThin; ++r)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[r][j] = 0.0f;
+  if (c < cols) {
+#pragma unroll 1
+    for (int k = threadIdx.x / 16 * 4; k < red; k += kThreads / 4) {
+      float4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(b + (k + i) * bld + c);
+#pragma unroll
+      for (int r = 0; r < kThin; ++r) {
+        if (r < rows) {
+          const float4 x = *reinterpret_cast<const float4*>(a + r * ald + k);
+          s[r][0] = fmaf(x.w, w[3].x, fmaf(x.z, w[2].x, fmaf(x.y, w[1].x, fmaf(x.x, w[0].x, s[r][0]))));
+          s[r][1] = fmaf(x.w, w[3].y, fmaf(x.z, w[2].y, fmaf(x.y, w[1].y, fmaf(x.x, w[0].y, s[r][1]))));
+          s[r][2] = fmaf(x.w, w[3].z, fmaf(x.z, w[2].z, fmaf(x.y, w[1].z, fmaf(x.x, w[0].z, s[r][2]))));
+          s[r][3] = fmaf(x.w, w[3].w, fmaf(x.z, w[2].w, fmaf(x.y, w[1].w, fmaf(x.x, w[0].w, s[r][3]))));
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kThin; ++r) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[r][j] += __shfl_xor_sync(0xffffffffu, s[r][j], 16);
+    if (lane < 16) store4(&part[threadIdx.x / 32][r][c], s[r]);
+  }
+}
 
 // A tile per block, rows and columns of a thread in two runs of four, kHalf
 // apart, so that a warp's shared-memory reads of four floats do not collide;
@@ -149,6 +237,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm) ep_product_simt_kernel(const
       b_lim = p.K - c0;
       red = cnt;
     }
+    const bool thin = rows_out && a_lim > 0 && a_lim <= kThin;
+    constexpr int parts = b_kc ? 1 : kThreads / 32;
+    static_assert(sizeof(sa) >= parts * sizeof(Thin), "the parts have room");
+    Thin* part = reinterpret_cast<Thin*>(&sa[0][0][0]);
+    if (thin) {
+      if constexpr (b_kc) {
+        thin_along(ab, ald, a_lim, red, [&](int c) -> const float* {
+          const bool up = kind == kProdFwdSwiglu && c >= kHalf;
+          const int in = up ? c - kHalf : c;
+          if (in >= (kind == kProdFwdSwiglu && b_lim > kHalf ? kHalf : b_lim)) return nullptr;
+          return bb + (static_cast<long long>(in) + (up ? F : 0)) * bld;
+        }, part[0]);
+      } else {
+        thin_across(ab, ald, a_lim, bb, bld, b_lim, red, part);
+      }
+      __syncthreads();
+    }
     alignas(16) float acc[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -168,7 +273,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm) ep_product_simt_kernel(const
         lb.load(bb, bld, b_lim, k0, red);
       }
     };
-    if (a_lim > 0 && red > 0) {
+    if (thin) {
+      if (group == 0 && ty * 4 < a_lim) {
+        for (int w = 0; w < parts; ++w) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] += part[w][ty * 4 + i][(j >> 2) * kHalf + tx * 4 + (j & 3)];
+        }
+      }
+    } else if (a_lim > 0 && red > 0) {
       load(0);
       la.store(sa[0]);
       lb.store(sb[0]);
@@ -204,23 +318,25 @@ __global__ void __launch_bounds__(kThreads, kPerSm) ep_product_simt_kernel(const
     // i < 4 (in acc[0..3]), group 1 the others.
     static_assert(sizeof(sa) >= kGroup * 32 * sizeof(float), "half of a group's sums have room");
     float4* sums = reinterpret_cast<float4*>(&sa[0][0][0]);
+    if (!thin) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (group != g) {
+      for (int g = 0; g < 2; ++g) {
+        if (group != g) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sums[i * kGroup + t] = reinterpret_cast<float4*>(acc[g * 4])[i];
-      }
-      __syncthreads();
-      if (group == g) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 o = sums[i * kGroup + t];
-          const float* mine = &acc[g * 4 + (i >> 1)][(i & 1) * 4];
-          float* v = &acc[i >> 1][(i & 1) * 4];
-          v[0] = mine[0] + o.x, v[1] = mine[1] + o.y, v[2] = mine[2] + o.z, v[3] = mine[3] + o.w;
+          for (int i = 0; i < 8; ++i) sums[i * kGroup + t] = reinterpret_cast<float4*>(acc[g * 4])[i];
         }
+        __syncthreads();
+        if (group == g) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 o = sums[i * kGroup + t];
+            const float* mine = &acc[g * 4 + (i >> 1)][(i & 1) * 4];
+            float* v = &acc[i >> 1][(i & 1) * 4];
+            v[0] = mine[0] + o.x, v[1] = mine[1] + o.y, v[2] = mine[2] + o.z, v[3] = mine[3] + o.w;
+          }
+        }
+        __syncthreads();
       }
-      __syncthreads();
     }
     // Epilogue: rows m0 + kHalf group + 4 ty + i.  A padding row's operand was
     // not read but taken as zero, which an infinite weight makes NaN: its sums
