@@ -262,6 +262,7 @@ struct Consumer {
       for (int i = 0; i < kGroups / 2; ++i) reinterpret_cast<uint32_t*>(scales + lane * 16)[i] = next[i];
       if (it + 1 < iters) load_scales();
       if (!__all_sync(0xffffffffu, tc::mbar_wait(tc::smem_addr(&s.full[stage]), phase, &s.gave_up))) return false;
+      __syncwarp();  // the scales of all lanes are there: a vote orders no memory
       const unsigned char* words = smem + stage * kStageBytes + word_at;
       const unsigned char* slab = smem + stage * kStageBytes + kWBytes + sub * NT * kSlabBytes + g * (kChunk * 2);
 #pragma unroll
