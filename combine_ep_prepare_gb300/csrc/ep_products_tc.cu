@@ -541,13 +541,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t d = tmem + buf * kTileN;
             const int k1 = min(t.slabs, k0 + segment);
             for (int k = k0; k < k1; ++k) {
-              lost = !tc::mbar_wait(tc::smem_addr(&s.full[stage]), phase, gave_up);
+              const int left = kind == kProdWgrad ? t.cnt - k * kSlab : kSlab;
+              // A slab with zeroed rows was handed over by threads of both blocks.
+              lost = left < kSlab && (left & 15) ? !tc::mbar_wait<true>(tc::smem_addr(&s.full[stage]), phase, gave_up)
+                                                 : !tc::mbar_wait(tc::smem_addr(&s.full[stage]), phase, gave_up);
               if (lost) break;
               tc::fence_after();
               const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * (kABytes + kBBytes)), b = a + kABytes;
               const uint64_t da = a_mn ? tc::desc_mn_major(a, kBoxBytes) : tc::desc_k_major(a);
               const uint64_t db = b_mn ? tc::desc_mn_major(b, kBoxBytes) : tc::desc_k_major(b);
-              const int left = kind == kProdWgrad ? t.cnt - k * kSlab : kSlab;
 #pragma unroll
               for (int q = 0; q < kSlab / 16; ++q)
                 if (q * 16 < left)
@@ -590,13 +592,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int chunks = (16 - (left & 15)) * 8, boxes = kHalfM / 64 + (t.n / 2 + 63) / 64;
         for (int j = lane; j < chunks * boxes; j += 32)
           *reinterpret_cast<uint4*>(slab + j / chunks * kBoxBytes + left * 128 + j % chunks * 16) = make_uint4(0, 0, 0, 0);
-        // The fence hands each lane's zeros to the asynchronous proxy, in which
-        // this SM's tensor core reads them; the arrival then only has to come
-        // after it.  (An arrival with a release for the whole cluster cost 20%
-        // of wgrad's time: 484 us for 404 at 128 experts x 500 rows.)
+        // Each lane's fence orders its zeros before the asynchronous proxy's
+        // reads; the arrival hands them to the thread that issues the mma, in
+        // the second block with a release for the cluster.  (That release and
+        // its acquire cost 71 us of 483 at 128 experts x 500 rows, where every
+        // tile has such a slab: 512 rows take 412.)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(tc::in_block(tc::smem_addr(&s.full[at]), 0));
+        if (lane == 0) {
+          if (rank == 0) tc::mbar_arrive(tc::smem_addr(&s.full[at]));
+          else tc::mbar_publish_cluster(tc::in_block(tc::smem_addr(&s.full[at]), 0));
+        }
       }
     } else if (warp >= 4) {
       int buf = 0;

@@ -37,9 +37,15 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
-// An arrival on a barrier of any block of the cluster.
+// An arrival on a barrier of any block of the cluster.  It hands no memory
+// over: what comes before it is ordered within this block alone.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same, releasing this thread's earlier writes, and those it has observed,
+// to the cluster; a wait with mbar_wait_cluster acquires them.
+__device__ __forceinline__ void mbar_publish_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_init_fence() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -50,15 +56,26 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+template <bool cluster = false>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (cluster) {
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  }
   return done != 0;
 }
 __device__ __forceinline__ unsigned long long now_ns() {
@@ -69,12 +86,14 @@ __device__ __forceinline__ unsigned long long now_ns() {
 
 // A wait ends when the phase does, when another thread of the block has given
 // up, or after kWaitNs: false then, and the block's give-up flag is set.
+// cluster: it acquires what threads of the cluster's other blocks published.
 constexpr unsigned long long kWaitNs = 2000000000ull;
+template <bool cluster = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (mbar_try(bar, parity)) return true;
+  if (mbar_try<cluster>(bar, parity)) return true;
   unsigned long long start = 0;
   for (unsigned i = 0;; ++i) {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try<cluster>(bar, parity)) return true;
     if ((i & 63u) == 63u) {
       if (*gave_up) return false;
       const unsigned long long t = now_ns();
