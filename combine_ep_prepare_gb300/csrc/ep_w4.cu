@@ -435,14 +435,6 @@ __global__ void __launch_bounds__(kThreads, 2) ep_w4_kernel(const __grid_constan
           }
         }
       }
-      if (*gave_up) {
-        // The copies in flight land before the block's shared memory goes; a
-        // copy takes microseconds.
-        const unsigned long long start = tc::now_ns();
-        while (tc::now_ns() - start < tc::kWaitNs / 100) {
-        }
-        atomicOr(&p.hdr[kHdrStatus], static_cast<int>(EP_ST_TIMEOUT));
-      }
     }
   } else {
     Consumer<T, G, gated> c{p, s, chunks, warp, lane, 0, 0};
@@ -458,6 +450,16 @@ __global__ void __launch_bounds__(kThreads, 2) ep_w4_kernel(const __grid_constan
         break;
       }
     }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && s.gave_up) {
+    // Whoever gave up, the loading warp may have left before: the copies in
+    // flight land before the block's shared memory goes; a copy takes
+    // microseconds.
+    const unsigned long long start = tc::now_ns();
+    while (tc::now_ns() - start < tc::kWaitNs / 100) {
+    }
+    atomicOr(&p.hdr[kHdrStatus], static_cast<int>(EP_ST_TIMEOUT));
   }
 }
 
