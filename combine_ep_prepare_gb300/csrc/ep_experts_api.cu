@@ -128,7 +128,7 @@ ep_status_t router_params(const ep_router_config_t& c, int64_t T, const void* lo
   if (c.dtype != EP_DTYPE_BF16 && c.dtype != EP_DTYPE_FP16 && c.dtype != EP_DTYPE_FP32)
     return fail(EP_ERR_INVALID_ARG, "%s %lld is not an ep_dtype_t", "dtype", (long long)c.dtype);
   if (!std::isfinite(c.scale)) return fail(EP_ERR_INVALID_ARG, "%s is not finite", "scale");
-  if (T < 0 || T * c.top_k > (1LL << 24))
+  if (T < 0 || T > (1LL << 24) / c.top_k)
     return fail(EP_ERR_SHAPE, "%s %lld: num_tokens*top_k must lie in [0, 2^24]", "num_tokens", (long long)T);
   if (T > 0) {
     const ep_status_t st = check_ptr(logits, "logits", c.dtype == EP_DTYPE_FP32 ? 4 : 2);
