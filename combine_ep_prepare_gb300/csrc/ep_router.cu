@@ -234,11 +234,15 @@ __global__ void __launch_bounds__(kWarps * 32) ep_router_kernel(const RouterPara
 }
 
 // d loss / d logits, the choice held fixed.  With s_k the chosen scores, S
-// their sum and g the gradient of the weights (times `scale`):
-//   sigmoid              ds_k = g_k                 (dz = ds s (1 - s))
-//   sigmoid, normalised  ds_k = (g_k - sum g s / S) / S
+// their sum, w_k = s_k / S the normalised ones and g the gradient of the
+// weights (times `scale`):
+//   sigmoid              dz_k = s_k (1 - s_k) g_k
+//   sigmoid, normalised  dz_k = w_k (1 - s_k) (g_k - sum g w)
 //   softmax, normalised  dz_k = w_k (g_k - sum g w)
 //   softmax              dz_e = p_e ([e chosen] g_e - sum_k g_k p_k), every e
+// 1 - s is the sigmoid of -z: the difference would lose its digits from z = 8
+// on and be 0 from 17 on.  Dividing s by S before anything else keeps the
+// quotients of very small scores in range.
 // The row is written once densely and the K chosen entries after it: bound by
 // the write of [T][E].
 template <typename T, int J>
@@ -256,13 +260,13 @@ __global__ void __launch_bounds__(kWarps * 32) ep_router_bwd_kernel(const Router
   float d;
   if (p.sigmoid || p.normalize) {
     if (p.sigmoid) {
-      const float s = e >= 0 ? sigmoidf(ze) : 0.0f;
-      float ds = g;
+      float w = e >= 0 ? sigmoidf(ze) : 0.0f, inner = 0.0f;
       if (p.normalize) {
-        const float S = warp_sum(s), gs = warp_sum(g * s);
-        ds = S > 0.0f ? (g - gs / S) / S : 0.0f;
+        const float S = warp_sum(w);
+        w = S > 0.0f ? w / S : 0.0f;
+        inner = warp_sum(g * w);
       }
-      d = ds * s * (1.0f - s);
+      d = w * sigmoidf(-ze) * (g - inner);
     } else {
       const unsigned m = __reduce_max_sync(kAll, key_of(ze));
       const float x = exp_or_0(ze, m ? value_of(m) : 0.0f);
