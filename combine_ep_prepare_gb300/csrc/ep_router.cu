@@ -45,7 +45,9 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// exp(z - m), 0 where the logit cannot be chosen.
+// exp(z - m), 0 where the logit cannot be chosen.  A largest logit of +inf
+// makes this NaN, the sum over it and so all weights of the row: a sum is
+// compared with 0 alone, which only a row without a choice has.
 __device__ __forceinline__ float exp_or_0(float z, float m) { return z > -INFINITY ? expf(z - m) : 0.0f; }
 
 // This lane's J logits from expert lane J on; -inf past the last.
@@ -223,9 +225,9 @@ __global__ void __launch_bounds__(kWarps * 32) ep_router_kernel(const RouterPara
     const float m = __shfl_sync(kAll, zk, 0);  // the first choice has the largest logit
     w = exp_or_0(zk, m);
     const float total = warp_sum(w);
-    w = total > 0.0f ? w / total : 0.0f;
+    w = total != 0.0f ? w / total : 0.0f;
   } else {
-    w = exp_or_0(zk, zmax) / (zsum > 0.0f ? zsum : 1.0f);
+    w = exp_or_0(zk, zmax) / (zsum != 0.0f ? zsum : 1.0f);
   }
   if (lane < p.K) {
     p.idx[static_cast<long long>(t) * p.K + lane] = mine;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kWarps * 32) ep_router_bwd_kernel(const Router
       const unsigned m = __reduce_max_sync(kAll, key_of(ze));
       const float x = exp_or_0(ze, m ? value_of(m) : 0.0f);
       const float S = warp_sum(x);
-      const float w = S > 0.0f ? x / S : 0.0f;
+      const float w = S != 0.0f ? x / S : 0.0f;
       d = w * (g - warp_sum(g * w));
     }
     constexpr int kVec = 16 / sizeof(T);
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32) ep_router_bwd_kernel(const Router
       s += z[j];
     }
     s = warp_sum(s);
-    const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+    const float inv = s != 0.0f ? 1.0f / s : 0.0f;
     const float pe = exp_or_0(ze, zmax) * inv;
     const float inner = warp_sum(g * pe);
     d = pe * (g - inner);

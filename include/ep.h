@@ -557,7 +557,8 @@ ep_status_t ep_expert_gemv_w4_swiglu(ep_handle_t handle, const void* x, const ui
  * Weights: the chosen experts' scores (softmax over all logits that can be
  * chosen, whether their group stayed or not; or sigmoid), with normalize = 1
  * divided by their sum (0 where that sum is 0), times scale.  All arithmetic
- * is float32.
+ * is float32.  A logit of +infinity is chosen like any other; the softmax of
+ * its row is NaN, weights and gradient.
  * ------------------------------------------------------------------------ */
 typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t;
 

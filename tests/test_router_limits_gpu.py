@@ -44,3 +44,22 @@ def test_sigmoid_gradient_of_confident_logits(ep, low, high, size, normalize, dt
     bound = (K + 16) * 2.0 ** -23 * size + UNIT[dtype] * want.abs() + TINY[dtype]
     d = (got - want).abs()
     assert bool((d <= bound).all()), (d / bound).max().item()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("normalize", [True, False])
+def test_an_infinite_logit_shows_in_its_row_alone(ep, normalize, dtype):  # noqa: F811
+    """exp(inf - inf): the softmax of a row with +infinity is NaN, not a set of
+    zero weights that would drop the token unseen."""
+    T, E, K = 9, 40, 5
+    z = torch.randn(T, E, generator=torch.Generator().manual_seed(22)).to(TYPES[dtype])
+    z[4, 17] = float("inf")
+    z = z.cuda()
+    idx, w = torch.empty(T, K, dtype=torch.int64, device="cuda"), torch.empty(T, K, device="cuda")
+    ep.ep_router(z, idx, w, normalize=normalize)
+    assert idx[4, 0].item() == 17 and bool((idx >= 0).all())
+    gz = torch.zeros_like(z)
+    ep.ep_router_bwd(z, idx, torch.ones_like(w), gz, normalize=normalize)
+    row = torch.arange(T, device="cuda") == 4
+    assert bool(torch.isnan(w[row]).all()) and bool(torch.isfinite(w[~row]).all())
+    assert bool(torch.isnan(gz.gather(1, idx)[row]).all()) and bool(torch.isfinite(gz[~row]).all())
