@@ -63,9 +63,10 @@ class MoELayer:
         self.x: Optional[torch.Tensor] = None
 
     def _route(self, x, gate, bias):
-        """Router, routing map and dispatch of a batch."""
-        T = x.shape[0]
-        self.x, self.logits = x, x.float() @ gate.float().t()
+        """Router, routing map and dispatch of a batch.  The buffers are then no
+        longer those of an earlier forward."""
+        T, self.x = x.shape[0], None
+        self.logits = x.float() @ gate.float().t()
         self.t_idx, self.t_weights = self.idx[:T], self.weights[:T]
         ep.ep_router(self.logits, self.t_idx, self.t_weights, bias=bias, **self.routing)
         ep.ep_prepare(self.handle, self.t_idx, self.counts, self.alignment)
@@ -78,6 +79,7 @@ class MoELayer:
         ep.ep_expert_gemm(self.handle, self.act, w2, self.expert_out)
         out = torch.empty_like(x)
         ep.ep_combine_weighted(self.handle, self.expert_out, self.recv_weights, out)
+        self.x = x
         return out
 
     def backward(self, grad, w13, w2, gate, into: Optional[Grads] = None) -> Grads:
@@ -114,7 +116,6 @@ class MoELayer:
         self._route(x, gate, bias)
         ep.ep_expert_gemv_w4_swiglu(self.handle, self.recv, q.w13, q.s13, self.act)
         ep.ep_expert_gemv_w4(self.handle, self.act, q.w2, q.s2, self.expert_out)
-        self.x = None
         out = torch.empty_like(x)
         ep.ep_combine_weighted(self.handle, self.expert_out, self.recv_weights, out)
         return out
