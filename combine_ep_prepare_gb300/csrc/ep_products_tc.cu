@@ -55,12 +55,23 @@ constexpr int kStages = 6;
 constexpr int kBoxBytes = kSlab * 128;  // 64 rows of 64 elements
 // The accumulator in tensor memory is rounded toward zero with every mma: a
 // weight gradient of 512 rows is off by 4.7e-7 (of its norm), of 4,096 by
-// 4.4e-6, of 16,384 by 1.9e-5.  That drowns in a 16-bit result.  A float32
-// gradient is summed over segments of twelve slabs (768 rows, 7e-7): each is
-// added to the output in float32, rounded to nearest, by the lanes that wrote
-// the one before.  (Adding costs: at 128 experts of 300 to 900 rows the up
-// products' backward pass took 1.02 ms with segments of 512 rows.)
+// 4.4e-6, of 16,384 by 1.9e-5, all to one side.  That drowns in a 16-bit
+// result up to kLong slabs (32,768 elements: 4e-5 beside the 2e-4 of fp16's
+// rounding).  Longer sums are taken in parts of kLong slabs: each is added in
+// float32, rounded to nearest, to what the other accumulator's columns carry
+// of the parts before, so that the error stays there at any length (2^20
+// elements in one sum were off by 1.2e-3).  A float32 gradient is summed over
+// segments of twelve slabs (768 rows, 7e-7): each is added to the output in
+// float32, rounded to nearest, by the lanes that wrote the one before.
+// (Adding costs: at 128 experts of 300 to 900 rows the up products' backward
+// pass took 1.02 ms with segments of 512 rows.)
 constexpr int kSegment = 12;
+constexpr int kLong = 512;
+// Whether a tile's sum is taken in parts, and how many slabs each has.
+template <typename O>
+__device__ __forceinline__ bool folded(int slabs) { return sizeof(O) != 4 && slabs > kLong; }
+template <typename O>
+__device__ __forceinline__ int part_slabs(int slabs) { return sizeof(O) == 4 ? kSegment : min(slabs, kLong); }
 
 // f0: first feature; r0, n: first row and row count (N, a multiple of 32) of
 // the pair's tile (wgrad: output features).
@@ -250,6 +261,25 @@ struct Rows {
     }
   }
 };
+
+// One part of a long sum: this warp's lanes and columns of the accumulator are
+// added to what the carried ones hold (first: they become it).
+__device__ __forceinline__ void carry_half(uint32_t acc, uint32_t carried, int half, int n, bool first) {
+#pragma unroll 1
+  for (int c = kRows * half; c < n; c += 2 * kRows) {
+    float v[kRows], old[kRows];
+    __syncwarp();
+    tc::tmem_ld16(acc + c, v);
+    if (!first) tc::tmem_ld16(carried + c, old);
+    tc::tmem_ld_wait();
+    if (!first) {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) v[j] += old[j];
+    }
+    tc::tmem_st16(carried + c, v);
+  }
+  tc::tmem_st_wait();
+}
 
 template <typename T, int kind, typename O>
 __device__ __forceinline__ void write_half(const ProductParams& p, const Tile& t, uint32_t acc, int rank, int w, int half,
@@ -527,15 +557,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && rank == 0) {
       if (lane == 0) {
         int stage = 0, buf = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        uint32_t phase = 0, acc_phases = 0;  // a bit for each accumulator
         bool lost = false;
         for (long long i = first; i < walk.total && !lost; i += step) {
           walk.at(i, &t);
           if (t.slabs == 0) continue;
           const uint32_t desc = tc::mma_desc(std::is_same<T, __nv_bfloat16>::value, a_mn, b_mn, kTileM, t.n);
-          const int segment = sizeof(O) == 4 ? kSegment : t.slabs;
+          const int segment = part_slabs<O>(t.slabs);
           for (int k0 = 0; k0 < t.slabs && !lost; k0 += segment) {
-            lost = !tc::mbar_wait(tc::smem_addr(&s.acc_empty[buf]), acc_phase ^ 1, gave_up);
+            lost = !tc::mbar_wait(tc::smem_addr(&s.acc_empty[buf]), (acc_phases >> buf & 1) ^ 1, gave_up);
             if (lost) break;
             tc::fence_after();
             const uint32_t d = tmem + buf * kTileN;
@@ -562,10 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 phase ^= 1;
               }
             }
-            if (++buf == 2) {
-              buf = 0;
-              acc_phase ^= 1;
-            }
+            acc_phases ^= 1u << buf;
+            // A sum in parts keeps to one accumulator, the tile after it too:
+            // the other one carries the sum until this one is released last.
+            if (!folded<O>(t.slabs)) buf ^= 1;
           }
         }
         if (lost) {
@@ -606,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp >= 4) {
       int buf = 0;
-      uint32_t acc_phase = 0;
+      uint32_t acc_phases = 0;
       const int half = (warp - 4) >> 2;
       const int w = warp & 3;  // the accumulator lanes a warp can reach go by its number
       for (long long i = first; i < walk.total; i += step) {
@@ -615,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!has && p.accumulate) continue;  // an expert without rows keeps its gradient
         auto wait = [&]() {
           // The four warps go on or leave together: write_half has barriers.
-          const bool ok = half_all(half, tc::mbar_wait(tc::smem_addr(&s.acc_full[buf]), acc_phase, gave_up));
+          const bool ok = half_all(half, tc::mbar_wait(tc::smem_addr(&s.acc_full[buf]), acc_phases >> buf & 1, gave_up));
           tc::fence_after();
           return ok;
         };
@@ -623,18 +653,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive_cluster(tc::in_block(tc::smem_addr(&s.acc_empty[buf]), 0));
-          if (++buf == 2) {
-            buf = 0;
-            acc_phase ^= 1;
-          }
+          acc_phases ^= 1u << buf;
+          if (!folded<O>(t.slabs)) buf ^= 1;
         };
         const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
         bool fine = true;
-        for (int k = 0; k < t.slabs && fine; k += sizeof(O) == 4 ? kSegment : t.slabs) {
+        const int segment = part_slabs<O>(t.slabs);
+        for (int k = 0; k < t.slabs && fine; k += segment) {
           fine = wait();
           if (!fine) break;
-          write_half<T, kind, O>(p, t, tmem + buf * kTileN + lanes, rank, w, half, lane, rows_out + half * kRows * kHalfM,
-                                 p.accumulate || k > 0);
+          uint32_t acc = tmem + buf * kTileN + lanes;
+          if (folded<O>(t.slabs)) {
+            const uint32_t carried = tmem + (buf ^ 1) * kTileN + lanes;
+            carry_half(acc, carried, half, t.n, k == 0);
+            acc = carried;
+          }
+          if (!folded<O>(t.slabs) || k + segment >= t.slabs)
+            write_half<T, kind, O>(p, t, acc, rank, w, half, lane, rows_out + half * kRows * kHalfM,
+                                   p.accumulate || (sizeof(O) == 4 && k > 0));
           release();
         }
         if (!fine) break;

@@ -472,8 +472,11 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t handle, const void* const* gr
  *
  * Types.  Row buffers (R rows), weights and row outputs hold the layer's
  * payload type.  Sums are float32, rounded once at the end, so the activation
- * is applied to unrounded sums; the tensor cores truncate as they add, which
- * leaves a float32 weight gradient within 1e-6 of its norm (random rows, any
+ * is applied to unrounded sums.  The tensor cores truncate as they add: the
+ * sum of a 16-bit result is taken in parts of at most 32,768 elements, added
+ * in float32, which leaves it within 4e-5 of its norm before the rounding
+ * (random terms, any length); a float32 weight gradient is left
+ * within 1e-6 of its norm (random rows, any
  * number of them).  Feature counts are multiples of 8 up to 2^20
  * and need not match the layer's hidden.  Pointers are 16-byte aligned;
  * outputs must not overlap inputs.  The order of a sum is fixed by the sizes
