@@ -475,10 +475,11 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t handle, const void* const* gr
  * is applied to unrounded sums.  The tensor cores truncate as they add: the
  * sum of a 16-bit result is taken in parts of at most 32,768 elements, added
  * in float32, which leaves it within 4e-5 of its norm before the rounding
- * (random terms, any length); a float32 weight gradient is left
- * within 1e-6 of its norm (random rows, any
- * number of them).  Feature counts are multiples of 8 up to 2^20
- * and need not match the layer's hidden.  Pointers are 16-byte aligned;
+ * (random terms, any length); a float32 weight gradient of 16-bit rows is
+ * summed in runs of 768 rows, each added to dw in float32, which leaves it
+ * within 1.4e-6 of its norm for experts of up to 200,000 random rows and
+ * 2.6e-6 at four million.  Feature counts are multiples of 8 up to 2^20 and
+ * need not match the layer's hidden.  Pointers are 16-byte aligned;
  * outputs must not overlap inputs.  The order of a sum is fixed by the sizes
  * and the counts: the same inputs give the same bits.
  *
@@ -520,8 +521,9 @@ ep_status_t ep_expert_dgrad_swiglu(ep_handle_t handle, const void* dy, const voi
                                    int64_t out_features, int64_t ffn_features, void* dpre, void* stream);
 
 /* Weight gradient: dw[e][n][k] = sum over the expert's rows of dy[r][n] x[r][k];
- * accumulate = 1 adds it to dw (one float32 addition per element, then the
- * rounding to dw's type).  An expert without rows gets zeros, or keeps its
+ * accumulate = 1 adds it to dw in float32, then rounds to dw's type (one
+ * addition per element; into a float32 dw from 16-bit rows one for every 768
+ * rows of the expert).  An expert without rows gets zeros, or keeps its
  * dw.   dy [R, out], x [R, in], dw [E, out, in] out, of the payload type or
  * float32 (dw_dtype). */
 ep_status_t ep_expert_wgrad(ep_handle_t handle, const void* dy, const void* x, int64_t out_features,

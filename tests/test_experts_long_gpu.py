@@ -1,10 +1,14 @@
-"""16-bit products over long reductions.
+"""Products of 16-bit rows over long reductions.
 
 Tolerances.  Element by element, those of test_experts_gpu.py.  On norms: the
 tensor core truncates as it adds, 1.2e-9 of the norm for each element of a sum
 of random terms, and a sum is taken in parts of 32,768 elements, 4e-5; 6e-5 is
 allowed beyond what rounding the 64-bit result alone leaves, and 2e-4 behind
 the activation (whose slope is at most three here).
+A float32 weight gradient is summed in runs of 768 rows, each added in float32
+with rounding to nearest.  A run's truncating accumulations leave 1e-6 (768
+rows at 1.3e-9); the additions 2^-25 each, as a random walk whose steps are of the
+size of the sum so far: 2^-25 * sqrt(n / 2) of the norm for n of them.
 """
 import pytest
 import torch
@@ -98,3 +102,22 @@ def test_gated_forward_and_input_gradients_of_many_features(ep, dtype):  # noqa:
     p = torch.nan_to_num(pre.double()).requires_grad_()
     wanted = torch.autograd.grad(torch.nn.functional.silu(p[:, :f]) * p[:, f:], p, want)[0]
     check_norm(dpre[live], wanted[live], BEHIND_ACTIVATION)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [768, 2000, 20000, 200000, 1 << 22])
+def test_float32_gradients_of_16_bit_rows(ep, rows, dtype, accumulate):  # noqa: F811
+    """What the header promises: 1.4e-6 of the norm up to 200,000 rows, 2.6e-6 at four million."""
+    s = Step(ep, 1, 1, rows, 1, dtype, 41, idx=torch.zeros(rows, 1, dtype=torch.int64))
+    g = torch.Generator(device="cuda").manual_seed(42)
+    dy = torch.randn(rows, 72, generator=g, device="cuda").to(s.tt)
+    x = torch.randn(rows, 136, generator=g, device="cuda").to(s.tt)
+    dw = torch.randn(1, 72, 136, generator=g, device="cuda")
+    want = dw[0].double() if accumulate else 0
+    for i in range(0, rows, 1 << 16):
+        want = want + dy[i:i + (1 << 16)].double().t() @ x[i:i + (1 << 16)].double()
+    ep.ep_expert_wgrad(s.h, dy, x, dw, accumulate=accumulate)
+    bound = 1e-6 + 2.0 ** -25 * (rows / 768 / 2) ** 0.5
+    assert bound <= (1.4e-6 if rows <= 200000 else 2.6e-6)
+    assert off(dw[0], want) <= bound
