@@ -593,7 +593,8 @@ def _w4(h: EpHandle, wq: torch.Tensor, scales: torch.Tensor):
 def ep_expert_gemv_w4(h: EpHandle, x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
                       y: torch.Tensor, stream=None):
     """y[r] = w[e] x[r] with 4-bit weights: wq uint8 [E, out, in/2] (see
-    pack_w4), scales [E, out, in/group] of the payload type."""
+    pack_w4), scales [E, out, in/group] of the payload type.  For up to some
+    32 rows per expert; with more, ep_expert_gemm on 16-bit weights is faster."""
     wp, sp, n, k, group = _w4(h, wq, scales)
     _check(_lib.ep_expert_gemv_w4(h.c, _rows(h, x, k, "x"), wp, sp, n, k, group, _rows(h, y, n, "y"),
                                   _stream(stream)))
@@ -655,7 +656,9 @@ def ep_router(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.
               num_groups: int = 1, topk_groups: int = 1, scale: float = 1.0, stream=None):
     """The chosen experts and their weights, from logits [T, E]: topk_idx
     int64 [T, K] and topk_weights float32 [T, K] as ep_prepare and
-    ep_dispatch take them."""
+    ep_dispatch take them.  Groups are ranked by the sum of their two largest
+    selection values: with the softmax score those are logits, not
+    probabilities."""
     if topk_idx.dim() != 2:
         raise ValueError("topk_idx must be [tokens, top_k], got %s" % (tuple(topk_idx.shape),))
     cfg = _router_config(logits, topk_idx.shape[1], num_groups, topk_groups, score, normalize, scale)

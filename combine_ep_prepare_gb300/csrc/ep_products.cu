@@ -17,8 +17,11 @@ namespace {
 // Output tiles of 64 x 64, 8 x 8 sums per thread, 16 reduction elements at a
 // time, of which each of two groups of 64 threads multiplies eight.  What
 // bounds the kernel is the shared memory's reads, four of 16 bytes for the 64
-// multiply-adds of a thread and reduction element: 8,192 rows x 2048 -> 2 x
-// 1024 take 1.59 ms, 43 of the CUDA cores' 80 TFLOP/s.  Larger tiles save no
+// multiply-adds of a thread and reduction element, 81% busy while the
+// multiply-add unit is 63% (8 experts x 1,024 rows, 1024 -> 2048: 786 us for a
+// floor of 430 at the CUDA cores' 80 TFLOP/s; 8,192 rows x 2048 -> 2 x 1024
+// take 1.59 ms).  The weight gradient, whose operands are written to shared
+// memory as they lie, takes 666 us there (71% and 68%).  Larger tiles save no
 // such reads.  128 x 128 by one group of 256 threads took the same there, but
 // leaves SMs without work where tiles are few (2,500 rows of 8 experts, 1024
 // -> 1024: 206 us for 137; 800 rows of 4: 106 for 63) and multiplies more
@@ -78,12 +81,13 @@ struct Slab {
 
 // Tiles of a few rows are bound by the weights' bytes: their blocks read the
 // weights as they lie, straight into registers, and keep no operand in shared
-// memory.  16 tokens' top 2 of 32 experts, 1024 -> 4096: 139 us for 333 by the
-// way of full tiles; one token's top 2 of 8, 1024 -> 1024: 12.5 for 38.  Eight
-// rows by four columns are the sums that a thread has registers for beside the
-// loads.  wgrad is not treated so: sums straight from global memory gained 11%
-// with two rows to each expert and cost 2% with 512.  Sums go to
-// part[..][row][column].
+// memory.  Warps wait for those loads three quarters of their time: one row
+// each of 32 experts, 1024 -> 4096, takes 111 us, 4.9 TB/s, for a floor of 79.
+// 16 tokens' top 2 of 32 experts, 1024 -> 4096: 139 us for 333 by the way of
+// full tiles; one token's top 2 of 8, 1024 -> 1024: 12.5 for 38.  Eight rows by
+// four columns are the sums that a thread has registers for beside the loads.
+// wgrad is not treated so: sums straight from global memory gained 11% with two
+// rows to each expert and cost 2% with 512.  Sums go to part[..][row][column].
 constexpr int kThin = 8;
 using Thin = float[kThin][kTile];
 

@@ -38,7 +38,8 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 // An arrival on a barrier of any block of the cluster.  It hands no memory
-// over: what comes before it is ordered within this block alone.
+// over: what comes before it is ordered within this block alone.  (Tensor
+// memory is handed over by the tcgen05 fences around it.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

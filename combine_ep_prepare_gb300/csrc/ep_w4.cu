@@ -4,10 +4,12 @@
 // row n (low nibble of a byte: even k).  out[r][n] = sum_k x[r][k] w[e][n][k]
 // for the rows of expert e, or silu(gate) * up of the two halves of n.
 //
-// Bound by the logic unit, which unpacks the weights, and not far behind by
-// their bytes: without the unpacking a decode batch's down products (64
-// experts, 8 rows each, 2048 -> 7168) take 90 us, with it 136; memory alone
-// would take 73.  (Without the copies it takes 131.)
+// The logic unit has most to do, 68% of its rate on a decode batch's down
+// products (64 experts, 8 rows each, 2048 -> 7168): 54 M warp instructions,
+// near 60 for a step of 32 weight rows x 32 elements, of which the unpacking is
+// 28 and the rows' order, addresses and scales are the rest.  No unit is busier.
+// Those products take 141 us; without the unpacking 90, without the copies
+// 131, and memory alone would take 73.
 //
 // Two persistent blocks per SM walk units of 256 down to 64 weight rows of one
 // expert: one warp keeps a ring of two 32 KB stages filled by TMA (and the
@@ -28,6 +30,9 @@
 // of a 16-bit number, one packed operation gives q - 8 exactly, and the
 // integers' sum over a group is exact up to the float32 accumulation of q x;
 // the scale multiplies that sum in float32, so no weight is ever rounded.
+// The weights are unpacked again for every 16 rows: from 33 rows per expert on
+// the 16-bit product is faster (16 experts, 2048 -> 7168: 76 us against 79 at
+// 32 rows each, 123 against 81 at 48, 294 against 84 at 128).
 #include "ep_experts.cuh"
 #include "ep_tc.cuh"
 

@@ -52,7 +52,12 @@
 extern "C" {
 #endif
 
+/* The version counts changes to what a caller of an earlier header relies on.
+ * The expert products, the 4-bit products and the router were added within
+ * version 4: ask EP_HAS_EXPERT_CALLS of a header, and the symbol (dlsym) of a
+ * loaded library. */
 #define EP_ABI_VERSION 4u
+#define EP_HAS_EXPERT_CALLS 1
 
 typedef enum {
   EP_OK = 0,
@@ -80,7 +85,10 @@ typedef enum {
                                     write nothing; the grid-wide routing map (batches over
                                     65,536 routes) then does nothing on the handle until its
                                     memory is zero-filled again, while a smaller batch's
-                                    prepare, which does not use the wait, rewrites it */
+                                    prepare, which does not use the wait, rewrites it.
+                                    Reported without EP_ST_NOT_PREPARED: a wait inside an
+                                    expert product on the handle gave up, and that call's
+                                    outputs are incomplete; the next prepare clears it */
 #define EP_ST_NOT_PREPARED 8u    /* reported by ep_read_info when no ep_prepare has
                                     written this handle memory; row calls then write nothing.
                                     Detected by a marker word in the handle header: zero-fill
@@ -480,8 +488,10 @@ ep_status_t ep_rank_major_dispatch_bwd(ep_handle_t handle, const void* const* gr
  * within 1.4e-6 of its norm for experts of up to 200,000 random rows and
  * 2.6e-6 at four million.  Feature counts are multiples of 8 up to 2^20 and
  * need not match the layer's hidden.  Pointers are 16-byte aligned;
- * outputs must not overlap inputs.  The order of a sum is fixed by the sizes
- * and the counts: the same inputs give the same bits.
+ * outputs must not overlap inputs.  The order of a sum is fixed by the sizes,
+ * the counts and, in the 4-bit products, the device's number of SMs: the same
+ * inputs give the same bits.  A row's bits may change with the number of rows
+ * beside it.
  *
  * Weights are [E][out_features][in_features], row-major.  A gated layer keeps
  * its two input matrices in one [E][2*ffn_features][in_features]: gate rows
@@ -533,7 +543,10 @@ ep_status_t ep_expert_wgrad(ep_handle_t handle, const void* dy, const void* x, i
  * fp16 layers).  w[e][n][k] = scales[e][n][k / group] * (q - 8), q the
  * unsigned nibble k of a row: low half of byte k/2 for even k, high half for
  * odd k.  The sum over a group is taken on the integers, then multiplied by
- * its scale in float32.
+ * its scale in float32.  Any number of rows is taken, but the weights are
+ * unpacked again for every 16 rows of an expert: from about 33 rows per expert
+ * on, ep_expert_gemm on 16-bit weights is faster (measured on 16 experts, 2048
+ * -> 7168: 76 and 79 us at 32 rows each, 123 and 81 at 48).
  *   x [R, in], wq uint8 [E, out, in/2], scales [E, out, in/group] of the
  *   payload type, y [R, out] out; group 32, 64 or 128, dividing in. */
 ep_status_t ep_expert_gemv_w4(ep_handle_t handle, const void* x, const uint8_t* wq, const void* scales,
@@ -554,6 +567,9 @@ ep_status_t ep_expert_gemv_w4_swiglu(ep_handle_t handle, const void* x, const ui
  * num_groups > 1 the experts form groups of E/num_groups consecutive ones, a
  * group's rank is the sum of its two largest v (twice the largest where only
  * one can be chosen) and only the topk_groups highest groups' experts stay.
+ * With the softmax score that is a sum of logits: a model that ranks its
+ * groups by the largest probability, or by a sum of probabilities, chooses
+ * other groups.
  * The top_k largest v are chosen, in descending order; ties go to the lower
  * index, between groups too.  An expert whose logit or v is -infinity or NaN
  * is never chosen; where fewer than top_k can be chosen the remaining ids are
