@@ -32,6 +32,9 @@ _BINDING_NAMES = {
     "ep_rank_major_dispatch_bwd",
     "ep_expert_gemm", "ep_expert_gemm_swiglu", "ep_expert_dgrad", "ep_expert_dgrad_swiglu", "ep_expert_wgrad",
     "ep_expert_gemv_w4", "ep_expert_gemv_w4_swiglu", "pack_w4", "ep_router", "ep_router_bwd",
+    "ep_rmsnorm", "rmsnorm_bwd_workspace", "ep_rmsnorm_bwd", "ep_quantize_rows", "ep_expert_quantize", "ep_dispatch_f8",
+    "ep_expert_gemm_f8", "ep_expert_gemm_f8_swiglu", "ep_expert_dgrad_f8", "ep_expert_dgrad_f8_swiglu", "pack_f8",
+    "scale_columns", "ep_moe_few", "moe_few_workspace", "MAX_FEW_TOKENS",
 }
 
 

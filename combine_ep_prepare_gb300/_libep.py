@@ -57,6 +57,11 @@ class RouterConfig(ctypes.Structure):
 SCORE_CODES = {"softmax": 0, "sigmoid": 1}
 
 
+class MoeFewConfig(ctypes.Structure):
+    _fields_ = [("router", RouterConfig), ("hidden", ctypes.c_int64), ("ffn", ctypes.c_int64),
+                ("dtype", ctypes.c_int64), ("weight_f8", ctypes.c_int64)]
+
+
 class Handle(ctypes.Structure):
     _fields_ = [("id", ctypes.c_uint64), ("mem", ctypes.c_void_p)]
 
@@ -116,6 +121,18 @@ def _load(path=None):
         "ep_expert_gemv_w4_swiglu": ([Handle, p, p, p, i64, i64, i64, p, p], st),
         "ep_router": ([RouterConfig, p, p, i64, p, p, p], st),
         "ep_router_bwd": ([RouterConfig, p, p, p, i64, p, p], st),
+        "ep_rmsnorm": ([p, p, p, i64, i64, i64, ctypes.c_float, p, p, p, p, p], st),
+        "ep_rmsnorm_bwd_workspace": ([i64, i64, ctypes.POINTER(ctypes.c_size_t)], st),
+        "ep_rmsnorm_bwd": ([p, p, p, p, i64, i64, i64, ctypes.c_float, p, p, ctypes.c_int, p, p], st),
+        "ep_quantize_rows": ([p, i64, i64, i64, p, p, p], st),
+        "ep_expert_quantize": ([Handle, p, i64, p, p, p], st),
+        "ep_dispatch_f8": ([Handle, p, i64, p, p, p, p, p, p, p], st),
+        "ep_expert_gemm_f8": ([Handle, p, p, p, p, i64, i64, p, p], st),
+        "ep_expert_gemm_f8_swiglu": ([Handle, p, p, p, p, i64, i64, p, p, p, p, p], st),
+        "ep_expert_dgrad_f8": ([Handle, p, p, p, p, i64, i64, p, p], st),
+        "ep_expert_dgrad_f8_swiglu": ([Handle, p, p, p, p, p, i64, i64, p, p], st),
+        "ep_moe_few_workspace": ([MoeFewConfig, i64, ctypes.POINTER(ctypes.c_size_t)], st),
+        "ep_moe_few": ([MoeFewConfig, p, p, p, p, p, p, p, i64, p, p, p, p, p], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -134,7 +151,10 @@ SYMBOLS = ("ep_abi_version", "ep_last_error", "ep_launch_count", "ep_register_la
            "ep_rank_major_dispatch", "ep_rank_major_combine", "ep_rank_major_combine_bwd",
            "ep_rank_major_dispatch_bwd",
            "ep_expert_gemm", "ep_expert_gemm_swiglu", "ep_expert_dgrad", "ep_expert_dgrad_swiglu",
-           "ep_expert_wgrad", "ep_expert_gemv_w4", "ep_expert_gemv_w4_swiglu", "ep_router", "ep_router_bwd")
+           "ep_expert_wgrad", "ep_expert_gemv_w4", "ep_expert_gemv_w4_swiglu", "ep_router", "ep_router_bwd",
+           "ep_rmsnorm", "ep_rmsnorm_bwd_workspace", "ep_rmsnorm_bwd", "ep_quantize_rows", "ep_expert_quantize",
+           "ep_dispatch_f8", "ep_expert_gemm_f8", "ep_expert_gemm_f8_swiglu", "ep_expert_dgrad_f8",
+           "ep_expert_dgrad_f8_swiglu", "ep_moe_few_workspace", "ep_moe_few")
 
 
 def lib():
@@ -688,3 +708,256 @@ def ep_router_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, grad_topk_weight
     _check(_lib.ep_router_bwd(cfg, _ptr(logits, None, "logits"), _ptr(topk_idx, torch.int64, "topk_idx"),
                               _ptr(grad_topk_weights, torch.float32, "grad_topk_weights"), T,
                               _ptr(grad_logits, logits.dtype, "grad_logits"), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# 8-bit rows and weights (e4m3 with a float32 scale for each block of 128)
+# ----------------------------------------------------------------------------
+
+F8 = torch.float8_e4m3fn
+_F8_BLOCK = 128
+
+
+def _f8_blocks(n: int) -> int:
+    return (n + _F8_BLOCK - 1) // _F8_BLOCK
+
+
+def scale_columns(features: int) -> int:
+    """Floats of a row of scales: one for each 128 features, padded to a
+    multiple of four."""
+    return (_f8_blocks(features) + 3) // 4 * 4
+
+
+def _f8_ptr(t: torch.Tensor, name: str) -> Optional[int]:
+    return _ptr(t, F8, name)
+
+
+def _shaped(t: torch.Tensor, shape, dtype, name: str) -> Optional[int]:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    return _ptr(t, dtype, name)
+
+
+def _f8_rows(h: EpHandle, t: torch.Tensor, scales: torch.Tensor, width: int, name: str):
+    """8-bit receive rows and their scales: at least the layer's capacity."""
+    capacity = _layer_experts.get(h.id, (0, 0))[1]
+    for x, cols, n, dtype in ((t, width, name, F8), (scales, scale_columns(width), name + "_scales", torch.float32)):
+        _ptr(x, dtype, n)
+        if x.dim() != 2 or x.shape[1] != cols or x.shape[0] < capacity:
+            raise ValueError("%s must be [>= %d rows, %d], got %s" % (n, capacity, cols, tuple(x.shape)))
+    return t.data_ptr() or None, scales.data_ptr() or None
+
+
+def _f8_weights(h: EpHandle, w: torch.Tensor, scales: torch.Tensor):
+    wp, n, k = _expert_weights(h, w, "w", F8)
+    return wp, _shaped(scales, (w.shape[0], _f8_blocks(n), _f8_blocks(k)), torch.float32, "w_scales"), n, k
+
+
+def pack_f8(w: torch.Tensor):
+    """Round weights [E, out, in] to e4m3 with one float32 scale for each
+    128 x 128 block: (w float8_e4m3fn [E, out, in], scales [E, ceil(out/128),
+    ceil(in/128)]).  Laid out once, when weights are loaded or updated; plain
+    torch."""
+    E, n, k = w.shape
+    nb, kb = _f8_blocks(n), _f8_blocks(k)
+    g = torch.nn.functional.pad(w.float(), (0, kb * _F8_BLOCK - k, 0, nb * _F8_BLOCK - n))
+    g = g.view(E, nb, _F8_BLOCK, kb, _F8_BLOCK)
+    m = g.abs().amax(dim=(2, 4), keepdim=True).clamp_min(2.0 ** -100)
+    q = (g * (torch.full_like(m, 448.0) / m)).clamp(-448.0, 448.0).to(F8)
+    q = q.view(E, nb * _F8_BLOCK, kb * _F8_BLOCK)[:, :n, :k].contiguous()
+    return q, (m / 448.0).view(E, nb, kb).contiguous()
+
+
+def ep_quantize_rows(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None):
+    """q (float8_e4m3fn) and scales [rows, scale_columns(n)] of the rows x
+    [rows, n]: each block of 128 scaled so that its largest magnitude is 448."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, features], got %s" % (tuple(x.shape),))
+    rows, n = x.shape
+    code = _dtype_code(x.dtype)
+    _check(_lib.ep_quantize_rows(_ptr(x, None, "x"), rows, n, code, _shaped(q, x.shape, F8, "q"),
+                                 _shaped(scales, (rows, scale_columns(n)), torch.float32, "scales"), _stream(stream)))
+
+
+def ep_expert_quantize(h: EpHandle, x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None):
+    """The same for the receive rows of a prepared handle; padding rows become
+    zeros with zero scales."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, features], got %s" % (tuple(x.shape),))
+    n = x.shape[1]
+    xp = _rows(h, x, n, "x")
+    qp, sp = _f8_rows(h, q, scales, n, "q")
+    _check(_lib.ep_expert_quantize(h.c, xp, n, qp, sp, _stream(stream)))
+
+
+def ep_dispatch_f8(h: EpHandle, topk_idx: torch.Tensor, tokens: torch.Tensor, scales: torch.Tensor,
+                   topk_weights: torch.Tensor, recv_tokens: torch.Tensor, recv_scales: torch.Tensor,
+                   recv_topk_weights: torch.Tensor, stream=None):
+    """ep_dispatch of 8-bit rows with their scales."""
+    if tokens.dim() != 2:
+        raise ValueError("tokens must be [tokens, hidden], got %s" % (tuple(tokens.shape),))
+    T, n = tokens.shape
+    sp = _shaped(scales, (T, scale_columns(n)), torch.float32, "scales")
+    rp, rsp = _f8_rows(h, recv_tokens, recv_scales, n, "recv_tokens")
+    _check(_lib.ep_dispatch_f8(h.c, _ptr(topk_idx, torch.int64, "topk_idx"), T, _f8_ptr(tokens, "tokens"), sp,
+                               _ptr(topk_weights, torch.float32, "topk_weights"), rp, rsp,
+                               _ptr(recv_topk_weights, torch.float32, "recv_topk_weights"), _stream(stream)))
+
+
+def ep_expert_gemm_f8(h: EpHandle, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                      y: torch.Tensor, stream=None):
+    """y[r] = w[e] x[r] of 8-bit rows and weights (see pack_f8); w [E, out, in],
+    y of the layer's payload type."""
+    wp, wsp, n, k = _f8_weights(h, w, w_scales)
+    xp, xsp = _f8_rows(h, x, x_scales, k, "x")
+    _check(_lib.ep_expert_gemm_f8(h.c, xp, xsp, wp, wsp, n, k, _rows(h, y, n, "y"), _stream(stream)))
+
+
+def ep_expert_gemm_f8_swiglu(h: EpHandle, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                             w_scales: torch.Tensor, act: Optional[torch.Tensor] = None,
+                             act_q: Optional[torch.Tensor] = None, act_scales: Optional[torch.Tensor] = None,
+                             pre: Optional[torch.Tensor] = None, stream=None):
+    """act[r] = silu(gate) * up of w[e] x[r]; w [E, 2*ffn, in], gate rows
+    first.  act and pre [R, 2*ffn] in the payload type, act_q and act_scales
+    in 8 bits; any may be left out, not all."""
+    wp, wsp, n, k = _f8_weights(h, w, w_scales)
+    f = _gated(n, "w")
+    xp, xsp = _f8_rows(h, x, x_scales, k, "x")
+    if (act_q is None) != (act_scales is None):
+        raise ValueError("act_q and act_scales go together")
+    qp, qsp = (None, None) if act_q is None else _f8_rows(h, act_q, act_scales, f, "act_q")
+    _check(_lib.ep_expert_gemm_f8_swiglu(h.c, xp, xsp, wp, wsp, f, k, None if pre is None else _rows(h, pre, n, "pre"),
+                                         None if act is None else _rows(h, act, f, "act"), qp, qsp, _stream(stream)))
+
+
+def ep_expert_dgrad_f8(h: EpHandle, dy: torch.Tensor, dy_scales: torch.Tensor, w: torch.Tensor,
+                       w_scales: torch.Tensor, dx: torch.Tensor, stream=None):
+    """dx[r] = transpose(w[e]) dy[r] of 8-bit rows and weights."""
+    wp, wsp, n, k = _f8_weights(h, w, w_scales)
+    dp, dsp = _f8_rows(h, dy, dy_scales, n, "dy")
+    _check(_lib.ep_expert_dgrad_f8(h.c, dp, dsp, wp, wsp, n, k, _rows(h, dx, k, "dx"), _stream(stream)))
+
+
+def ep_expert_dgrad_f8_swiglu(h: EpHandle, dy: torch.Tensor, dy_scales: torch.Tensor, w: torch.Tensor,
+                              w_scales: torch.Tensor, pre: torch.Tensor, dpre: torch.Tensor, stream=None):
+    """transpose(w[e]) dy[r] taken through the gated activation; w [E, out,
+    ffn], pre and dpre [R, 2*ffn] in the payload type."""
+    wp, wsp, n, f = _f8_weights(h, w, w_scales)
+    dp, dsp = _f8_rows(h, dy, dy_scales, n, "dy")
+    _check(_lib.ep_expert_dgrad_f8_swiglu(h.c, dp, dsp, wp, wsp, _rows(h, pre, 2 * f, "pre"), n, f,
+                                          _rows(h, dpre, 2 * f, "dpre"), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# Root-mean-square norm
+# ----------------------------------------------------------------------------
+
+def ep_rmsnorm(x: torch.Tensor, weight: torch.Tensor, y: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, sum: Optional[torch.Tensor] = None,
+               q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
+    """h = x + residual (rounded), y = h / rms(h) * weight: `sum` receives h,
+    y the norm in x's type, q and scales the unrounded norm in 8 bits.  Any
+    result may be left out, not all."""
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, hidden], got %s" % (tuple(x.shape),))
+    T, H = x.shape
+    code, dt = _dtype_code(x.dtype), x.dtype
+    opt = lambda t, name: None if t is None else _shaped(t, x.shape, dt, name)  # noqa: E731
+    _check(_lib.ep_rmsnorm(_ptr(x, None, "x"), opt(residual, "residual"), _shaped(weight, (H,), dt, "weight"), T, H, code, eps,
+                           opt(sum, "sum"), opt(y, "y"), None if q is None else _shaped(q, x.shape, F8, "q"),
+                           None if scales is None else _shaped(scales, (T, scale_columns(H)), torch.float32, "scales"),
+                           _stream(stream)))
+
+
+def rmsnorm_bwd_workspace(tokens: int, hidden: int, device="cuda") -> torch.Tensor:
+    """The workspace of ep_rmsnorm_bwd for batches of up to that many tokens."""
+    size = ctypes.c_size_t(0)
+    _check(_lib.ep_rmsnorm_bwd_workspace(tokens, hidden, ctypes.byref(size)))
+    return torch.empty(max(16, int(size.value)), dtype=torch.uint8, device=device)
+
+
+def ep_rmsnorm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, grad_h: torch.Tensor,
+                   grad_weight: torch.Tensor, workspace: torch.Tensor, grad_sum: Optional[torch.Tensor] = None,
+                   eps: float = 1e-6, accumulate: bool = False, stream=None):
+    """grad_h (of x and of the residual alike) and grad_weight float32 [H]
+    (accumulate: added to) from the norm's gradient and what comes down the
+    residual stream; h is ep_rmsnorm's `sum`, or its x."""
+    if h.dim() != 2:
+        raise ValueError("h must be [tokens, hidden], got %s" % (tuple(h.shape),))
+    T, H = h.shape
+    code, dt = _dtype_code(h.dtype), h.dtype
+    size = ctypes.c_size_t(0)
+    _check(_lib.ep_rmsnorm_bwd_workspace(T, H, ctypes.byref(size)))
+    if workspace.numel() * workspace.element_size() < size.value:
+        raise ValueError("workspace must hold %d bytes, got %d" % (size.value, workspace.numel() * workspace.element_size()))
+    _check(_lib.ep_rmsnorm_bwd(_shaped(grad_y, h.shape, dt, "grad_y"), _ptr(h, None, "h"), _shaped(weight, (H,), dt, "weight"),
+                               None if grad_sum is None else _shaped(grad_sum, h.shape, dt, "grad_sum"), T, H, code, eps,
+                               _shaped(grad_h, h.shape, dt, "grad_h"), _shaped(grad_weight, (H,), torch.float32, "grad_weight"),
+                               1 if accumulate else 0, _ptr(workspace, None, "workspace"), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# A whole layer for a few tokens
+# ----------------------------------------------------------------------------
+
+MAX_FEW_TOKENS = 32
+
+
+def moe_few_workspace(experts: int, top_k: int, hidden: int, ffn: int, tokens: int = MAX_FEW_TOKENS,
+                      device="cuda") -> torch.Tensor:
+    """A workspace of ep_moe_few for batches of up to that many tokens and
+    either type of weights."""
+    code = 1 if ffn % _F8_BLOCK == 0 and hidden % 16 == 0 else 0
+    cfg = MoeFewConfig(RouterConfig(experts, top_k, 1, 1, 0, 0, 0, 1.0), hidden, ffn, 0, code)
+    size = ctypes.c_size_t(0)
+    _check(_lib.ep_moe_few_workspace(cfg, tokens, ctypes.byref(size)))
+    return torch.empty(int(size.value), dtype=torch.uint8, device=device)
+
+
+_few_configs = {}  # arguments -> (MoeFewConfig, {tokens: workspace bytes})
+
+
+def ep_moe_few(x: torch.Tensor, gate: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, out: torch.Tensor,
+               topk_idx: torch.Tensor, topk_weights: torch.Tensor, workspace: torch.Tensor,
+               s13: Optional[torch.Tensor] = None, s2: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, score: str = "softmax", normalize: bool = True,
+               num_groups: int = 1, topk_groups: int = 1, scale: float = 1.0, stream=None):
+    """out [T, H] of a whole layer for up to 32 tokens in two kernels: the
+    gate's product, the choice (as ep_router), the chosen experts' gated
+    products and their weighted sum.  w13 [E, 2*ffn, H] and w2 [E, H, ffn] of
+    x's type, or float8_e4m3fn with the scales s13 and s2 (see pack_f8); the
+    rows then are quantised as ep_quantize_rows does.  Calls on one workspace
+    have to be ordered."""
+    if x.dim() != 2 or gate.dim() != 2 or topk_idx.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("x, gate and topk_idx are matrices, w13 and w2 [experts, out, in]")
+    T, H = x.shape
+    E, F, K = gate.shape[0], w2.shape[2], topk_idx.shape[1]
+    f8 = w13.dtype == F8
+    key = (E, K, H, F, x.dtype, gate.dtype, f8, score, bool(normalize), num_groups, topk_groups, scale)
+    entry = _few_configs.get(key)
+    if entry is None:
+        if score not in SCORE_CODES:
+            raise ValueError("score must be softmax or sigmoid, got %s" % score)
+        entry = (MoeFewConfig(RouterConfig(E, K, num_groups, topk_groups, SCORE_CODES[score], 1 if normalize else 0,
+                                           _dtype_code(gate.dtype), scale), H, F, _dtype_code(x.dtype), 1 if f8 else 0), {})
+        if len(_few_configs) < 1024:
+            _few_configs[key] = entry
+    cfg, sizes = entry
+    need = sizes.get(T)
+    if need is None:
+        size = ctypes.c_size_t(0)
+        _check(_lib.ep_moe_few_workspace(cfg, T, ctypes.byref(size)))
+        need = sizes[T] = int(size.value)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace must hold %d bytes, got %d" % (need, workspace.numel() * workspace.element_size()))
+    wt = F8 if f8 else x.dtype
+    if f8 and (s13 is None or s2 is None):
+        raise ValueError("8-bit weights need s13 and s2")
+    sp = lambda s, n, k, name: None if s is None else _shaped(s, (E, _f8_blocks(n), _f8_blocks(k)), torch.float32, name)  # noqa: E731
+    _check(_lib.ep_moe_few(cfg, _ptr(x, None, "x"), _shaped(gate, (E, H), None, "gate"),
+                           None if bias is None else _shaped(bias, (E,), torch.float32, "bias"),
+                           _shaped(w13, (E, 2 * F, H), wt, "w13"), sp(s13, 2 * F, H, "s13"),
+                           _shaped(w2, (E, H, F), wt, "w2"), sp(s2, H, F, "s2"), T, _shaped(out, x.shape, x.dtype, "out"),
+                           _shaped(topk_idx, (T, K), torch.int64, "topk_idx"),
+                           _shaped(topk_weights, (T, K), torch.float32, "topk_weights"), _ptr(workspace, None, "workspace"),
+                           _stream(stream)))

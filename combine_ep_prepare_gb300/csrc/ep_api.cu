@@ -623,6 +623,45 @@ ep_status_t ep_dispatch(ep_handle_t h, const int64_t* topk_idx, int64_t T, const
   return EP_OK;
 }
 
+ep_status_t ep_dispatch_f8(ep_handle_t h, const int64_t* topk_idx, int64_t T, const uint8_t* tokens, const float* scales,
+                           const float* topk_weights, uint8_t* recv_tokens, float* recv_scales,
+                           float* recv_topk_weights, void* stream) {
+  const LayerInfo* L = nullptr;
+  ep_status_t st = lookup(h, &L);
+  if (st != EP_OK) return st;
+  if (L->cfg.hidden % 16 != 0)
+    return fail(EP_ERR_SHAPE, "hidden %lld is not a multiple of 16, as 8-bit rows need", (long long)L->cfg.hidden);
+  if ((st = check_tokens(L, T)) != EP_OK) return st;
+  if (T > 0 && topk_idx == nullptr) return fail(EP_ERR_INVALID_ARG, "topk_idx is NULL");
+  if ((st = check_payload(tokens, T, "tokens", T > 0)) != EP_OK) return st;
+  if ((st = check_payload(scales, T, "scales", T > 0)) != EP_OK) return st;
+  if ((st = check_f32(topk_weights, "topk_weights", T > 0)) != EP_OK) return st;
+  if ((st = check_payload(recv_tokens, T, "recv_tokens", true)) != EP_OK) return st;
+  if ((st = check_payload(recv_scales, T, "recv_scales", true)) != EP_OK) return st;
+  if ((st = check_f32(recv_topk_weights, "recv_topk_weights", true)) != EP_OK) return st;
+  int sms = 0;
+  if ((st = check_device(&sms)) != EP_OK) return st;
+  // Rows are moved as bytes: the 8-bit ones with the weights, then the scales.
+  ep::RowParams p = row_params(L, h, T);
+  p.rowbytes = static_cast<int>(L->cfg.hidden);
+  p.src = tokens;
+  p.dst = recv_tokens;
+  p.w_in = topk_weights;
+  p.w_out = recv_topk_weights;
+  cudaError_t e = ep::launch_scatter(p, true, static_cast<int>(L->lay.pad_cap), sms, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) {
+    p.rowbytes = static_cast<int>((L->cfg.hidden + 511) / 512 * 16);
+    p.src = scales;
+    p.dst = recv_scales;
+    p.w_in = nullptr;
+    p.w_out = nullptr;
+    e = ep::launch_scatter(p, false, static_cast<int>(L->lay.pad_cap), sms, static_cast<cudaStream_t>(stream));
+  }
+  g_launches.fetch_add(2, std::memory_order_relaxed);
+  if (e != cudaSuccess) return cuda_fail(e, "ep_dispatch_f8 launch");
+  return EP_OK;
+}
+
 ep_status_t ep_combine(ep_handle_t h, const void* expert_out, int64_t T, void* result,
                        void* stream) {
   const LayerInfo* L = nullptr;

@@ -2,28 +2,13 @@
 // host-side validation and parameters.  Like the row calls these only enqueue
 // work on the stream: no allocation, no host synchronisation.
 #include <cmath>
-#include <cstdio>
 
-#include "ep_experts.cuh"
+#include "ep_api_checks.h"
 
 namespace {
 
-using ep::api_fail;
+using namespace ep::checks;
 using ep::LayerInfo;
-
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-
-ep_status_t fail(ep_status_t code, const char* fmt, const char* name, long long v = 0) {
-  char buf[256];
-  snprintf(buf, sizeof buf, fmt, name, v);
-  return api_fail(code, buf);
-}
-
-ep_status_t check_ptr(const void* p, const char* name, size_t align = 16) {
-  if (p == nullptr) return fail(EP_ERR_INVALID_ARG, "%s is NULL", name);
-  if (misaligned(p, align)) return fail(EP_ERR_INVALID_ARG, "%s is not %lld-byte aligned", name, (long long)align);
-  return EP_OK;
-}
 
 // Feature counts: rows of 16-byte vectors, bounded so that 32-bit column
 // indices and the tile counts of EP_MAX_EXPERTS experts hold.
@@ -34,13 +19,6 @@ ep_status_t check_features(int64_t n, const char* name) {
 }
 
 ep_status_t layer(const ep_handle_t& h, const LayerInfo** L) { return ep::api_expert_layer(h, L); }
-
-template <typename T>
-T* at(void* mem, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(mem) + off); }
-
-int own_experts(const LayerInfo* L) {
-  return static_cast<int>(L->nranks > 0 ? L->cfg.num_experts / L->nranks : L->cfg.num_experts);
-}
 
 ep::ProductParams product_params(const LayerInfo* L, const ep_handle_t& h, int kind, int64_t N, int64_t K) {
   ep::ProductParams p;
@@ -113,6 +91,18 @@ ep_status_t w4(ep_handle_t h, bool gated, const void* x, const uint8_t* wq, cons
 }
 
 ep_status_t router_params(const ep_router_config_t& c, int64_t T, const void* logits, ep::RouterParams* p) {
+  const ep_status_t st = router_config(c, T, p);
+  if (st != EP_OK) return st;
+  p->logits = logits;
+  return T > 0 ? check_ptr(logits, "logits", c.dtype == EP_DTYPE_FP32 ? 4 : 2) : EP_OK;
+}
+
+}  // namespace
+
+namespace ep {
+namespace checks {
+
+ep_status_t router_config(const ep_router_config_t& c, int64_t T, RouterParams* p) {
   if (c.num_experts < 1 || c.num_experts > EP_MAX_EXPERTS)
     return fail(EP_ERR_LIMIT, "%s %lld outside [1, EP_MAX_EXPERTS]", "num_experts", (long long)c.num_experts);
   if (c.top_k < 1 || c.top_k > EP_MAX_TOPK || c.top_k > c.num_experts)
@@ -130,10 +120,6 @@ ep_status_t router_params(const ep_router_config_t& c, int64_t T, const void* lo
   if (!std::isfinite(c.scale)) return fail(EP_ERR_INVALID_ARG, "%s is not finite", "scale");
   if (T < 0 || T > (1LL << 24) / c.top_k)
     return fail(EP_ERR_SHAPE, "%s %lld: num_tokens*top_k must lie in [0, 2^24]", "num_tokens", (long long)T);
-  if (T > 0) {
-    const ep_status_t st = check_ptr(logits, "logits", c.dtype == EP_DTYPE_FP32 ? 4 : 2);
-    if (st != EP_OK) return st;
-  }
   p->T = static_cast<int>(T);
   p->E = static_cast<int>(c.num_experts);
   p->K = static_cast<int>(c.top_k);
@@ -143,7 +129,7 @@ ep_status_t router_params(const ep_router_config_t& c, int64_t T, const void* lo
   p->normalize = static_cast<int>(c.normalize);
   p->dtype = static_cast<int>(c.dtype);
   p->scale = c.scale;
-  p->logits = logits;
+  p->logits = nullptr;
   p->bias = nullptr;
   p->idx = nullptr;
   p->w = nullptr;
@@ -152,7 +138,8 @@ ep_status_t router_params(const ep_router_config_t& c, int64_t T, const void* lo
   return EP_OK;
 }
 
-}  // namespace
+}  // namespace checks
+}  // namespace ep
 
 extern "C" {
 

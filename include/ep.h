@@ -58,6 +58,8 @@ extern "C" {
  * loaded library. */
 #define EP_ABI_VERSION 4u
 #define EP_HAS_EXPERT_CALLS 1
+/* The 8-bit calls, the norm and ep_moe_few, added within version 4 too. */
+#define EP_HAS_F8_CALLS 1
 
 typedef enum {
   EP_OK = 0,
@@ -604,6 +606,149 @@ ep_status_t ep_router(ep_router_config_t config, const void* logits, const float
  * topk_idx and the logits given to ep_router.  Masked routes have no part. */
 ep_status_t ep_router_bwd(ep_router_config_t config, const void* logits, const int64_t* topk_idx,
                           const float* grad_topk_weights, int64_t num_tokens, void* grad_logits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit rows and weights: e4m3 (4 exponent and 3 mantissa bits, largest value
+ * 448, no infinity) with float32 scales.
+ *
+ * Rows.  A row of n features has one scale for each 128 of them (the last
+ * block may be shorter): feature k stands for q[k] * scales[k / 128].  A row
+ * of scales is padded to S(n) = roundup(ceil(n / 128), 4) floats.  Quantising
+ * a block takes m = its largest magnitude, at least 2^-100; the scale is
+ * m / 448 and q = x * (448 / m), rounded to nearest even (quotient and product
+ * rounded to float32 first).  A block with a NaN or an infinity becomes NaN
+ * throughout; so does no other.
+ *
+ * Weights.  [E][out][in] with one scale for each 128 x 128 block (those at the
+ * ends may be smaller): w_scales float32 [E][ceil(out/128)][ceil(in/128)].
+ *
+ * Products.  The sum over a block of 128 is taken by the tensor cores, then
+ * multiplied by the row's and the weights' scales and added in float32.
+ * y[r][n] = sum over b of xs[r][b] ws[e][n/128][b] * sum over k in b of
+ * x[r][k] w[e][n][k].  Experts, counts, padding rows and P are as for the
+ * other expert products; an untouched row's scales are left alone with it, a
+ * padding row's are zero.  Layers of bf16 and fp16 payload take them, which is
+ * the type of their 16-bit operands and results.  Feature counts are multiples
+ * of 16 up to 2^20; ffn_features, a gated pair's, are multiples of 128.
+ * ------------------------------------------------------------------------ */
+
+/* Largest feature count of the row calls that hold a row on chip. */
+#define EP_MAX_NORM_HIDDEN 32768
+
+/* Root-mean-square norm of num_tokens rows, with an addition before it:
+ *   h = x + residual, rounded to the payload type (h = x without a residual)
+ *   y = h * (mean of h^2 + eps)^(-1/2) * weight
+ * in float32 from h on.  Any of the results may be left out (NULL), not all:
+ * sum [T, H] receives h (only with a residual), y [T, H] the norm rounded to
+ * the payload type, q [T, H] and scales float32 [T, S(H)] the unrounded norm
+ * quantised (both or neither).  sum may be x or residual itself, y may be x.
+ *   x, residual, weight [H] of dtype (ep_dtype_t).  H a multiple of 8 (16 for
+ *   q) up to EP_MAX_NORM_HIDDEN; eps finite and >= 0. */
+ep_status_t ep_rmsnorm(const void* x, const void* residual, const void* weight, int64_t num_tokens,
+                       int64_t hidden, int64_t dtype, float eps, void* sum, void* y, uint8_t* q,
+                       float* scales, void* stream);
+
+/* Bytes of the workspace of ep_rmsnorm_bwd. */
+ep_status_t ep_rmsnorm_bwd_workspace(int64_t num_tokens, int64_t hidden, size_t* bytes /* host, out */);
+
+/* Gradient of ep_rmsnorm with respect to h (so to x and to residual alike) and
+ * to the weight; quantising counts as the identity:
+ *   grad_h = grad_sum + r w dy - h r^3 mean(w dy h),  r = (mean h^2 + eps)^(-1/2)
+ *   grad_weight = sum over tokens of dy h r
+ *   grad_y [T, H], h [T, H] (the sum that ep_rmsnorm gave, or its x), grad_sum
+ *   [T, H] or NULL (what comes down the residual stream), grad_h [T, H] out
+ *   (may be grad_y or grad_sum), grad_weight float32 [H] out (accumulate = 1:
+ *   added to).  The sum over tokens is taken in an order fixed by the sizes.
+ *   workspace: device memory, 16-byte aligned, that no other call uses until
+ *   this one's work is done. */
+ep_status_t ep_rmsnorm_bwd(const void* grad_y, const void* h, const void* weight, const void* grad_sum,
+                           int64_t num_tokens, int64_t hidden, int64_t dtype, float eps, void* grad_h,
+                           float* grad_weight, int accumulate, void* workspace, void* stream);
+
+/* Quantises rows: x [rows, features] of dtype, q [rows, features] out, scales
+ * float32 [rows, S(features)] out (the padding columns zero). */
+ep_status_t ep_quantize_rows(const void* x, int64_t rows, int64_t features, int64_t dtype, uint8_t* q,
+                             float* scales, void* stream);
+
+/* The same for the receive rows of a prepared handle (x [R, features] of the
+ * layer's payload type): rows of an expert are quantised, padding rows become
+ * zeros with zero scales, rows from P on are left alone.  Receive rows are the
+ * same as for the expert products. */
+ep_status_t ep_expert_quantize(ep_handle_t handle, const void* x, int64_t features, uint8_t* q,
+                               float* scales, void* stream);
+
+/* ep_dispatch of 8-bit rows with their scales, on a prepared handle of a
+ * single-buffer layer whose hidden is a multiple of 16: tokens [T, H], scales
+ * [T, S(H)], topk_weights [T, K] to recv_tokens [R, H], recv_scales [R, S(H)],
+ * recv_topk_weights [R]; padding rows zero in all three. */
+ep_status_t ep_dispatch_f8(ep_handle_t handle, const int64_t* topk_idx, int64_t num_tokens,
+                           const uint8_t* tokens, const float* scales, const float* topk_weights,
+                           uint8_t* recv_tokens, float* recv_scales, float* recv_topk_weights, void* stream);
+
+/* y[r] = w[e] x[r].  x [R, in], x_scales [R, S(in)], w [E, out, in], w_scales,
+ * y [R, out] out, of the payload type. */
+ep_status_t ep_expert_gemm_f8(ep_handle_t handle, const uint8_t* x, const float* x_scales, const uint8_t* w,
+                              const float* w_scales, int64_t out_features, int64_t in_features, void* y,
+                              void* stream);
+
+/* The gated pair: pre = w[e] x[r] (gate, then up), act = silu(gate) * up of
+ * the float32 sums.  pre [R, 2*ffn], act [R, ffn] of the payload type; act_q
+ * [R, ffn] and act_scales [R, S(ffn)] the unrounded act quantised (both or
+ * neither).  Any result may be left out (NULL), not all. */
+ep_status_t ep_expert_gemm_f8_swiglu(ep_handle_t handle, const uint8_t* x, const float* x_scales,
+                                     const uint8_t* w, const float* w_scales, int64_t ffn_features,
+                                     int64_t in_features, void* pre, void* act, uint8_t* act_q,
+                                     float* act_scales, void* stream);
+
+/* Input gradient: dx[r] = transpose(w[e]) dy[r].  dy [R, out], dy_scales
+ * [R, S(out)], w and w_scales as in the forward pass, dx [R, in] out. */
+ep_status_t ep_expert_dgrad_f8(ep_handle_t handle, const uint8_t* dy, const float* dy_scales, const uint8_t* w,
+                               const float* w_scales, int64_t out_features, int64_t in_features, void* dx,
+                               void* stream);
+
+/* Input gradient taken through the activation, as ep_expert_dgrad_swiglu:
+ * w [E, out, ffn], pre [R, 2*ffn], dpre [R, 2*ffn] out. */
+ep_status_t ep_expert_dgrad_f8_swiglu(ep_handle_t handle, const uint8_t* dy, const float* dy_scales,
+                                      const uint8_t* w, const float* w_scales, const void* pre,
+                                      int64_t out_features, int64_t ffn_features, void* dpre, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A whole MoE layer for a few tokens (serving), two kernels, no handle:
+ *   logits = x gate^T in float32; choice and weights p as ep_router gives them
+ *   a[t][k] = silu(g) * u of w13[e] x[t],  out[t] = sum over k of p[t][k] w2[e] a[t][k]
+ * with e = topk_idx[t][k]; sums in float32, rounded once.  A token without a
+ * choice gets zeros.  16-bit weights take a rounded to the payload type; 8-bit
+ * weights (weight_f8 = 1) take x and the unrounded a quantised as above, as
+ * the path over ep_dispatch_f8 does.
+ *
+ * workspace: device memory of ep_moe_few_workspace's size, 256-byte aligned,
+ * used by one call at a time (calls on one workspace are ordered by a stream
+ * or events; two graphs that may run at once need two).  Its contents need not
+ * be set, and nothing is kept there from one call to the next.  The second
+ * kernel is a cooperative launch whose blocks wait for one another once, with
+ * a limit of about a second; if that runs out, out is incomplete and the
+ * workspace's first 32-bit word is EP_ST_TIMEOUT, else 0.
+ * ------------------------------------------------------------------------ */
+#define EP_MAX_FEW_TOKENS 32
+
+typedef struct {
+  ep_router_config_t router; /* dtype: of gate */
+  int64_t hidden;            /* H, a multiple of 8 (weight_f8: 16) up to 32768 */
+  int64_t ffn;               /* F, a multiple of 8 (weight_f8: 128) up to 32768 */
+  int64_t dtype;             /* of x, out and 16-bit weights: bf16 or fp16 */
+  int64_t weight_f8;         /* 0: weights of dtype; 1: e4m3 with scales */
+} ep_moe_few_config_t;
+
+ep_status_t ep_moe_few_workspace(ep_moe_few_config_t config, int64_t num_tokens, size_t* bytes /* host, out */);
+
+/* x [T, H], gate [E, H], bias float32 [E] or NULL (sigmoid only), w13
+ * [E, 2*ffn, H] (gate rows, then up rows), w2 [E, H, ffn], their scales
+ * (weight_f8 only, else NULL), out [T, H], topk_idx int64 [T, K] out,
+ * topk_weights float32 [T, K] out; 0 <= T <= EP_MAX_FEW_TOKENS. */
+ep_status_t ep_moe_few(ep_moe_few_config_t config, const void* x, const void* gate, const float* bias,
+                       const void* w13, const float* w13_scales, const void* w2, const float* w2_scales,
+                       int64_t num_tokens, void* out, int64_t* topk_idx, float* topk_weights, void* workspace,
+                       void* stream);
 
 #ifdef __cplusplus
 }
