@@ -1,105 +1,791 @@
 // ep_products_f8.cu -- products grouped by expert of e4m3 rows and weights
-// with a scale for each block of 128.
+// with a scale for each block of 128, on tcgen05.mma.
 //
 //   forward  out[r][n] = sum_b as[r][b] ws[n/128][b] sum_{k in b} a[r][k] w[n][k]
 //   dgrad    out[r][k] = sum_b as[r][b] ws[b][k/128] sum_{n in b} a[r][n] w[n][k]
 //
-// A block takes one row's 128 features, a thread one of them.
-#include <cuda_fp8.h>
+// Tiles are as for the 16-bit products: a pair of SMs takes 256 features (the
+// M side, 128 in each SM) times up to 256 rows of an expert (the N side), and
+// a slab of the reduction is 128 bytes wide -- here 128 elements, one block of
+// the scales.  The scales are arbitrary float32 numbers, so the tensor core
+// can sum over one block only: each slab goes to one of two accumulators in
+// tensor memory, and eight warps add it to sums in registers, times the row's
+// scale and the weights', while the next slab is multiplied into the other.
+//
+// A slab's mma take 512 clocks at the nominal rate of 8-bit operands.  Adding
+// it takes a warp 64 packed multiply-adds, 8 loads from tensor memory and 16
+// of the scales.  The loads are 16 lanes x 256 bits, which give a lane two
+// columns (rows of the tile) in eight, so that it needs 32 rows' scales and
+// not all 128 of its half: with one lane per feature the scales' loads alone
+// would keep shared memory busy for 256 clocks a slab, next to the operands'.
+// A warp of its own brings the scales in, four slabs at a time.
+//
+// The gated pair: 16 gate rows and the 16 up rows of the same features
+// alternate in the tile, and land in one lane's two halves of the sums.  Its
+// 8-bit result needs the largest magnitude of a row's 128 features, 64 in each
+// SM of the pair: they exchange theirs through distributed shared memory.
+#include <algorithm>
+#include <atomic>
 
 #include "ep_f8.cuh"
+#include "ep_pack.cuh"
+#include "ep_tc.cuh"
 
 namespace ep {
 namespace {
 
-__device__ __forceinline__ float e4m3(uint8_t v) {
-  return static_cast<float>(*reinterpret_cast<const __nv_fp8_e4m3*>(&v));
+constexpr int kEpilogueWarps = 8;  // two for each 32 accumulator lanes
+constexpr int kThreads = (4 + kEpilogueWarps) * 32;
+constexpr int kTileM = 256, kTileN = 256, kSlab = 128;  // of the pair
+constexpr int kHalfM = kTileM / 2, kHalfN = kTileN / 2;
+constexpr int kABytes = kHalfM * kSlab, kBBytes = kHalfN * kSlab;
+constexpr int kStages = 6;
+constexpr int kGroup = 4, kGroups = 2;  // slabs whose scales come together; groups in flight
+// Registers of a loading warp and of an adding one: 128 threads of the first
+// and 256 of the second have what 384 x 168 gave them.
+constexpr int kFewRegs = 88, kManyRegs = 208;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "more registers than the block is launched with");
+// Staging of one half of the epilogue, in words: 16 pairs of rows x 128
+// features, or eight pairs in float32.  The paddings keep the lanes of a
+// store on different banks.
+constexpr int kPairStride = kHalfM + 8, kPairStride32 = kHalfM + 4, kGatedStride = kHalfM / 2 + 8;
+constexpr int kStageWords = 16 * kPairStride;
+static_assert(8 * 2 * kPairStride32 <= kStageWords && 16 * kGatedStride <= kStageWords, "staging");
+
+struct Tile {
+  int e, f0, r0, n, cnt, off, rows;
+  bool last;
+};
+
+__device__ __forceinline__ int row_blocks(int cnt) { return (cnt + kTileN - 1) / kTileN; }
+
+// The walk over tiles, the same in every role: an expert's row blocks one
+// after the other on the same features.
+template <int kind>
+struct Walk {
+  static constexpr int kPer = kind == kProdFwdSwiglu ? kTileM / 2 : kTileM;
+  const F8Params& p;
+  const int* cum;  // row blocks of the experts before e
+  long long total;
+  int ftiles, e;
+  __device__ Walk(const F8Params& p_, const int* cum_) : p(p_), cum(cum_), e(0) {
+    const int cols = kind == kProdFwd ? p.N : kind == kProdFwdSwiglu ? p.N / 2 : p.K;
+    ftiles = (cols + kPer - 1) / kPer;
+    total = static_cast<long long>(cum[p.E]) * ftiles;
+  }
+  __device__ __forceinline__ void at(long long t, Tile* o) {
+    while (t >= static_cast<long long>(cum[e + 1]) * ftiles) ++e;
+    const int in = static_cast<int>(t - static_cast<long long>(cum[e]) * ftiles);
+    const int nb = cum[e + 1] - cum[e], b = in % nb;
+    o->e = e;
+    o->f0 = in / nb * kPer;
+    o->off = p.offsets[e];
+    o->cnt = p.counts[e];
+    o->rows = p.offsets[e + 1] - o->off;
+    o->n = ((o->cnt + nb - 1) / nb + 31) & ~31;
+    o->r0 = b * o->n;
+    o->last = b + 1 == nb;
+    if (o->last) o->n = (o->cnt - o->r0 + 31) & ~31;
+  }
+};
+
+__device__ __forceinline__ void scan_row_blocks(const F8Params& p, int* cum, int* part) {
+  int base = 0;
+  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    const int v = block_scan<kThreads>(e < p.E ? row_blocks(p.counts[e]) : 0, part);
+    if (e < p.E) cum[e + 1] = base + v;
+    if (threadIdx.x == kThreads - 1) part[0] = v;
+    __syncthreads();
+    base += part[0];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) cum[0] = 0;
+  __syncthreads();
 }
 
+struct Shared {
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+  uint64_t scales_full[kGroups], scales_empty[kGroups], peer_full[2];
+  uint32_t tmem;
+  int gave_up, ok;
+  int part[32];
+  float ws[kGroups][2][kGroup];  // weight scales: the features', or gate's and up's
+  alignas(16) float peer_max[2][kTileN];  // the other block's largest magnitudes, a buffer for every other tile
+  alignas(16) float as[kGroups][kGroup][kTileN];
+  int cum[EP_MAX_EXPERTS + 1];
+};
+constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * (kABytes + kBBytes) + 2 * kStageWords * 4 + 1024 + sizeof(Shared);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+
+// 16 lanes x 32 columns of the accumulator: word 4 i + j of a lane is row
+// lane / 4 + 8 (j / 2), column 8 i + 2 (lane % 4) + j % 2.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+
+// Two float32 numbers side by side in a register pair.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(uint32_t lo, uint32_t hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
+  return p;
+}
+__device__ __forceinline__ float2 floats_of(Pair p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+  return f;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__host__ __device__ constexpr uint32_t mma_desc_f8(bool a_mn, int m, int n) {  // e4m3 operands, float32 sums
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u)
+      : "memory");
+}
+// MN-major e4m3: a row of 128 features per element of the reduction; 32
+// elements, one mma's share, are 4096 bytes.
+constexpr uint64_t kDescStepMn8 = 4096 >> 4;
+
+__device__ __forceinline__ void store_peer(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// A warp's sums of a tile: columns 32 i + 8 j + 2 (lane % 4) + {0, 1} of its
+// half's, features lane / 4 + {0, 8} of the first (h = 0) and second 16 of its
+// 32 (the gated pair: gate and up of the same features).
+struct Sums {
+  Pair v[4][2][8];  // [i][h][2 j + (feature >= 8)]
+};
+
 template <typename T, int kind>
-__global__ void __launch_bounds__(128) ep_product_f8_kernel(const F8Params p) {
-  __shared__ float part[4];
-  pdl_wait();
-  if (!blocks_ok(p.hdr, p.R)) return;
-  constexpr bool fwd = kind == kProdFwd || kind == kProdFwdSwiglu;
-  const int red = fwd ? p.K : p.N, kb = f8_blocks(p.K), nb = f8_blocks(p.N);
-  const int cols = kind == kProdFwd ? p.N : kind == kProdFwdSwiglu ? p.N / 2 : p.K;
-  const int c = blockIdx.y * 128 + threadIdx.x;
-  int e = 0;
-  for (int r = blockIdx.x; r < p.hdr[kHdrP]; r += gridDim.x) {
-    while (r >= p.offsets[e + 1]) ++e;
-    const bool live = r - p.offsets[e] < p.counts[e];
-    const uint8_t* w = p.w + static_cast<long long>(e) * p.N * p.K;
-    const float* ws = p.ws + static_cast<long long>(e) * nb * kb;
-    const uint8_t* a = p.a + static_cast<long long>(r) * red;
-    const float* as = p.as + static_cast<long long>(r) * scale_columns(red);
-    float s0 = 0.0f, s1 = 0.0f;
-    if (live && c < cols) {
-      for (int b = 0; b < f8_blocks(red); ++b) {
-        float t0 = 0.0f, t1 = 0.0f;
-        for (int i = b * 128; i < min(red, b * 128 + 128); ++i) {
-          const float x = e4m3(a[i]);
-          t0 = fmaf(x, e4m3(fwd ? w[static_cast<long long>(c) * p.K + i] : w[static_cast<long long>(i) * p.K + c]), t0);
-          if (kind == kProdFwdSwiglu) t1 = fmaf(x, e4m3(w[static_cast<long long>(c + cols) * p.K + i]), t1);
-        }
-        s0 = fmaf(t0, as[b] * (fwd ? ws[c / 128 * kb + b] : ws[b * kb + c / 128]), s0);
-        if (kind == kProdFwdSwiglu) s1 = fmaf(t1, as[b] * ws[(c + cols) / 128 * kb + b], s1);
-      }
+struct Epilogue {
+  const F8Params& p;
+  Shared& s;
+  uint32_t* stage;  // of this half
+  int rank, half, w, lane;
+
+  // First row of the tile not to be stored, counted from the half's first.
+  __device__ __forceinline__ int rows_left(const Tile& t, int c0) const { return t.cnt - t.r0 - c0; }
+
+  // 16-bit words of two rows: staged[pair][feature], `features` of them, go to
+  // rows c0 + 2 pair + {0, 1} of the tile.
+  template <int features>
+  __device__ __forceinline__ void store_pairs(const Tile& t, T* out, long long cols, int f, int width, int c0) const {
+    constexpr int stride = features == kHalfM ? kPairStride : kGatedStride, per = 32 / (features / 4);
+    const int l = lane & (features / 4 - 1), sub = lane / (features / 4);
+    const int stop = f + 4 * l < width ? rows_left(t, c0) : 0;
+    T* o = out + (static_cast<long long>(t.off) + t.r0 + c0) * cols + f + 4 * l;
+#pragma unroll
+    for (int i = 0; i < 4; i += per) {
+      const int pair = 4 * w + i + sub;
+      const uint4 q = *reinterpret_cast<const uint4*>(stage + pair * stride + 4 * l);
+      if (2 * pair < stop)
+        __stcs(reinterpret_cast<uint2*>(o + 2 * pair * cols), make_uint2(__byte_perm(q.x, q.y, 0x5410), __byte_perm(q.z, q.w, 0x5410)));
+      if (2 * pair + 1 < stop)
+        __stcs(reinterpret_cast<uint2*>(o + (2 * pair + 1) * cols), make_uint2(__byte_perm(q.x, q.y, 0x7632), __byte_perm(q.z, q.w, 0x7632)));
     }
-    const long long at = static_cast<long long>(r) * cols + c;
-    if constexpr (kind == kProdFwdSwiglu) {
-      const float act = swiglu(s0, s1);
-      if (c < cols) {
-        if (p.pre != nullptr) {
-          static_cast<T*>(p.pre)[static_cast<long long>(r) * p.N + c] = from_f32<T>(s0);
-          static_cast<T*>(p.pre)[static_cast<long long>(r) * p.N + cols + c] = from_f32<T>(s1);
+  }
+
+  __device__ __forceinline__ void plain(const Tile& t, const Sums& a, int nh) const {
+    const int width = kind == kProdFwd ? p.N : p.K, f = t.f0 + rank * kHalfM;
+    uint32_t* put = stage + (lane & 3) * kPairStride + w * 32 + (lane >> 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= nh) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 v = floats_of(a.v[i][h][j]);
+          put[j / 2 * 4 * kPairStride + h * 16 + (j & 1) * 8] = pack2<T>(v.x, v.y);
         }
-        if (p.out != nullptr) static_cast<T*>(p.out)[at] = from_f32<T>(act);
-      }
-      if (p.q != nullptr) {
-        float m = c < cols ? fabsf(act) : 0.0f;
-        for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-        __syncthreads();
-        const BlockScale s = block_scale(max_nan(max_nan(part[0], part[1]), max_nan(part[2], part[3])));
-        __syncthreads();
-        if (c < cols) p.q[at] = live ? static_cast<uint8_t>(e4m3x2(act * s.inv, 0.0f)) : 0;
-        const long long sat = static_cast<long long>(r) * scale_columns(cols);
-        if (threadIdx.x == 0) p.qs[sat + blockIdx.y] = live ? s.scale : 0.0f;
-        if (blockIdx.y == 0 && threadIdx.x >= f8_blocks(cols) && threadIdx.x < scale_columns(cols)) p.qs[sat + threadIdx.x] = 0.0f;
-      }
-    } else if (c < cols) {
-      if constexpr (kind == kProdDgradSwiglu) {
-        const long long i = static_cast<long long>(r) * 2 * cols + c;
-        float dg = 0.0f, du = 0.0f;
-        if (live)
-          swiglu_bwd(to_f32(static_cast<const T*>(p.pre_in)[i]), to_f32(static_cast<const T*>(p.pre_in)[i + cols]), s0, &dg, &du);
-        static_cast<T*>(p.out)[i] = from_f32<T>(dg);
-        static_cast<T*>(p.out)[i + cols] = from_f32<T>(du);
-      } else {
-        static_cast<T*>(p.out)[at] = from_f32<T>(s0);
+      half_sync(half);
+      Tile part = t;
+      part.cnt = min(t.cnt, t.r0 + (half + 1) * nh);  // past the half's columns lies the other half's
+      store_pairs<kHalfM>(part, static_cast<T*>(p.out), width, f, width, half * nh + 32 * i);
+      half_sync(half);
+    }
+  }
+
+  __device__ __forceinline__ void through_activation(const Tile& t, const Sums& a, int nh) const {
+    const int f = t.f0 + rank * kHalfM + 4 * lane;
+    const long long cols = 2LL * p.K;
+    float2* put = reinterpret_cast<float2*>(stage) + (lane & 3) * kPairStride32 + w * 32 + (lane >> 2);
+    const int stop = f < p.K ? min(t.cnt - t.r0, (half + 1) * nh) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= nh) break;
+#pragma unroll
+      for (int j2 = 0; j2 < 2; ++j2) {  // 16 rows at a time
+        const int c0 = half * nh + 32 * i + 16 * j2;
+        uint2 g[4], u[4];
+        const T* pre = static_cast<const T*>(p.pre_in) + (static_cast<long long>(t.off) + t.r0 + c0 + 4 * w) * cols + f;
+        T* out = static_cast<T*>(p.out) + (static_cast<long long>(t.off) + t.r0 + c0 + 4 * w) * cols + f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (c0 + 4 * w + r < stop) {
+            g[r] = __ldg(reinterpret_cast<const uint2*>(pre + r * cols));
+            u[r] = __ldg(reinterpret_cast<const uint2*>(pre + r * cols + p.K));
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) put[j / 2 * 4 * kPairStride32 + h * 16 + (j & 1) * 8] = floats_of(a.v[i][h][4 * j2 + j]);
+        half_sync(half);
+        float x[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float2*>(stage) + (2 * w + r / 2) * kPairStride32 + 4 * lane);
+          const float4 lo = q[0], hi = q[1];
+          x[r][0] = lo.x; x[r + 1][0] = lo.y; x[r][1] = lo.z; x[r + 1][1] = lo.w;
+          x[r][2] = hi.x; x[r + 1][2] = hi.y; x[r][3] = hi.z; x[r + 1][3] = hi.w;
+        }
+        half_sync(half);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (c0 + 4 * w + r < stop) {
+            const float4 gv = unpack4<T>(g[r]), uv = unpack4<T>(u[r]);
+            const float gs[4] = {gv.x, gv.y, gv.z, gv.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
+            float dg[4], du[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float sg = fast_sigmoid(gs[k]);
+              dg[k] = x[r][k] * us[k] * sg * (1.0f + gs[k] * (1.0f - sg));
+              du[k] = x[r][k] * gs[k] * sg;
+            }
+            store4(out + r * cols, make_float4(dg[0], dg[1], dg[2], dg[3]));
+            store4(out + r * cols + p.K, make_float4(du[0], du[1], du[2], du[3]));
+          }
       }
     }
   }
+
+  // `turn`: which of the two buffers this tile's exchange uses; `parity` its phase.
+  __device__ __forceinline__ void gated(const Tile& t, Sums& a, int nh, int turn, uint32_t parity) const {
+    const int F = p.N / 2, f = t.f0 + rank * (kHalfM / 2);
+    Tile part = t;
+    part.cnt = min(t.cnt, t.r0 + (half + 1) * nh);
+    if (p.pre != nullptr) {
+      uint32_t* put = stage + (lane & 3) * kGatedStride + w * 16 + (lane >> 2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (32 * i >= nh) break;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 v = floats_of(a.v[i][h][j]);
+            put[j / 2 * 4 * kGatedStride + (j & 1) * 8] = pack2<T>(v.x, v.y);
+          }
+          half_sync(half);
+          store_pairs<kHalfM / 2>(part, static_cast<T*>(p.pre) + h * F, p.N, f, F, half * nh + 32 * i);
+          half_sync(half);
+        }
+    }
+    // The activation takes the place of the gate's sums.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= nh) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 g = floats_of(a.v[i][0][j]), u = floats_of(a.v[i][1][j]);
+        a.v[i][0][j] = pair_of(__float_as_uint(g.x * fast_sigmoid(g.x) * u.x), __float_as_uint(g.y * fast_sigmoid(g.y) * u.y));
+      }
+    }
+    if (p.out != nullptr) {
+      uint32_t* put = stage + (lane & 3) * kGatedStride + w * 16 + (lane >> 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (32 * i >= nh) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 v = floats_of(a.v[i][0][j]);
+          put[j / 2 * 4 * kGatedStride + (j & 1) * 8] = pack2<T>(v.x, v.y);
+        }
+        half_sync(half);
+        store_pairs<kHalfM / 2>(part, static_cast<T*>(p.out), F, f, F, half * nh + 32 * i);
+        half_sync(half);
+      }
+    }
+    if (p.q == nullptr) return;
+    // Largest magnitudes: over this warp's 16 features, the half's four warps,
+    // then the other block's 64 features.
+    float* most = reinterpret_cast<float*>(stage);  // [4 warps][128 columns], then [128]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= nh) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = floats_of(a.v[i][0][2 * j]), y = floats_of(a.v[i][0][2 * j + 1]);
+        float m0 = max_nan(fabsf(x.x), fabsf(y.x)), m1 = max_nan(fabsf(x.y), fabsf(y.y));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          m0 = max_nan(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+          m1 = max_nan(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+        }
+        if (lane < 4) *reinterpret_cast<float2*>(most + w * kHalfN + 32 * i + 8 * j + 2 * lane) = make_float2(m0, m1);
+      }
+    }
+    half_sync(half);
+    {
+      const int c = w * 32 + lane;
+      float m = 0.0f;
+      if (c < nh) {
+        m = max_nan(max_nan(most[c], most[kHalfN + c]), max_nan(most[2 * kHalfN + c], most[3 * kHalfN + c]));
+        store_peer(tc::in_block(tc::smem_addr(&s.peer_max[turn][half * nh + c]), rank ^ 1), m);
+      }
+      half_sync(half);
+      most[c] = m;
+      if (threadIdx.x % 128 == 0) tc::mbar_publish_cluster(tc::in_block(tc::smem_addr(&s.peer_full[half]), rank ^ 1));
+      half_sync(half);
+    }
+    tc::mbar_wait<true>(tc::smem_addr(&s.peer_full[half]), parity, &s.gave_up);
+    const float* other = s.peer_max[turn] + half * nh;
+    float m_scale[4][4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= nh) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 32 * i + 8 * j + 2 * (lane & 3);
+        const float2 x = *reinterpret_cast<const float2*>(most + c), y = *reinterpret_cast<const float2*>(other + c);
+        const BlockScale b0 = block_scale(max_nan(x.x, y.x)), b1 = block_scale(max_nan(x.y, y.y));
+        m_scale[i][j][0] = b0.inv;
+        m_scale[i][j][1] = b1.inv;
+        if (rank == 0 && w == 0 && lane < 4) {
+          float* qs = p.qs + (static_cast<long long>(t.off) + t.r0 + half * nh + c) * scale_columns(F) + t.f0 / kF8Block;
+          const int stop = part.cnt - t.r0 - half * nh;
+          if (c < stop) qs[0] = b0.scale;
+          if (c + 1 < stop) qs[scale_columns(F)] = b1.scale;
+          if (t.f0 + kF8Block >= F)
+            for (int k = 1; t.f0 / kF8Block + k < scale_columns(F); ++k) {
+              if (c < stop) qs[k] = 0.0f;
+              if (c + 1 < stop) qs[scale_columns(F) + k] = 0.0f;
+            }
+        }
+      }
+    }
+    half_sync(half);  // read: `most` gives way to the values
+    // Two rows' bytes of a feature are a half word: staged[pair][64 features], 144 bytes apart.
+    unsigned short* put = reinterpret_cast<unsigned short*>(stage) + (lane & 3) * 72 + w * 16 + (lane >> 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= nh) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 v = floats_of(a.v[i][0][j]);
+        put[j / 2 * 4 * 72 + (j & 1) * 8] = static_cast<unsigned short>(e4m3x2(v.x * m_scale[i][j / 2][0], v.y * m_scale[i][j / 2][1]));
+      }
+      half_sync(half);
+      {
+        const int pair = 4 * w + (lane >> 3), l = lane & 7, c0 = half * nh + 32 * i;
+        const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(stage) + pair * 144 + 16 * l);
+        uint8_t* o = p.q + (static_cast<long long>(t.off) + t.r0 + c0 + 2 * pair) * F + f + 8 * l;
+        const int stop = part.cnt - t.r0 - c0;
+        if (2 * pair < stop) __stcs(reinterpret_cast<uint2*>(o), make_uint2(__byte_perm(q.x, q.y, 0x6420), __byte_perm(q.z, q.w, 0x6420)));
+        if (2 * pair + 1 < stop) __stcs(reinterpret_cast<uint2*>(o + F), make_uint2(__byte_perm(q.x, q.y, 0x7531), __byte_perm(q.z, q.w, 0x7531)));
+      }
+      half_sync(half);
+    }
+  }
+
+  // Padding rows [cnt, rows) of the expert, the tile's features: zeros.
+  __device__ __forceinline__ void zero_rows(const Tile& t) const {
+    const int from = t.cnt + half * 4 + w;
+    if constexpr (kind == kProdFwdSwiglu) {
+      const int F = p.N / 2, f = t.f0 + rank * (kHalfM / 2) + 4 * (lane & 15);
+      for (int r = from; r < t.rows; r += kEpilogueWarps) {
+        const long long row = static_cast<long long>(t.off) + r;
+        if (lane < 16) {
+          if (p.out != nullptr) *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * F + f) = make_uint2(0, 0);
+          if (p.q != nullptr) *reinterpret_cast<uint32_t*>(p.q + row * F + f) = 0;
+        }
+        if (p.pre != nullptr) *reinterpret_cast<uint2*>(static_cast<T*>(p.pre) + row * p.N + (lane >> 4) * F + f) = make_uint2(0, 0);
+        if (p.q != nullptr && rank == 0 && t.f0 == 0)
+          for (int b = lane; b < scale_columns(F); b += 32) p.qs[row * scale_columns(F) + b] = 0.0f;
+      }
+    } else {
+      const int width = kind == kProdFwd ? p.N : p.K, f = t.f0 + rank * kHalfM + 4 * lane;
+      if (f >= width) return;
+      const long long cols = kind == kProdDgradSwiglu ? 2LL * width : width;
+      for (int r = from; r < t.rows; r += kEpilogueWarps) {
+        T* o = static_cast<T*>(p.out) + (static_cast<long long>(t.off) + r) * cols + f;
+        *reinterpret_cast<uint2*>(o) = make_uint2(0, 0);
+        if (kind == kProdDgradSwiglu) *reinterpret_cast<uint2*>(o + width) = make_uint2(0, 0);
+      }
+    }
+  }
+};
+
+template <typename T, int kind>
+__global__ void __launch_bounds__(kThreads, 1)
+    ep_product_f8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                         const __grid_constant__ CUtensorMap map_b64, const __grid_constant__ CUtensorMap map_b32,
+                         const __grid_constant__ CUtensorMap map_b16, const F8Params p) {
+  constexpr bool fwd = kind == kProdFwd || kind == kProdFwdSwiglu;
+  extern __shared__ unsigned char raw[];
+  unsigned char* ring = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
+  uint32_t* staging = reinterpret_cast<uint32_t*>(ring + static_cast<size_t>(kStages) * (kABytes + kBBytes));
+  Shared& s = *reinterpret_cast<Shared*>(staging + 2 * kStageWords);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(tc::cluster_rank());
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch_desc(&map_a);
+    tc::tma_prefetch_desc(&map_b);
+    tc::tma_prefetch_desc(&map_b16);
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(tc::smem_addr(&s.full[i]), 2);  // the first block's two loaders account for both blocks' copies
+      tc::mbar_init(tc::smem_addr(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_addr(&s.acc_full[i]), 1);
+      tc::mbar_init(tc::smem_addr(&s.acc_empty[i]), 2 * kEpilogueWarps);
+      tc::mbar_init(tc::smem_addr(&s.peer_full[i]), 1);
+    }
+    for (int i = 0; i < kGroups; ++i) {
+      tc::mbar_init(tc::smem_addr(&s.scales_full[i]), 32);
+      tc::mbar_init(tc::smem_addr(&s.scales_empty[i]), kEpilogueWarps);
+    }
+    tc::mbar_init(tc::smem_addr(&s.drained), 1);
+    tc::mbar_init_fence();
+    s.gave_up = 0;
+  }
+  if (warp == 2) tc::tmem_alloc(tc::smem_addr(&s.tmem), 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after();
+  const uint32_t tmem = s.tmem;
+  pdl_wait();
+  if (threadIdx.x == 0) s.ok = blocks_ok(p.hdr, p.R);
+  __syncthreads();
+  const bool ok = s.ok;
+  if (ok) scan_row_blocks(p, s.cum, s.part);
+  const int red = fwd ? p.K : p.N, slabs = (red + kSlab - 1) / kSlab;
+  volatile int* gave_up = &s.gave_up;
+  const long long first = blockIdx.x / 2, step = gridDim.x / 2;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (ok) {
+      Walk<kind> walk(p, s.cum);
+      Tile t;
+      if (warp == 0 || warp == 2) {
+        if (lane == 0) {
+          const bool load_a = warp == 0;
+          int stage = 0;
+          uint32_t phase = 0;
+          for (long long i = first; i < walk.total && !*gave_up; i += step) {
+            walk.at(i, &t);
+            const int half = t.n / 2;  // this block's rows
+            const int bytes = load_a ? kABytes : (half > 64 ? 128 : half > 32 ? 64 : half > 16 ? 32 : 16) * kSlab;
+            for (int k = 0; k < slabs; ++k) {
+              if (!tc::mbar_wait(tc::smem_addr(&s.empty[stage]), phase ^ 1, gave_up)) break;
+              const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * (kABytes + kBBytes)), b = a + kABytes;
+              const uint32_t bar = rank == 0 ? tc::smem_addr(&s.full[stage]) : tc::in_block(tc::smem_addr(&s.full[stage]), 0);
+              if (rank == 0) tc::mbar_expect(bar, 2 * bytes);  // the other block's copies too
+              const int x = k * kSlab;
+              if (load_a) {
+                if constexpr (kind == kProdFwd) {
+                  tc::tma_pair_3d(a, &map_a, bar, x, t.f0 + rank * kHalfM, t.e);
+                } else if constexpr (kind == kProdFwdSwiglu) {
+                  for (int j = 0; j < 4; ++j)  // 16 gate rows, then the up rows of the same features
+                    tc::tma_pair_4d(a + j * (kABytes / 4), &map_a, bar, x, t.f0 + rank * (kHalfM / 2) + j * 16, 0, t.e);
+                } else {
+                  tc::tma_pair_3d(a, &map_a, bar, t.f0 + rank * kHalfM, x, t.e);
+                }
+              } else {
+                tc::tma_pair_2d(b, half > 64 ? &map_b : half > 32 ? &map_b64 : half > 16 ? &map_b32 : &map_b16, bar, x,
+                                t.off + t.r0 + rank * half);
+              }
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+          }
+          if (load_a) pdl_trigger();
+          // Every stage is read out before the block ends.
+          for (int j = 0; j < kStages && !*gave_up; ++j) {
+            if (!tc::mbar_wait(tc::smem_addr(&s.empty[stage]), phase ^ 1, gave_up)) break;
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          // After a wait that gave up, the copies in flight land before the
+          // block's shared memory goes; a copy takes microseconds.
+          if (*gave_up) {
+            const unsigned long long start = tc::now_ns();
+            while (tc::now_ns() - start < tc::kWaitNs / 100) {
+            }
+          }
+        }
+      } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+          int stage = 0, buf = 0;
+          uint32_t phase = 0, acc_phase = 0;
+          bool lost = false;
+          for (long long i = first; i < walk.total && !lost; i += step) {
+            walk.at(i, &t);
+            const uint32_t desc = mma_desc_f8(!fwd, kTileM, t.n);
+            for (int k = 0; k < slabs; ++k) {
+              lost = !tc::mbar_wait(tc::smem_addr(&s.acc_empty[buf]), acc_phase ^ 1, gave_up) ||
+                     !tc::mbar_wait(tc::smem_addr(&s.full[stage]), phase, gave_up);
+              if (lost) break;
+              tc::fence_after();
+              const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * (kABytes + kBBytes)), b = a + kABytes;
+              const uint64_t da = fwd ? tc::desc_k_major(a) : tc::desc_mn_major(a, kABytes);
+              const uint64_t db = tc::desc_k_major(b);
+              const int left = red - k * kSlab;
+#pragma unroll
+              for (int q = 0; q < kSlab / 32; ++q)
+                if (q * 32 < left)
+                  mma_f8(tmem + buf * kTileN, da + q * (fwd ? tc::kDescStepK : kDescStepMn8), db + q * tc::kDescStepK, desc, q > 0);
+              tc::mma_commit(tc::smem_addr(&s.empty[stage]));
+              tc::mma_commit(tc::smem_addr(&s.acc_full[buf]));
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+              }
+              buf ^= 1;
+              if (buf == 0) acc_phase ^= 1;
+            }
+          }
+          if (lost) {
+            // What was issued ends before tensor memory is freed.
+            tc::mma_commit(tc::smem_addr(&s.drained));
+            const unsigned long long start = tc::now_ns();
+            while (!tc::mbar_try(tc::smem_addr(&s.drained), 0) && tc::now_ns() - start < tc::kWaitNs) {
+            }
+          }
+        }
+      } else {
+        // Scales of four slabs: lane l brings rows l, l + 32, ...
+        int slot = 0;
+        uint32_t phase = 0;
+        const int cols = scale_columns(red), kb = f8_blocks(p.K), nb = f8_blocks(p.N);
+        for (long long i = first; i < walk.total && !*gave_up; i += step) {
+          walk.at(i, &t);
+          const int row0 = t.off + t.r0;
+          const int fb = min((t.f0 + (kind == kProdFwdSwiglu ? rank * (kHalfM / 2) : rank * kHalfM)) / kF8Block, (fwd ? nb : kb) - 1);
+          const float* ws = p.ws + static_cast<long long>(t.e) * nb * kb;
+          for (int k = 0; k < slabs; k += kGroup) {
+            float4 v[kTileN / 32];
+#pragma unroll
+            for (int j = 0; j < kTileN / 32; ++j) {
+              const int r = j * 32 + lane;
+              v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (r < t.n && row0 + r < p.R) v[j] = __ldg(reinterpret_cast<const float4*>(p.as + static_cast<long long>(row0 + r) * cols + k));
+            }
+            float w = 0.0f;
+            const int b = k + (lane & 3), up = lane >> 2;  // lanes 4 to 7: the up rows' scales
+            if (up < (kind == kProdFwdSwiglu ? 2 : 1) && b < slabs)
+              w = __ldg(ws + (fwd ? static_cast<long long>(fb + up * (nb / 2)) * kb + b : static_cast<long long>(b) * kb + fb));
+            if (!tc::mbar_wait(tc::smem_addr(&s.scales_empty[slot]), phase ^ 1, gave_up)) break;
+#pragma unroll
+            for (int j = 0; j < kTileN / 32; ++j) {
+              s.as[slot][0][j * 32 + lane] = v[j].x;
+              s.as[slot][1][j * 32 + lane] = v[j].y;
+              s.as[slot][2][j * 32 + lane] = v[j].z;
+              s.as[slot][3][j * 32 + lane] = v[j].w;
+            }
+            if (lane < 8) s.ws[slot][up][lane & 3] = w;
+            tc::mbar_arrive(tc::smem_addr(&s.scales_full[slot]));
+            if (++slot == kGroups) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    if (ok) {
+      Walk<kind> walk(p, s.cum);
+      Tile t;
+      const int half = (warp - 4) >> 2, w = warp & 3;  // the accumulator lanes a warp can reach go by its number
+      const Epilogue<T, kind> out{p, s, staging + half * kStageWords, rank, half, w, lane};
+      int buf = 0, slot = 0, turn = 0;
+      uint32_t acc_phase = 0, scale_phase = 0, peer_phase = 0;
+      // A wait that gave up leaves its warp in step with the others, with
+      // nothing of use in its sums: every later wait ends at once.
+      for (long long i = first; i < walk.total; i += step) {
+        walk.at(i, &t);
+        const int nh = t.n / 2;
+        Sums a;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a.v[c][h][j] = 0;
+#pragma unroll 1
+        for (int k = 0; k < slabs; ++k) {
+          if ((k & (kGroup - 1)) == 0) tc::mbar_wait(tc::smem_addr(&s.scales_full[slot]), scale_phase, gave_up);
+          const float w0 = s.ws[slot][0][k & (kGroup - 1)], w1 = kind == kProdFwdSwiglu ? s.ws[slot][1][k & (kGroup - 1)] : w0;
+          const Pair w0p = pair_of(__float_as_uint(w0), __float_as_uint(w0)), w1p = pair_of(__float_as_uint(w1), __float_as_uint(w1));
+          const float* as = &s.as[slot][k & (kGroup - 1)][half * nh + 2 * (lane & 3)];
+          tc::mbar_wait(tc::smem_addr(&s.acc_full[buf]), acc_phase, gave_up);
+          __syncwarp();
+          tc::fence_after();
+          const uint32_t acc = tmem + buf * kTileN + half * nh + (static_cast<uint32_t>(w * 32) << 16);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (32 * c < nh) {
+              uint32_t r0[16], r1[16];
+              tmem_ld_rows(acc + 32 * c, r0);
+              tmem_ld_rows(acc + 32 * c + (16u << 16), r1);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const Pair x = *reinterpret_cast<const Pair*>(as + 32 * c + 8 * j);
+                const Pair x0 = mul2(x, w0p), x1 = kind == kProdFwdSwiglu ? mul2(x, w1p) : x0;
+                a.v[c][0][2 * j] = fma2(pair_of(r0[4 * j], r0[4 * j + 1]), x0, a.v[c][0][2 * j]);
+                a.v[c][0][2 * j + 1] = fma2(pair_of(r0[4 * j + 2], r0[4 * j + 3]), x0, a.v[c][0][2 * j + 1]);
+                a.v[c][1][2 * j] = fma2(pair_of(r1[4 * j], r1[4 * j + 1]), x1, a.v[c][1][2 * j]);
+                a.v[c][1][2 * j + 1] = fma2(pair_of(r1[4 * j + 2], r1[4 * j + 3]), x1, a.v[c][1][2 * j + 1]);
+              }
+            }
+          }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive_cluster(tc::in_block(tc::smem_addr(&s.acc_empty[buf]), 0));
+            if ((k & (kGroup - 1)) == kGroup - 1 || k + 1 == slabs) tc::mbar_arrive(tc::smem_addr(&s.scales_empty[slot]));
+          }
+          buf ^= 1;
+          if (buf == 0) acc_phase ^= 1;
+          if ((k & (kGroup - 1)) == kGroup - 1 || k + 1 == slabs) {
+            if (++slot == kGroups) {
+              slot = 0;
+              scale_phase ^= 1;
+            }
+          }
+        }
+        if constexpr (kind == kProdFwdSwiglu) {
+          out.gated(t, a, nh, turn, peer_phase);
+          turn ^= 1;
+          peer_phase ^= 1;
+        } else if constexpr (kind == kProdDgradSwiglu) {
+          out.through_activation(t, a, nh);
+        } else {
+          out.plain(t, a, nh);
+        }
+        if (t.last) out.zero_rows(t);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && s.gave_up) atomicOr(&p.hdr[kHdrStatus], static_cast<int>(EP_ST_TIMEOUT));
+  tc::cluster_sync();  // neither block leaves while the other may reach into it
+  tc::fence_after();
+  if (warp == 2) tc::tmem_free(tmem, 512);
+}
+
+// A map of [dim 3]..[dim 1][dim 0] bytes.
+bool make_map(CUtensorMap* m, const void* base, int dims, const long long (&size)[4], const long long (&stride)[3],
+              const int (&box)[4]) {
+  const tc::EncodeFn f = tc::tensor_map_encoder();
+  if (f == nullptr) return false;
+  cuuint64_t sz[4], st[3];
+  cuuint32_t bx[4];
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < dims; ++i) {
+    sz[i] = static_cast<cuuint64_t>(size[i]);
+    bx[i] = static_cast<cuuint32_t>(box[i]);
+    if (i + 1 < dims) st[i] = static_cast<cuuint64_t>(stride[i]);
+  }
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(dims), const_cast<void*>(base), sz, st, bx, one,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs of blocks that fit on the current device at once (0: the query
+// failed); the kernel's shared memory is raised on the way.  Once per device.
+template <typename T, int kind>
+int resident_pairs(int num_sms) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  int pairs = known[dev].load(std::memory_order_acquire);
+  if (pairs == 0) {
+    const auto kern = ep_product_f8_kernel<T, kind>;
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes)) != cudaSuccess)
+      return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs < 1) return 0;
+    pairs = std::min(pairs, num_sms / 2);
+    known[dev].store(pairs, std::memory_order_release);
+  }
+  return pairs;
+}
+
+template <typename T, int kind>
+cudaError_t launch_kind(const F8Params& p, int num_sms, cudaStream_t s) {
+  CUtensorMap a, b, b64, b32, b16;
+  constexpr bool fwd = kind == kProdFwd || kind == kProdFwdSwiglu;
+  const long long K = p.K, N = p.N, red = fwd ? K : N, F = N / 2;
+  bool ok = kind == kProdFwdSwiglu ? make_map(&a, p.w, 4, {K, F, 2, p.E}, {K, F * K, 2 * F * K}, {kSlab, 16, 2, 1})
+                                   : make_map(&a, p.w, 3, {K, N, p.E, 1}, {K, N * K, 0}, {kSlab, 128, 1, 1});
+  CUtensorMap* maps[4] = {&b, &b64, &b32, &b16};
+  for (int i = 0; i < 4; ++i) ok = ok && make_map(maps[i], p.a, 2, {red, p.R, 1, 1}, {red, 0, 0}, {kSlab, 128 >> i, 1, 1});
+  if (!ok) return cudaErrorInvalidValue;
+  const int pairs = resident_pairs<T, kind>(num_sms);
+  if (pairs == 0) return cudaErrorLaunchOutOfResources;
+  return launch_pdl(ep_product_f8_kernel<T, kind>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, 2, a, b, b64, b32, b16, p);
 }
 
 template <typename T>
-cudaError_t launch_typed(const F8Params& p, cudaStream_t s) {
-  const int cols = p.kind == kProdFwd ? p.N : p.kind == kProdFwdSwiglu ? p.N / 2 : p.K;
-  const dim3 grid(p.R < 4096 ? p.R : 4096, (cols + 127) / 128), block(128);
+cudaError_t launch_typed(const F8Params& p, int num_sms, cudaStream_t s) {
   switch (p.kind) {
-    case kProdFwd: return launch_pdl(ep_product_f8_kernel<T, kProdFwd>, grid, block, 0, s, 0, p);
-    case kProdFwdSwiglu: return launch_pdl(ep_product_f8_kernel<T, kProdFwdSwiglu>, grid, block, 0, s, 0, p);
-    case kProdDgrad: return launch_pdl(ep_product_f8_kernel<T, kProdDgrad>, grid, block, 0, s, 0, p);
-    default: return launch_pdl(ep_product_f8_kernel<T, kProdDgradSwiglu>, grid, block, 0, s, 0, p);
+    case kProdFwd: return launch_kind<T, kProdFwd>(p, num_sms, s);
+    case kProdFwdSwiglu: return launch_kind<T, kProdFwdSwiglu>(p, num_sms, s);
+    case kProdDgrad: return launch_kind<T, kProdDgrad>(p, num_sms, s);
+    default: return launch_kind<T, kProdDgradSwiglu>(p, num_sms, s);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_product_f8(const F8Params& p, int, cudaStream_t s) {
-  if (p.dtype == EP_DTYPE_FP16) return launch_typed<__half>(p, s);
-  return launch_typed<__nv_bfloat16>(p, s);
+cudaError_t launch_product_f8(const F8Params& p, int num_sms, cudaStream_t s) {
+  if (p.dtype == EP_DTYPE_FP16) return launch_typed<__half>(p, num_sms, s);
+  return launch_typed<__nv_bfloat16>(p, num_sms, s);
 }
 
 }  // namespace ep
