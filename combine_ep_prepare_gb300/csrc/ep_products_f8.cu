@@ -39,11 +39,15 @@ constexpr int kThreads = (4 + kEpilogueWarps) * 32;
 constexpr int kTileM = 256, kTileN = 256, kSlab = 128;  // of the pair
 constexpr int kHalfM = kTileM / 2, kHalfN = kTileN / 2;
 constexpr int kABytes = kHalfM * kSlab, kBBytes = kHalfN * kSlab;
-constexpr int kStages = 6;
+// The ring: stages of the features' 16 KB and of the rows' as many bytes as the
+// largest tile needs, so that more are in flight where there are few rows.
+constexpr int kRingBytes = 6 * (kABytes + kBBytes), kMaxStages = 10;
+__device__ __forceinline__ int box_rows(int half) { return half > 64 ? 128 : half > 32 ? 64 : half > 16 ? 32 : 16; }
 constexpr int kGroup = 4, kGroups = 2;  // slabs whose scales come together; groups in flight
+constexpr int kSlots = 8, kSlotColumns = 512 / kSlots;  // of tensor memory; an accumulator takes 1, 2 or 4
 // Registers of a loading warp and of an adding one: 128 threads of the first
 // and 256 of the second have what 384 x 168 gave them.
-constexpr int kFewRegs = 88, kManyRegs = 208;
+constexpr int kFewRegs = 72, kManyRegs = 216;
 static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "more registers than the block is launched with");
 // Staging of one half of the epilogue, in words: 16 pairs of rows x 128
 // features, or eight pairs in float32.  The paddings keep the lanes of a
@@ -89,11 +93,14 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ void scan_row_blocks(const F8Params& p, int* cum, int* part) {
+// cum[e] = row blocks of the experts before e; *most (0 before) the rows of the largest expert.
+__device__ __forceinline__ void scan_row_blocks(const F8Params& p, int* cum, int* part, int* most) {
   int base = 0;
   for (int e0 = 0; e0 < p.E; e0 += kThreads) {
     const int e = e0 + static_cast<int>(threadIdx.x);
-    const int v = block_scan<kThreads>(e < p.E ? row_blocks(p.counts[e]) : 0, part);
+    const int cnt = e < p.E ? p.counts[e] : 0;
+    if (cnt > 0) atomicMax(most, cnt);
+    const int v = block_scan<kThreads>(row_blocks(cnt), part);
     if (e < p.E) cum[e + 1] = base + v;
     if (threadIdx.x == kThreads - 1) part[0] = v;
     __syncthreads();
@@ -104,69 +111,91 @@ __device__ __forceinline__ void scan_row_blocks(const F8Params& p, int* cum, int
   __syncthreads();
 }
 
+// The accumulators in tensor memory: tiles of few rows have up to eight in
+// turn, which covers the way from an mma's end over the adding warps and back.
+// Where the width changes the walk begins again at the first one.
+struct Slots {
+  int width, at;
+  uint32_t phases;  // a bit for each slot's barriers
+  __device__ __forceinline__ Slots() : width(0), at(0), phases(0) {}
+  static __device__ __forceinline__ int of(int n) { return n > 2 * kSlotColumns ? 4 : n > kSlotColumns ? 2 : 1; }
+  __device__ __forceinline__ uint32_t phase() const { return phases >> at & 1; }
+  __device__ __forceinline__ void next() {
+    phases ^= 1u << at;
+    at = (at + width) & (kSlots - 1);
+  }
+};
+
 struct Shared {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kSlots], acc_empty[kSlots], drained;
   uint64_t scales_full[kGroups], scales_empty[kGroups], peer_full[2];
   uint32_t tmem;
-  int gave_up, ok;
+  int gave_up, ok, most;  // most: rows of the largest tile
   int part[32];
   float ws[kGroups][2][kGroup];  // weight scales: the features', or gate's and up's
   alignas(16) float peer_max[2][kTileN];  // the other block's largest magnitudes, a buffer for every other tile
   alignas(16) float as[kGroups][kGroup][kTileN];
   int cum[EP_MAX_EXPERTS + 1];
 };
-constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * (kABytes + kBBytes) + 2 * kStageWords * 4 + 1024 + sizeof(Shared);
+constexpr size_t kSmemBytes = static_cast<size_t>(kRingBytes) + 2 * kStageWords * 4 + 1024 + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// A wait of the whole warp: true when every lane's was.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, gave_up));
+}
 
 __device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
-// 16 lanes x 32 columns of the accumulator: word 4 i + j of a lane is row
+// 16 lanes x 16 columns of the accumulator: word 4 i + j of a lane is row
 // lane / 4 + 8 (j / 2), column 8 i + 2 (lane % 4) + j % 2.
-__device__ __forceinline__ void tmem_ld_rows(uint32_t addr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
+__device__ __forceinline__ void tmem_ld_rows(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
 }
 
-// Two float32 numbers side by side in a register pair.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair_of(uint32_t lo, uint32_t hi) {
-  Pair p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
-  return p;
-}
-__device__ __forceinline__ float2 floats_of(Pair p) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
-  return f;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
+// Waits for the loads so far; what is computed from these words stays behind it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[2][8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]), "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]),
+                 "+r"(r[1][0]), "+r"(r[1][1]), "+r"(r[1][2]), "+r"(r[1][3]), "+r"(r[1][4]), "+r"(r[1][5]), "+r"(r[1][6]), "+r"(r[1][7]));
 }
 
 __host__ __device__ constexpr uint32_t mma_desc_f8(bool a_mn, int m, int n) {  // e4m3 operands, float32 sums
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u)
-      : "memory");
-}
 // MN-major e4m3: a row of 128 features per element of the reduction; 32
 // elements, one mma's share, are 4096 bytes.
 constexpr uint64_t kDescStepMn8 = 4096 >> 4;
+
+// A slab's four mma into accumulator d, and what arrives after them: `empty`
+// for the stage, `full` for the accumulator, in both blocks.  The whole warp
+// calls it and one lane issues: outside a divergent branch the compiler keeps
+// descriptors and addresses in uniform registers, where the instructions want
+// them.  (From one lane's branch the issuing thread took 890 clocks a slab.)
+template <uint64_t a_step>
+__device__ __forceinline__ void mma_slab(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t empty, uint32_t full) {
+  asm volatile(
+      "{\n .reg .pred e, no, yes;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " setp.ne.u32 no, 0, 0;\n setp.eq.u32 yes, 0, 0;\n"
+      " add.u64 a1, %1, %6;\n add.u64 a2, a1, %6;\n add.u64 a3, a2, %6;\n"
+      " add.u64 b1, %2, %7;\n add.u64 b2, b1, %7;\n add.u64 b3, b2, %7;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, no;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, yes;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, yes;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, yes;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], %8;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], %8;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(empty), "r"(full), "n"(a_step), "n"(tc::kDescStepK), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ bool elect() {
+  uint32_t is;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(is));
+  return is != 0;
+}
 
 __device__ __forceinline__ void store_peer(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -176,8 +205,126 @@ __device__ __forceinline__ void store_peer(uint32_t addr, float v) {
 // half's, features lane / 4 + {0, 8} of the first (h = 0) and second 16 of its
 // 32 (the gated pair: gate and up of the same features).
 struct Sums {
-  Pair v[4][2][8];  // [i][h][2 j + (feature >= 8)]
+  float2 v[4][2][8];  // [i][h][2 j + (feature >= 8)]
 };
+
+// Where the adding warps are in the rings.
+struct Turn {
+  Slots slots;
+  int slot = 0;  // of the scales
+  uint32_t phase = 0;
+};
+
+// Of a tile's slabs, what an adding warp has of the one at hand.
+struct Slab {
+  uint32_t acc;     // its part of the accumulator
+  const float* as;  // the rows' scales from this lane's first on
+  float w0, w1;     // gated: the weights' scales
+  float4 x;         // the rows' scales of the 16 columns to come
+};
+
+// A tile's slabs, one after the other: 16 times `chunks` columns of the
+// accumulator times the scales, to the sums.  While sixteen columns are added
+// the next ones and their scales are loaded; when all are in registers the
+// accumulator is handed back.  (With the width known here there is no branch
+// between loads and sums, and the sums keep their registers.)
+//
+// A wait that gave up leaves its warp in step with the others, with nothing of
+// use in its sums: every later wait ends at once.
+template <int kind, int chunks>
+struct Adder {
+  Sums& a;
+  Shared& s;
+  Turn& turn;
+  uint32_t tmem, empty;  // empty: the first block's barriers of the accumulators
+  int lane, slabs, first_column;
+  Slab now;
+  uint32_t r[2][2][8];
+
+  // Slab k's accumulator is there: its first columns are on their way to r[0].
+  __device__ __forceinline__ void begin(int k) {
+    volatile int* gave_up = &s.gave_up;
+    const int in = k & (kGroup - 1);
+    if (in == 0) tc::mbar_wait(tc::smem_addr(&s.scales_full[turn.slot]), turn.phase, gave_up);
+    if constexpr (kind == kProdFwdSwiglu) {
+      now.w0 = s.ws[turn.slot][0][in];
+      now.w1 = s.ws[turn.slot][1][in];
+    }
+    now.as = &s.as[turn.slot][in][first_column + 4 * (lane & 3)];
+    now.x = *reinterpret_cast<const float4*>(now.as);
+    tc::mbar_wait(tc::smem_addr(&s.acc_full[turn.slots.at]), turn.slots.phase(), gave_up);
+    __syncwarp();
+    tc::fence_after();
+    now.acc = tmem + turn.slots.at * kSlotColumns;
+    load(0);
+  }
+  __device__ __forceinline__ void load(int c) {
+    tmem_ld_rows(now.acc + 16 * c, r[c & 1][0]);
+    tmem_ld_rows(now.acc + 16 * c + (16u << 16), r[c & 1][1]);
+  }
+  // Slab k's accumulator and, with its last slab, the scales' slot are read.
+  __device__ __forceinline__ void end(int k) {
+    tc::fence_before();
+    __syncwarp();
+    const bool ends = (k & (kGroup - 1)) == kGroup - 1 || k + 1 == slabs;
+    if (lane == 0) {
+      tc::mbar_arrive_cluster(empty + 8 * turn.slots.at);
+      if (ends) tc::mbar_arrive(tc::smem_addr(&s.scales_empty[turn.slot]));
+    }
+    turn.slots.next();
+    if (ends && ++turn.slot == kGroups) {
+      turn.slot = 0;
+      turn.phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void slab(int k) {
+    begin(k);
+#pragma unroll
+    for (int c = 0; c < chunks; ++c) {
+      tmem_ld_wait(r[c & 1]);
+      const float4 x = now.x;
+      const float w0 = now.w0, w1 = now.w1;
+      if (c + 1 < chunks) {
+        load(c + 1);
+        now.x = *reinterpret_cast<const float4*>(now.as + 16 * (c + 1));
+      } else {
+        end(k);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t (&v)[8] = r[c & 1][h];
+        const float2 w = h == 0 ? make_float2(w0, w0) : make_float2(w1, w1);
+        float2 x0 = make_float2(x.x, x.y), x1 = make_float2(x.z, x.w);
+        if (kind == kProdFwdSwiglu) {
+          x0 = __fmul2_rn(x0, w);
+          x1 = __fmul2_rn(x1, w);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2& sum = a.v[c / 2][h][4 * (c & 1) + j];
+          sum = __ffma2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), j < 2 ? x0 : x1, sum);
+        }
+      }
+    }
+  }
+};
+
+template <int kind, int chunks>
+__device__ __forceinline__ void add_slabs(Sums& a, Shared& s, Turn& turn, uint32_t tmem, int half, int w, int lane, int slabs) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a.v[c][h][j] = make_float2(0.0f, 0.0f);
+  Turn at = turn;
+  const int column = half * 16 * chunks;
+  Adder<kind, chunks> add{a, s, at, tmem + column + (static_cast<uint32_t>(w * 32) << 16),
+                          tc::in_block(tc::smem_addr(&s.acc_empty[0]), 0), lane, slabs, column, {}, {}};
+#pragma unroll 1
+  for (int k = 0; k < slabs; ++k) add.slab(k);
+  turn = at;
+}
 
 template <typename T, int kind>
 struct Epilogue {
@@ -218,7 +365,7 @@ struct Epilogue {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 v = floats_of(a.v[i][h][j]);
+          const float2 v = a.v[i][h][j];
           put[j / 2 * 4 * kPairStride + h * 16 + (j & 1) * 8] = pack2<T>(v.x, v.y);
         }
       half_sync(half);
@@ -252,7 +399,7 @@ struct Epilogue {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) put[j / 2 * 4 * kPairStride32 + h * 16 + (j & 1) * 8] = floats_of(a.v[i][h][4 * j2 + j]);
+          for (int j = 0; j < 4; ++j) put[j / 2 * 4 * kPairStride32 + h * 16 + (j & 1) * 8] = a.v[i][h][4 * j2 + j];
         half_sync(half);
         float x[4][4];
 #pragma unroll
@@ -296,7 +443,7 @@ struct Epilogue {
           if (32 * i >= nh) break;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float2 v = floats_of(a.v[i][h][j]);
+            const float2 v = a.v[i][h][j];
             put[j / 2 * 4 * kGatedStride + (j & 1) * 8] = pack2<T>(v.x, v.y);
           }
           half_sync(half);
@@ -310,8 +457,8 @@ struct Epilogue {
       if (32 * i >= nh) break;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float2 g = floats_of(a.v[i][0][j]), u = floats_of(a.v[i][1][j]);
-        a.v[i][0][j] = pair_of(__float_as_uint(g.x * fast_sigmoid(g.x) * u.x), __float_as_uint(g.y * fast_sigmoid(g.y) * u.y));
+        const float2 g = a.v[i][0][j], u = a.v[i][1][j];
+        a.v[i][0][j] = make_float2(g.x * fast_sigmoid(g.x) * u.x, g.y * fast_sigmoid(g.y) * u.y);
       }
     }
     if (p.out != nullptr) {
@@ -321,7 +468,7 @@ struct Epilogue {
         if (32 * i >= nh) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 v = floats_of(a.v[i][0][j]);
+          const float2 v = a.v[i][0][j];
           put[j / 2 * 4 * kGatedStride + (j & 1) * 8] = pack2<T>(v.x, v.y);
         }
         half_sync(half);
@@ -338,7 +485,7 @@ struct Epilogue {
       if (32 * i >= nh) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 x = floats_of(a.v[i][0][2 * j]), y = floats_of(a.v[i][0][2 * j + 1]);
+        const float2 x = a.v[i][0][2 * j], y = a.v[i][0][2 * j + 1];
         float m0 = max_nan(fabsf(x.x), fabsf(y.x)), m1 = max_nan(fabsf(x.y), fabsf(y.y));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
@@ -349,43 +496,32 @@ struct Epilogue {
       }
     }
     half_sync(half);
-    {
-      const int c = w * 32 + lane;
-      float m = 0.0f;
-      if (c < nh) {
-        m = max_nan(max_nan(most[c], most[kHalfN + c]), max_nan(most[2 * kHalfN + c], most[3 * kHalfN + c]));
-        store_peer(tc::in_block(tc::smem_addr(&s.peer_max[turn][half * nh + c]), rank ^ 1), m);
-      }
-      half_sync(half);
-      most[c] = m;
-      if (threadIdx.x % 128 == 0) tc::mbar_publish_cluster(tc::in_block(tc::smem_addr(&s.peer_full[half]), rank ^ 1));
-      half_sync(half);
+    const int c = w * 32 + lane;  // a column of the half for each thread
+    float m = 0.0f;
+    if (c < nh) {
+      m = max_nan(max_nan(most[c], most[kHalfN + c]), max_nan(most[2 * kHalfN + c], most[3 * kHalfN + c]));
+      store_peer(tc::in_block(tc::smem_addr(&s.peer_max[turn][half * nh + c]), rank ^ 1), m);
     }
+    half_sync(half);
+    if (c == 0) tc::mbar_publish_cluster(tc::in_block(tc::smem_addr(&s.peer_full[half]), rank ^ 1));
     tc::mbar_wait<true>(tc::smem_addr(&s.peer_full[half]), parity, &s.gave_up);
-    const float* other = s.peer_max[turn] + half * nh;
-    float m_scale[4][4][2];
+    if (c < nh) {
+      const BlockScale b = block_scale(max_nan(m, s.peer_max[turn][half * nh + c]));
+      most[c] = b.inv;
+      if (rank == 0 && c < part.cnt - t.r0 - half * nh) {
+        float* qs = p.qs + (static_cast<long long>(t.off) + t.r0 + half * nh + c) * scale_columns(F) + t.f0 / kF8Block;
+        qs[0] = b.scale;
+        if (t.f0 + kF8Block >= F)
+          for (int k = 1; t.f0 / kF8Block + k < scale_columns(F); ++k) qs[k] = 0.0f;
+      }
+    }
+    half_sync(half);
+    float2 inv[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (32 * i >= nh) break;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = 32 * i + 8 * j + 2 * (lane & 3);
-        const float2 x = *reinterpret_cast<const float2*>(most + c), y = *reinterpret_cast<const float2*>(other + c);
-        const BlockScale b0 = block_scale(max_nan(x.x, y.x)), b1 = block_scale(max_nan(x.y, y.y));
-        m_scale[i][j][0] = b0.inv;
-        m_scale[i][j][1] = b1.inv;
-        if (rank == 0 && w == 0 && lane < 4) {
-          float* qs = p.qs + (static_cast<long long>(t.off) + t.r0 + half * nh + c) * scale_columns(F) + t.f0 / kF8Block;
-          const int stop = part.cnt - t.r0 - half * nh;
-          if (c < stop) qs[0] = b0.scale;
-          if (c + 1 < stop) qs[scale_columns(F)] = b1.scale;
-          if (t.f0 + kF8Block >= F)
-            for (int k = 1; t.f0 / kF8Block + k < scale_columns(F); ++k) {
-              if (c < stop) qs[k] = 0.0f;
-              if (c + 1 < stop) qs[scale_columns(F) + k] = 0.0f;
-            }
-        }
-      }
+      for (int j = 0; j < 4; ++j) inv[i][j] = *reinterpret_cast<const float2*>(most + 32 * i + 8 * j + 2 * (lane & 3));
     }
     half_sync(half);  // read: `most` gives way to the values
     // Two rows' bytes of a feature are a half word: staged[pair][64 features], 144 bytes apart.
@@ -395,8 +531,8 @@ struct Epilogue {
       if (32 * i >= nh) break;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float2 v = floats_of(a.v[i][0][j]);
-        put[j / 2 * 4 * 72 + (j & 1) * 8] = static_cast<unsigned short>(e4m3x2(v.x * m_scale[i][j / 2][0], v.y * m_scale[i][j / 2][1]));
+        const float2 v = a.v[i][0][j];
+        put[j / 2 * 4 * 72 + (j & 1) * 8] = static_cast<unsigned short>(e4m3x2(v.x * inv[i][j / 2].x, v.y * inv[i][j / 2].y));
       }
       half_sync(half);
       {
@@ -447,42 +583,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool fwd = kind == kProdFwd || kind == kProdFwdSwiglu;
   extern __shared__ unsigned char raw[];
   unsigned char* ring = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
-  uint32_t* staging = reinterpret_cast<uint32_t*>(ring + static_cast<size_t>(kStages) * (kABytes + kBBytes));
+  uint32_t* staging = reinterpret_cast<uint32_t*>(ring + kRingBytes);
   Shared& s = *reinterpret_cast<Shared*>(staging + 2 * kStageWords);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Through a shuffle the compiler knows that a warp shares the value: tensor
+  // memory is addressed by uniform registers, and each conversion to one costs.
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(tc::cluster_rank());
   if (threadIdx.x == 0) {
     tc::tma_prefetch_desc(&map_a);
     tc::tma_prefetch_desc(&map_b);
     tc::tma_prefetch_desc(&map_b16);
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       tc::mbar_init(tc::smem_addr(&s.full[i]), 2);  // the first block's two loaders account for both blocks' copies
       tc::mbar_init(tc::smem_addr(&s.empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       tc::mbar_init(tc::smem_addr(&s.acc_full[i]), 1);
       tc::mbar_init(tc::smem_addr(&s.acc_empty[i]), 2 * kEpilogueWarps);
-      tc::mbar_init(tc::smem_addr(&s.peer_full[i]), 1);
     }
+    for (int i = 0; i < 2; ++i) tc::mbar_init(tc::smem_addr(&s.peer_full[i]), 1);
     for (int i = 0; i < kGroups; ++i) {
       tc::mbar_init(tc::smem_addr(&s.scales_full[i]), 32);
       tc::mbar_init(tc::smem_addr(&s.scales_empty[i]), kEpilogueWarps);
     }
     tc::mbar_init(tc::smem_addr(&s.drained), 1);
     tc::mbar_init_fence();
-    s.gave_up = 0;
+    s.gave_up = s.most = 0;
   }
   if (warp == 2) tc::tmem_alloc(tc::smem_addr(&s.tmem), 512);
   tc::fence_before();
   __syncthreads();
   tc::cluster_sync();
   tc::fence_after();
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
   pdl_wait();
   if (threadIdx.x == 0) s.ok = blocks_ok(p.hdr, p.R);
   __syncthreads();
   const bool ok = s.ok;
-  if (ok) scan_row_blocks(p, s.cum, s.part);
+  if (ok) scan_row_blocks(p, s.cum, s.part, &s.most);
+  const int stage_bytes = kABytes + box_rows((min(s.most, kTileN) + 31) / 32 * 16) * kSlab;
+  const int stages = min(kMaxStages, kRingBytes / stage_bytes);
   const int red = fwd ? p.K : p.N, slabs = (red + kSlab - 1) / kSlab;
   volatile int* gave_up = &s.gave_up;
   const long long first = blockIdx.x / 2, step = gridDim.x / 2;
@@ -499,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (long long i = first; i < walk.total && !*gave_up; i += step) {
             walk.at(i, &t);
             const int half = t.n / 2;  // this block's rows
-            const int bytes = load_a ? kABytes : (half > 64 ? 128 : half > 32 ? 64 : half > 16 ? 32 : 16) * kSlab;
+            const int bytes = load_a ? kABytes : box_rows(half) * kSlab;
             for (int k = 0; k < slabs; ++k) {
               if (!tc::mbar_wait(tc::smem_addr(&s.empty[stage]), phase ^ 1, gave_up)) break;
-              const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * (kABytes + kBBytes)), b = a + kABytes;
+              const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * stage_bytes), b = a + kABytes;
               const uint32_t bar = rank == 0 ? tc::smem_addr(&s.full[stage]) : tc::in_block(tc::smem_addr(&s.full[stage]), 0);
               if (rank == 0) tc::mbar_expect(bar, 2 * bytes);  // the other block's copies too
               const int x = k * kSlab;
@@ -510,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kind == kProdFwd) {
                   tc::tma_pair_3d(a, &map_a, bar, x, t.f0 + rank * kHalfM, t.e);
                 } else if constexpr (kind == kProdFwdSwiglu) {
-                  for (int j = 0; j < 4; ++j)  // 16 gate rows, then the up rows of the same features
-                    tc::tma_pair_4d(a + j * (kABytes / 4), &map_a, bar, x, t.f0 + rank * (kHalfM / 2) + j * 16, 0, t.e);
+                  // four times 16 gate rows, then the up rows of the same features
+                  tc::tma_pair_5d(a, &map_a, bar, x, 0, 0, (t.f0 + rank * (kHalfM / 2)) / 16, t.e);
                 } else {
                   tc::tma_pair_3d(a, &map_a, bar, t.f0 + rank * kHalfM, x, t.e);
                 }
@@ -519,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tma_pair_2d(b, half > 64 ? &map_b : half > 32 ? &map_b64 : half > 16 ? &map_b32 : &map_b16, bar, x,
                                 t.off + t.r0 + rank * half);
               }
-              if (++stage == kStages) {
+              if (++stage == stages) {
                 stage = 0;
                 phase ^= 1;
               }
@@ -527,9 +667,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (load_a) pdl_trigger();
           // Every stage is read out before the block ends.
-          for (int j = 0; j < kStages && !*gave_up; ++j) {
+          for (int j = 0; j < stages && !*gave_up; ++j) {
             if (!tc::mbar_wait(tc::smem_addr(&s.empty[stage]), phase ^ 1, gave_up)) break;
-            if (++stage == kStages) {
+            if (++stage == stages) {
               stage = 0;
               phase ^= 1;
             }
@@ -543,37 +683,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-          int stage = 0, buf = 0;
-          uint32_t phase = 0, acc_phase = 0;
+        if (rank == 0) {
+          int stage = 0;
+          uint32_t phase = 0;
+          Slots slots;
           bool lost = false;
+          const uint32_t ring0 = tc::smem_addr(ring), full0 = tc::smem_addr(&s.full[0]), empty0 = tc::smem_addr(&s.empty[0]);
+          const uint32_t acc_full0 = tc::smem_addr(&s.acc_full[0]), acc_empty0 = tc::smem_addr(&s.acc_empty[0]);
           for (long long i = first; i < walk.total && !lost; i += step) {
             walk.at(i, &t);
+            t.n = __shfl_sync(0xffffffffu, t.n, 0);
             const uint32_t desc = mma_desc_f8(!fwd, kTileM, t.n);
-            for (int k = 0; k < slabs; ++k) {
-              lost = !tc::mbar_wait(tc::smem_addr(&s.acc_empty[buf]), acc_phase ^ 1, gave_up) ||
-                     !tc::mbar_wait(tc::smem_addr(&s.full[stage]), phase, gave_up);
+            if (Slots::of(t.n) != slots.width) {
+              // The slots were others' parts: all of those are read out first.
+              for (int j = 0; slots.width > 0 && j < kSlots; j += slots.width)
+                lost = lost || !warp_wait(acc_empty0 + 8 * j, (slots.phases >> j & 1) ^ 1, gave_up);
+              slots.width = Slots::of(t.n);
+              slots.at = 0;
+            }
+            for (int k = 0; k < slabs && !lost; ++k) {
+              lost = !warp_wait(acc_empty0 + 8 * slots.at, slots.phase() ^ 1, gave_up) || !warp_wait(full0 + 8 * stage, phase, gave_up);
               if (lost) break;
               tc::fence_after();
-              const uint32_t a = tc::smem_addr(ring + static_cast<size_t>(stage) * (kABytes + kBBytes)), b = a + kABytes;
-              const uint64_t da = fwd ? tc::desc_k_major(a) : tc::desc_mn_major(a, kABytes);
-              const uint64_t db = tc::desc_k_major(b);
-              const int left = red - k * kSlab;
-#pragma unroll
-              for (int q = 0; q < kSlab / 32; ++q)
-                if (q * 32 < left)
-                  mma_f8(tmem + buf * kTileN, da + q * (fwd ? tc::kDescStepK : kDescStepMn8), db + q * tc::kDescStepK, desc, q > 0);
-              tc::mma_commit(tc::smem_addr(&s.empty[stage]));
-              tc::mma_commit(tc::smem_addr(&s.acc_full[buf]));
-              if (++stage == kStages) {
+              // What lies past the reduction's end came as zeros.
+              const uint32_t a = ring0 + stage * stage_bytes;
+              mma_slab<fwd ? tc::kDescStepK : kDescStepMn8>(tmem + slots.at * kSlotColumns,
+                                                           fwd ? tc::desc_k_major(a) : tc::desc_mn_major(a, kABytes),
+                                                           tc::desc_k_major(a + kABytes), desc, empty0 + 8 * stage, acc_full0 + 8 * slots.at);
+              if (++stage == stages) {
                 stage = 0;
                 phase ^= 1;
               }
-              buf ^= 1;
-              if (buf == 0) acc_phase ^= 1;
+              slots.next();
             }
           }
-          if (lost) {
+          if (lost && elect()) {
             // What was issued ends before tensor memory is freed.
             tc::mma_commit(tc::smem_addr(&s.drained));
             const unsigned long long start = tc::now_ns();
@@ -603,15 +747,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b = k + (lane & 3), up = lane >> 2;  // lanes 4 to 7: the up rows' scales
             if (up < (kind == kProdFwdSwiglu ? 2 : 1) && b < slabs)
               w = __ldg(ws + (fwd ? static_cast<long long>(fb + up * (nb / 2)) * kb + b : static_cast<long long>(b) * kb + fb));
-            if (!tc::mbar_wait(tc::smem_addr(&s.scales_empty[slot]), phase ^ 1, gave_up)) break;
+            if (!warp_wait(tc::smem_addr(&s.scales_empty[slot]), phase ^ 1, gave_up)) break;
+            // Of 16 rows, those of one quarter of a warp's lanes (2 l, 2 l + 1,
+            // and 8 further on) lie side by side.
+            const int to = (lane & 16) + (lane & 6) * 2 + (lane & 8) / 4 + (lane & 1);
+            float w4[kGroup];
+#pragma unroll
+            for (int q = 0; q < kGroup; ++q) w4[q] = kind == kProdFwdSwiglu ? 1.0f : __shfl_sync(0xffffffffu, w, q);
 #pragma unroll
             for (int j = 0; j < kTileN / 32; ++j) {
-              s.as[slot][0][j * 32 + lane] = v[j].x;
-              s.as[slot][1][j * 32 + lane] = v[j].y;
-              s.as[slot][2][j * 32 + lane] = v[j].z;
-              s.as[slot][3][j * 32 + lane] = v[j].w;
+              s.as[slot][0][j * 32 + to] = v[j].x * w4[0];
+              s.as[slot][1][j * 32 + to] = v[j].y * w4[1];
+              s.as[slot][2][j * 32 + to] = v[j].z * w4[2];
+              s.as[slot][3][j * 32 + to] = v[j].w * w4[3];
             }
-            if (lane < 8) s.ws[slot][up][lane & 3] = w;
+            if (kind == kProdFwdSwiglu && lane < 8) s.ws[slot][up][lane & 3] = w;
             tc::mbar_arrive(tc::smem_addr(&s.scales_full[slot]));
             if (++slot == kGroups) {
               slot = 0;
@@ -628,62 +778,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       Tile t;
       const int half = (warp - 4) >> 2, w = warp & 3;  // the accumulator lanes a warp can reach go by its number
       const Epilogue<T, kind> out{p, s, staging + half * kStageWords, rank, half, w, lane};
-      int buf = 0, slot = 0, turn = 0;
-      uint32_t acc_phase = 0, scale_phase = 0, peer_phase = 0;
-      // A wait that gave up leaves its warp in step with the others, with
-      // nothing of use in its sums: every later wait ends at once.
+      int turn = 0;
+      uint32_t peer_phase = 0;
+      Turn at;
       for (long long i = first; i < walk.total; i += step) {
         walk.at(i, &t);
+        t.n = __shfl_sync(0xffffffffu, t.n, 0);
         const int nh = t.n / 2;
+        if (Slots::of(t.n) != at.slots.width) {
+          at.slots.width = Slots::of(t.n);
+          at.slots.at = 0;
+        }
         Sums a;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a.v[c][h][j] = 0;
-#pragma unroll 1
-        for (int k = 0; k < slabs; ++k) {
-          if ((k & (kGroup - 1)) == 0) tc::mbar_wait(tc::smem_addr(&s.scales_full[slot]), scale_phase, gave_up);
-          const float w0 = s.ws[slot][0][k & (kGroup - 1)], w1 = kind == kProdFwdSwiglu ? s.ws[slot][1][k & (kGroup - 1)] : w0;
-          const Pair w0p = pair_of(__float_as_uint(w0), __float_as_uint(w0)), w1p = pair_of(__float_as_uint(w1), __float_as_uint(w1));
-          const float* as = &s.as[slot][k & (kGroup - 1)][half * nh + 2 * (lane & 3)];
-          tc::mbar_wait(tc::smem_addr(&s.acc_full[buf]), acc_phase, gave_up);
-          __syncwarp();
-          tc::fence_after();
-          const uint32_t acc = tmem + buf * kTileN + half * nh + (static_cast<uint32_t>(w * 32) << 16);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (32 * c < nh) {
-              uint32_t r0[16], r1[16];
-              tmem_ld_rows(acc + 32 * c, r0);
-              tmem_ld_rows(acc + 32 * c + (16u << 16), r1);
-              tc::tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const Pair x = *reinterpret_cast<const Pair*>(as + 32 * c + 8 * j);
-                const Pair x0 = mul2(x, w0p), x1 = kind == kProdFwdSwiglu ? mul2(x, w1p) : x0;
-                a.v[c][0][2 * j] = fma2(pair_of(r0[4 * j], r0[4 * j + 1]), x0, a.v[c][0][2 * j]);
-                a.v[c][0][2 * j + 1] = fma2(pair_of(r0[4 * j + 2], r0[4 * j + 3]), x0, a.v[c][0][2 * j + 1]);
-                a.v[c][1][2 * j] = fma2(pair_of(r1[4 * j], r1[4 * j + 1]), x1, a.v[c][1][2 * j]);
-                a.v[c][1][2 * j + 1] = fma2(pair_of(r1[4 * j + 2], r1[4 * j + 3]), x1, a.v[c][1][2 * j + 1]);
-              }
-            }
-          }
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            tc::mbar_arrive_cluster(tc::in_block(tc::smem_addr(&s.acc_empty[buf]), 0));
-            if ((k & (kGroup - 1)) == kGroup - 1 || k + 1 == slabs) tc::mbar_arrive(tc::smem_addr(&s.scales_empty[slot]));
-          }
-          buf ^= 1;
-          if (buf == 0) acc_phase ^= 1;
-          if ((k & (kGroup - 1)) == kGroup - 1 || k + 1 == slabs) {
-            if (++slot == kGroups) {
-              slot = 0;
-              scale_phase ^= 1;
-            }
-          }
+        switch (nh / 16) {
+          case 1: add_slabs<kind, 1>(a, s, at, tmem, half, w, lane, slabs); break;
+          case 2: add_slabs<kind, 2>(a, s, at, tmem, half, w, lane, slabs); break;
+          case 3: add_slabs<kind, 3>(a, s, at, tmem, half, w, lane, slabs); break;
+          case 4: add_slabs<kind, 4>(a, s, at, tmem, half, w, lane, slabs); break;
+          case 5: add_slabs<kind, 5>(a, s, at, tmem, half, w, lane, slabs); break;
+          case 6: add_slabs<kind, 6>(a, s, at, tmem, half, w, lane, slabs); break;
+          case 7: add_slabs<kind, 7>(a, s, at, tmem, half, w, lane, slabs); break;
+          default: add_slabs<kind, 8>(a, s, at, tmem, half, w, lane, slabs); break;
         }
         if constexpr (kind == kProdFwdSwiglu) {
           out.gated(t, a, nh, turn, peer_phase);
@@ -707,14 +822,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tc::tmem_free(tmem, 512);
 }
 
-// A map of [dim 3]..[dim 1][dim 0] bytes.
-bool make_map(CUtensorMap* m, const void* base, int dims, const long long (&size)[4], const long long (&stride)[3],
-              const int (&box)[4]) {
+// A map of [dim 4]..[dim 1][dim 0] bytes.
+bool make_map(CUtensorMap* m, const void* base, int dims, const long long (&size)[5], const long long (&stride)[4],
+              const int (&box)[5]) {
   const tc::EncodeFn f = tc::tensor_map_encoder();
   if (f == nullptr) return false;
-  cuuint64_t sz[4], st[3];
-  cuuint32_t bx[4];
-  const cuuint32_t one[4] = {1, 1, 1, 1};
+  cuuint64_t sz[5], st[4];
+  cuuint32_t bx[5];
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < dims; ++i) {
     sz[i] = static_cast<cuuint64_t>(size[i]);
     bx[i] = static_cast<cuuint32_t>(box[i]);
@@ -761,10 +876,11 @@ cudaError_t launch_kind(const F8Params& p, int num_sms, cudaStream_t s) {
   CUtensorMap a, b, b64, b32, b16;
   constexpr bool fwd = kind == kProdFwd || kind == kProdFwdSwiglu;
   const long long K = p.K, N = p.N, red = fwd ? K : N, F = N / 2;
-  bool ok = kind == kProdFwdSwiglu ? make_map(&a, p.w, 4, {K, F, 2, p.E}, {K, F * K, 2 * F * K}, {kSlab, 16, 2, 1})
-                                   : make_map(&a, p.w, 3, {K, N, p.E, 1}, {K, N * K, 0}, {kSlab, 128, 1, 1});
+  bool ok = kind == kProdFwdSwiglu
+                ? make_map(&a, p.w, 5, {K, 16, 2, F / 16, p.E}, {K, F * K, 16 * K, 2 * F * K}, {kSlab, 16, 2, 4, 1})
+                : make_map(&a, p.w, 3, {K, N, p.E, 1, 1}, {K, N * K, 0, 0}, {kSlab, 128, 1, 1, 1});
   CUtensorMap* maps[4] = {&b, &b64, &b32, &b16};
-  for (int i = 0; i < 4; ++i) ok = ok && make_map(maps[i], p.a, 2, {red, p.R, 1, 1}, {red, 0, 0}, {kSlab, 128 >> i, 1, 1});
+  for (int i = 0; i < 4; ++i) ok = ok && make_map(maps[i], p.a, 2, {red, p.R, 1, 1, 1}, {red, 0, 0, 0}, {kSlab, 128 >> i, 1, 1, 1});
   if (!ok) return cudaErrorInvalidValue;
   const int pairs = resident_pairs<T, kind>(num_sms);
   if (pairs == 0) return cudaErrorLaunchOutOfResources;

@@ -144,6 +144,13 @@ __device__ __forceinline__ void tma_pair_4d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
+__device__ __forceinline__ void tma_pair_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w, int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+      : "memory");
+}
+
 // Tensor memory of a pair of blocks, both of which call these: `cols` columns
 // (a power of two >= 32) in each, the address written to *slot.
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
