@@ -354,10 +354,16 @@ ep_status_t ep_moe_few(ep_moe_few_config_t config, const void* x, const void* ga
   p.w = topk_weights;
   const ep::FewLayout l = ep::few_layout(p.T, p.E, p.K, p.H, p.F, f8);
   p.hdr = at<int>(workspace, 0);
+  p.done = at<int>(workspace, l.done);
+  p.written = at<int>(workspace, l.written);
+  p.zeros = l.zeros;
   p.logits = at<float>(workspace, l.logits);
-  p.act = at<float>(workspace, l.act);
+  p.act = at<char>(workspace, l.act);
   p.xq = at<uint8_t>(workspace, l.xq);
   p.xs = at<float>(workspace, l.xs);
+  p.aq = at<uint8_t>(workspace, l.aq);
+  p.as = at<float>(workspace, l.as);
+  p.part = at<float>(workspace, l.part);
   p.router.logits = p.logits;
   p.router.dtype = EP_DTYPE_FP32;
   p.router.bias = bias;

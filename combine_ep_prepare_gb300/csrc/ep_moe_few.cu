@@ -1,11 +1,30 @@
 // ep_moe_few.cu -- a whole MoE layer for a few tokens in two kernels.
 //
-// The first takes the gate's product (and, for 8-bit weights, quantises the
-// tokens).  The second chooses the experts in every block by itself, then
-// multiplies: a = silu(g) u of the used experts' w13, one wait of the blocks
-// for one another, and out = sum over a token's experts of p w2 a.
-#include <cuda_fp8.h>
-
+//   logits = x gate^T;  a = silu(g) u of w13[e] x;  out = sum_k p_k w2[e_k] a_k
+//
+// The first kernel takes the gate's product (and, for 8-bit weights, quantises
+// the tokens).  The second is persistent, one block per SM: every block chooses
+// the experts by itself, a warp a token, which costs less than handing the
+// choice around; then come the gated products, one wait of the blocks for one
+// another, and the down products.
+//
+// The chosen experts' weights are read once, so memory bounds it; everything is
+// arranged to keep loads in flight and all SMs busy to the end.
+// - A piece of work is 16 weight rows (8 gate rows and their 8 up rows, or 16
+//   output rows of one expert) times the whole reduction; the pieces are dealt
+//   out in even runs.  The 16 warps of a block split the reduction: each lane
+//   loads 16 bytes of row lane / 4 and of row lane / 4 + 8, four such pairs ahead
+//   of their use and across the ends of pieces.
+// - They are the 16 x K side of mma.sync as they lie: a sum does not depend on
+//   its order, so a lane's 16 bytes may count as any of the fragment's columns,
+//   if the tokens' operand (the same 16 bytes of token lane / 4) does too.
+// - Up to eight tokens of an expert, side by side, are one n-tile.  8-bit
+//   operands are multiplied as e4m3; a step of 64 elements lies within a block
+//   of 128 and its sum is scaled in float32.
+// - A tile of outputs sums over experts in registers and shared memory.  Where
+//   the run of a block ends inside a tile, the parts go to the workspace and
+//   the block that comes last adds them in the blocks' order: no output depends
+//   on which one that was.
 #include <algorithm>
 #include <atomic>
 
@@ -16,20 +35,23 @@ namespace ep {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kGateThreads = 256, kGateWarps = kGateThreads / 32;
+constexpr int kWarps = 16, kThreads = kWarps * 32;
+constexpr int kAhead = 4;  // steps whose weights are in flight
 
 template <typename G, typename T>
-__global__ void __launch_bounds__(kThreads) ep_few_gate_kernel(const FewParams p) {
-  __shared__ float part[kWarps][EP_MAX_FEW_TOKENS];
+__global__ void __launch_bounds__(kGateThreads) ep_few_gate_kernel(const FewParams p) {
+  __shared__ float part[kGateWarps][EP_MAX_FEW_TOKENS];
   pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x == 0 && threadIdx.x < 2) p.hdr[threadIdx.x] = 0;
+  for (int i = blockIdx.x * kGateThreads + threadIdx.x; i < p.zeros; i += gridDim.x * kGateThreads) p.hdr[i] = 0;
   if (static_cast<int>(blockIdx.x) < p.E) {
     const int e = blockIdx.x;
     float acc[EP_MAX_FEW_TOKENS];
 #pragma unroll
     for (int t = 0; t < EP_MAX_FEW_TOKENS; ++t) acc[t] = 0.0f;
-    for (int k = threadIdx.x * 8; k < p.H; k += kThreads * 8) {
+    for (int k = threadIdx.x * 8; k < p.H; k += kGateThreads * 8) {
       Raw8<G> g;
       float gv[8];
       g.load(static_cast<const G*>(p.gate) + static_cast<long long>(e) * p.H + k);
@@ -56,12 +78,12 @@ __global__ void __launch_bounds__(kThreads) ep_few_gate_kernel(const FewParams p
     __syncthreads();
     if (threadIdx.x < p.T) {
       float s = 0.0f;
-      for (int w = 0; w < kWarps; ++w) s += part[w][threadIdx.x];
+      for (int w = 0; w < kGateWarps; ++w) s += part[w][threadIdx.x];
       p.logits[threadIdx.x * p.E + e] = s;
     }
   } else {  // a token's row in 8 bits
     const int t = blockIdx.x - p.E, cols = scale_columns(p.H);
-    for (int b = warp * 2; b < cols; b += kWarps * 2) {
+    for (int b = warp * 2; b < cols; b += kGateWarps * 2) {
       const int k = b * kF8Block + lane * 8;
       float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       if (k < p.H) {
@@ -76,8 +98,6 @@ __global__ void __launch_bounds__(kThreads) ep_few_gate_kernel(const FewParams p
     }
   }
 }
-
-__device__ __forceinline__ float e4m3(uint8_t v) { return static_cast<float>(*reinterpret_cast<const __nv_fp8_e4m3*>(&v)); }
 
 // All blocks of the grid have arrived, and what they wrote before can be read.
 // The word was zero when the kernel began.  False after about a second.
@@ -106,13 +126,16 @@ __device__ bool grid_wait(unsigned* word, int* status) {
   return ok_s != 0;
 }
 
+constexpr int kMaxRoutes = EP_MAX_FEW_TOKENS * EP_MAX_TOPK;
 struct Choice {
-  unsigned tokens[EP_MAX_EXPERTS];                       // an expert's tokens, a bit each
-  short first[EP_MAX_EXPERTS];                           // the routes of the experts before it
-  short used[EP_MAX_FEW_TOKENS * EP_MAX_TOPK];           // experts with a token, ascending
-  short expert[EP_MAX_FEW_TOKENS * EP_MAX_TOPK];         // [t][k]
-  float weight[EP_MAX_FEW_TOKENS * EP_MAX_TOPK];
-  int num_used;
+  unsigned tokens[EP_MAX_EXPERTS];  // an expert's tokens, a bit each
+  short first[EP_MAX_EXPERTS];      // the routes of the experts before it
+  short used[kMaxRoutes];           // experts with a token, ascending
+  short expert[kMaxRoutes];         // [t][k]
+  float weight[kMaxRoutes];
+  short token[kMaxRoutes];          // by expert, then token
+  float share[kMaxRoutes];
+  int num_used, last;
 };
 
 template <int J>
@@ -133,15 +156,13 @@ __device__ __forceinline__ void choose(const FewParams& p, Choice& c, int warp, 
   }
 }
 
-template <typename T, bool f8>
-__global__ void __launch_bounds__(kThreads) ep_few_experts_kernel(const FewParams p) {
-  __shared__ Choice c;
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The choice, and the routes sorted by expert.
+__device__ __forceinline__ void choose_experts(const FewParams& p, Choice& c, int warp, int lane) {
   for (int e = threadIdx.x; e < p.E; e += kThreads) c.tokens[e] = 0;
   __syncthreads();
   const int j = (p.E + 31) / 32;
-  if (j <= 4) choose<4>(p, c, warp, lane);
+  if (j <= 2) choose<2>(p, c, warp, lane);
+  else if (j <= 4) choose<4>(p, c, warp, lane);
   else if (j <= 8) choose<8>(p, c, warp, lane);
   else choose<32>(p, c, warp, lane);
   __syncthreads();
@@ -166,87 +187,414 @@ __global__ void __launch_bounds__(kThreads) ep_few_experts_kernel(const FewParam
     if (lane == 0) c.num_used = used;
   }
   __syncthreads();
-  const int hb = f8_blocks(p.H), fb = f8_blocks(p.F);
-  const int gw = blockIdx.x * kWarps + warp, warps = gridDim.x * kWarps;
-  for (int u = gw; u < c.num_used * p.F; u += warps) {
-    const int e = c.used[u / p.F], f = u % p.F;
-    const long long wg = (static_cast<long long>(e) * 2 * p.F + f) * p.H, wu = wg + static_cast<long long>(p.F) * p.H;
-    int pos = c.first[e];
-    for (unsigned left = c.tokens[e]; left; left &= left - 1, ++pos) {
-      const int t = __ffs(left) - 1;
-      float g = 0.0f, v = 0.0f;
-      for (int k = lane; k < p.H; k += 32) {
-        if constexpr (f8) {
-          const float x = e4m3(p.xq[static_cast<long long>(t) * p.H + k]) * p.xs[t * scale_columns(p.H) + k / 128];
-          const uint8_t* w = static_cast<const uint8_t*>(p.w13);
-          g = fmaf(x, e4m3(w[wg + k]) * p.s13[(static_cast<long long>(e) * 2 * fb + f / 128) * hb + k / 128], g);
-          v = fmaf(x, e4m3(w[wu + k]) * p.s13[(static_cast<long long>(e) * 2 * fb + fb + f / 128) * hb + k / 128], v);
-        } else {
-          const float x = to_f32(static_cast<const T*>(p.x)[static_cast<long long>(t) * p.H + k]);
-          g = fmaf(x, to_f32(static_cast<const T*>(p.w13)[wg + k]), g);
-          v = fmaf(x, to_f32(static_cast<const T*>(p.w13)[wu + k]), v);
-        }
+  for (int r = threadIdx.x; r < p.T * p.K; r += kThreads) {
+    const int t = r / p.K, e = c.expert[r];
+    if (e < 0) continue;
+    const int at = c.first[e] + __popc(c.tokens[e] & ((1u << t) - 1));
+    c.token[at] = static_cast<short>(t);
+    c.share[at] = c.weight[r];
+  }
+  __syncthreads();
+}
+
+// Sixteen bytes read once.
+__device__ __forceinline__ uint4 load_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// d += a b: a the 16 weight rows' words, b the 8 tokens' (T: bf16, fp16, or
+// uint8_t for e4m3).
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma<__half>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma<uint8_t>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Where a piece of work lies: its expert, its two eights of weight rows and the
+// rows of the tokens' operand.
+struct Piece {
+  int u, e;                   // its place among the used experts, its number
+  int row0, row1, n, pos;     // rows of the expert's matrix (row1 < 0: none); tokens, and the first one's route
+  int tile;                   // features (gate and up) or outputs, from 8 tile or 16 tile on
+};
+
+// One of the two products' pieces, in the order in which they are dealt out.
+template <bool down>
+struct Walk {
+  const FewParams& p;
+  const Choice& c;
+  int tiles, u, tile;  // up: by expert, then tile; down: by tile, then expert
+  __device__ __forceinline__ Walk(const FewParams& p_, const Choice& c_, int i) : p(p_), c(c_) {
+    tiles = down ? (p.H + kFewRows - 1) / kFewRows : p.F / 8;
+    u = down ? i % max(1, c.num_used) : i / tiles;
+    tile = down ? i / max(1, c.num_used) : i % tiles;
+  }
+  __device__ __forceinline__ void next() {
+    if (down) {
+      if (++u == c.num_used) {
+        u = 0;
+        ++tile;
       }
-      g = route::warp_sum(g);
-      v = route::warp_sum(v);
-      if (lane == 0) {
-        const float a = swiglu(g, v);
-        p.act[static_cast<long long>(pos) * p.F + f] = f8 ? a : to_f32(from_f32<T>(a));
-      }
+    } else if (++tile == tiles) {
+      tile = 0;
+      ++u;
     }
   }
-  if (!grid_wait(reinterpret_cast<unsigned*>(p.hdr + 1), p.hdr)) return;
-  for (int h = gw; h < p.H; h += warps) {
-    for (int t = 0; t < p.T; ++t) {
-      float y = 0.0f;
-      for (int k = 0; k < p.K; ++k) {
-        const int e = c.expert[t * p.K + k];
-        if (e < 0) continue;
-        const int pos = c.first[e] + __popc(c.tokens[e] & ((1u << t) - 1));
-        const float* a = p.act + static_cast<long long>(pos) * p.F;
-        const long long wr = (static_cast<long long>(e) * p.H + h) * p.F;
-        float s = 0.0f;
-        for (int f0 = 0; f0 < p.F; f0 += 128) {
-          float v[4], m = 0.0f;
-          for (int i = 0; i < 4; ++i) {
-            const int f = f0 + lane * 4 + i;
-            v[i] = f < p.F ? __ldcg(a + f) : 0.0f;
-            m = max_nan(m, fabsf(v[i]));
-          }
-          if constexpr (f8) {
-            for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, d));
-            const BlockScale b = block_scale(m);
-            const uint32_t q = e4m3x4(v[0] * b.inv, v[1] * b.inv, v[2] * b.inv, v[3] * b.inv);
-            const float scale = b.scale * p.s2[(static_cast<long long>(e) * hb + h / 128) * fb + f0 / 128];
-            float part = 0.0f;
-            for (int i = 0; i < 4; ++i)
-              part = fmaf(e4m3(q >> (8 * i)), e4m3(static_cast<const uint8_t*>(p.w2)[wr + f0 + lane * 4 + i]), part);
-            s = fmaf(part, scale, s);
-          } else {
-            for (int i = 0; i < 4; ++i)
-              if (f0 + lane * 4 + i < p.F) s = fmaf(v[i], to_f32(static_cast<const T*>(p.w2)[wr + f0 + lane * 4 + i]), s);
+  __device__ __forceinline__ Piece at() const {
+    Piece o;
+    o.u = u;
+    o.e = c.used[u];
+    o.n = __popc(c.tokens[o.e]);
+    o.pos = c.first[o.e];
+    o.tile = tile;
+    if (down) {
+      o.row0 = tile * kFewRows;
+      o.row1 = o.row0 + 8 < p.H ? o.row0 + 8 : -1;
+    } else {
+      o.row0 = tile * 8;
+      o.row1 = p.F + o.row0;
+    }
+    return o;
+  }
+};
+
+// A block's run [lo, hi) of `pieces`: of each piece, warp w takes the steps w,
+// w + 16, ... of the reduction.  done(piece, sums, last step's index) is called
+// by all warps when a piece's steps are over.
+template <typename T, bool f8, int NT, bool down, typename Done>
+__device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, int lo, int hi, int warp, int lane, Done done) {
+  using E = typename std::conditional<f8, uint8_t, T>::type;
+  constexpr int kVec = 16 / sizeof(E), kStep = 4 * kVec;  // elements of a lane's load and of a step
+  const int red = down ? p.F : p.H, rows = down ? p.H : 2 * p.F;
+  const int steps = (red + kStep - 1) / kStep, turns = (steps + kWarps - 1) / kWarps;
+  const int total = (hi - lo) * turns;
+  const int g = lane >> 2, t = lane & 3;
+  const E* w = static_cast<const E*>(down ? p.w2 : p.w13);
+  const float* ws = down ? p.s2 : p.s13;
+  const E* x = f8 ? reinterpret_cast<const E*>(down ? p.aq : p.xq) : static_cast<const E*>(down ? p.act : p.x);
+  const float* xs = down ? p.as : p.xs;
+  const int xcols = scale_columns(red), wcols = f8_blocks(red), wblocks = f8_blocks(rows);
+  uint4 a[kAhead][2], b[2][NT];
+  float sw[2][2], sx[2][NT][2];
+  Walk<down> walk_a(p, c, lo), walk_b(p, c, lo), walk_c(p, c, lo);
+  Piece pa, pb, pc;
+  int ja = 0, jb = 0, jc = 0;
+  if (total > 0) pa = pb = pc = walk_a.at();
+  auto load_a = [&](uint4 (&to)[2]) {
+    const int k = (warp + ja * kWarps) * kStep + t * kVec;
+    to[0] = to[1] = make_uint4(0, 0, 0, 0);
+    if (k < red) {
+      const E* base = w + static_cast<long long>(pa.e) * rows * red + k;
+      to[0] = load_stream(base + static_cast<long long>(pa.row0 + g) * red);
+      if (!down || pa.row1 >= 0) to[1] = load_stream(base + static_cast<long long>(pa.row1 + g) * red);
+    }
+    if (++ja == turns) {
+      ja = 0;
+      walk_a.next();
+      if (walk_a.u < c.num_used && walk_a.tile < walk_a.tiles) pa = walk_a.at();
+    }
+  };
+  auto load_b = [&](int to) {
+    const int step = warp + jb * kWarps, k = step * kStep + t * kVec;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      b[to][i] = make_uint4(0, 0, 0, 0);
+      if (8 * i + g < pb.n && k < red) {
+        const int row = down ? pb.pos + 8 * i + g : c.token[pb.pos + 8 * i + g];
+        const E* at = x + static_cast<long long>(row) * red + k;
+        // act is written in this kernel: not through the read-only path
+        b[to][i] = down ? __ldcg(reinterpret_cast<const uint4*>(at)) : __ldg(reinterpret_cast<const uint4*>(at));
+      }
+    }
+    if constexpr (f8) {
+      const int block = min(step * kStep / kF8Block, wcols - 1);
+      const float* s = ws + static_cast<long long>(pb.e) * wblocks * wcols + block;
+      sw[to][0] = __ldg(s + static_cast<long long>(pb.row0 / kF8Block) * wcols);
+      sw[to][1] = down ? sw[to][0] : __ldg(s + static_cast<long long>(pb.row1 / kF8Block) * wcols);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int col = 8 * i + 2 * t + q;
+          sx[to][i][q] = 0.0f;
+          if (col < pb.n) {
+            const int row = down ? pb.pos + col : c.token[pb.pos + col];
+            sx[to][i][q] = __ldcg(xs + static_cast<long long>(row) * xcols + block);
           }
         }
-        y = fmaf(c.weight[t * p.K + k], route::warp_sum(s), y);
+    }
+    if (++jb == turns) {
+      jb = 0;
+      walk_b.next();
+      if (walk_b.u < c.num_used && walk_b.tile < walk_b.tiles) pb = walk_b.at();
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q)
+    if (q < total) load_a(a[q]);
+  if constexpr (down) done.wait();  // the weights are on their way while the blocks wait for act
+  if (total > 0) load_b(0);
+  float sum[NT][4] = {};
+  for (int n0 = 0; n0 < total; n0 += kAhead) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int n = n0 + q;
+      if (n >= total) break;
+      if (n + 1 < total) load_b((q + 1) & 1);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if (8 * i >= pc.n) break;
+        const uint4 &u = a[q][0], &v = a[q][1], &y = b[q & 1][i];
+        if constexpr (f8) {
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma<E>(d, u.x, v.x, u.y, v.y, y.x, y.y);
+          mma<E>(d, u.z, v.z, u.w, v.w, y.z, y.w);
+          // A step without elements has zeros times whatever scale the block before has.
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[j], sw[q & 1][j >> 1] * sx[q & 1][i][j & 1], sum[i][j]);
+        } else {
+          mma<E>(sum[i], u.x, v.x, u.y, v.y, y.x, y.y);
+          mma<E>(sum[i], u.z, v.z, u.w, v.w, y.z, y.w);
+        }
       }
-      if (lane == 0) static_cast<T*>(p.out)[static_cast<long long>(t) * p.H + h] = from_f32<T>(y);
+      if (n + kAhead < total) load_a(a[q]);
+      if (++jc == turns) {
+        jc = 0;
+        walk_c.next();
+        done(pc, sum, n + 1 == total);
+        if (n + 1 < total) pc = walk_c.at();
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[i][j] = 0.0f;
+      }
     }
   }
 }
 
-template <typename T, bool f8>
+// After a piece of the gated products: its 16 warps' sums are joined, the
+// activation taken and written; with 8-bit weights the last piece of 128
+// features quantises them.
+template <typename T, bool f8, int NT>
+struct UpDone {
+  const FewParams& p;
+  Choice& c;
+  float* red;  // [2][kWarps][16][8 NT]
+  int warp, lane, turn;
+  __device__ __forceinline__ void wait() const {}
+  __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool) {
+    constexpr int kCols = 8 * NT;
+    float* mine = red + (turn * kWarps + warp) * 16 * kCols;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (8 * i >= o.n) break;
+      *reinterpret_cast<float2*>(mine + g * kCols + 8 * i + 2 * t) = make_float2(sum[i][0], sum[i][1]);
+      *reinterpret_cast<float2*>(mine + (g + 8) * kCols + 8 * i + 2 * t) = make_float2(sum[i][2], sum[i][3]);
+    }
+    __syncthreads();
+    const int f = threadIdx.x & 7, col = threadIdx.x >> 3;
+    if (col < o.n) {
+      const float* at = red + turn * kWarps * 16 * kCols + f * kCols + col;
+      float gate = 0.0f, up = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        gate += at[w * 16 * kCols];
+        up += at[w * 16 * kCols + 8 * kCols];
+      }
+      const float a = swiglu(gate, up);
+      const long long i = static_cast<long long>(o.pos + col) * p.F + o.tile * 8 + f;
+      if constexpr (f8) static_cast<float*>(p.act)[i] = a;
+      else static_cast<T*>(p.act)[i] = from_f32<T>(a);
+    }
+    turn ^= 1;  // the other buffer next: the sums here are still being read
+    if constexpr (f8) {
+      const int block = o.tile / (kF8Block / 8);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        c.last = atomicAdd(p.written + o.u * f8_blocks(p.F) + block, 1) == kF8Block / 8 - 1;
+        __threadfence();
+      }
+      __syncthreads();
+      if (c.last) {
+        for (int col8 = warp; col8 < o.n; col8 += kWarps) {
+          const long long at = static_cast<long long>(o.pos + col8) * p.F + block * kF8Block + lane * 4;
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(p.act) + at));
+          float m = max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, d));
+          const BlockScale s = block_scale(m);
+          *reinterpret_cast<uint32_t*>(p.aq + at) = e4m3x4(v.x * s.inv, v.y * s.inv, v.z * s.inv, v.w * s.inv);
+          if (lane == 0) p.as[static_cast<long long>(o.pos + col8) * scale_columns(p.F) + block] = s.scale;
+        }
+      }
+    }
+  }
+};
+
+// After a piece of the down products: its sums, times the tokens' shares, are
+// added to this warp's sums of the tile; after the tile's last piece here the
+// warps' sums are joined.
+template <typename T, int NT>
+struct DownDone {
+  const FewParams& p;
+  Choice& c;
+  float* red;  // [kWarps][16][T]
+  int warp, lane, lo, pieces, blocks;  // blocks: those that have pieces
+  __device__ __forceinline__ void zero() const {
+    for (int i = lane; i < 16 * p.T; i += 32) red[warp * 16 * p.T + i] = 0.0f;
+    __syncwarp();
+  }
+  __device__ __forceinline__ void wait() const {
+    grid_wait(reinterpret_cast<unsigned*>(p.hdr + 1), p.hdr);  // given up: the sums are of what happens to be in act
+    zero();
+  }
+  __device__ __forceinline__ int block_of(long long piece) const {
+    return static_cast<int>(((piece + 1) * blocks - 1) / pieces);
+  }
+  __device__ __forceinline__ int start_of(long long block) const { return static_cast<int>(block * pieces / blocks); }
+  __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool end) {
+    float* mine = red + warp * 16 * p.T;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (8 * i >= o.n) break;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int col = 8 * i + 2 * t + q;
+        if (col < o.n) {
+          const int token = c.token[o.pos + col];
+          const float share = c.share[o.pos + col];
+          mine[g * p.T + token] = fmaf(share, sum[i][q], mine[g * p.T + token]);
+          mine[(g + 8) * p.T + token] = fmaf(share, sum[i][2 + q], mine[(g + 8) * p.T + token]);
+        }
+      }
+    }
+    __syncwarp();  // an expert's columns are other lanes' in the next piece
+    if (!end && o.u + 1 < c.num_used) return;
+    __syncthreads();
+    const int first = block_of(static_cast<long long>(o.tile) * c.num_used);
+    const int last = block_of(static_cast<long long>(o.tile + 1) * c.num_used - 1);
+    const bool alone = first == last;
+    float* part = p.part + (static_cast<long long>(blockIdx.x) * 2 + (lo / c.num_used == o.tile ? 0 : 1)) * 16 * p.T;
+    for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += red[w * 16 * p.T + i];
+      if (alone) put(o.tile, i, s);
+      else part[i] = s;
+    }
+    if (!alone) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        c.last = atomicAdd(p.done + o.tile, 1) == last - first;
+        __threadfence();
+      }
+      __syncthreads();
+      if (c.last) {
+        for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
+          float s = 0.0f;
+          for (int b = first; b <= last; ++b)
+            s += __ldcg(p.part + (static_cast<long long>(b) * 2 + (start_of(b) / c.num_used == o.tile ? 0 : 1)) * 16 * p.T + i);
+          put(o.tile, i, s);
+        }
+      }
+    }
+    __syncthreads();  // read: the sums begin again
+    zero();
+  }
+  __device__ __forceinline__ void put(int tile, int i, float s) const {
+    const int h = tile * kFewRows + i / p.T;
+    if (h < p.H) static_cast<T*>(p.out)[static_cast<long long>(i % p.T) * p.H + h] = from_f32<T>(s);
+  }
+};
+
+// This block's even share of the pieces; where there are fewer than blocks, the
+// last blocks have none.
+struct Run {
+  int pieces, blocks, lo, hi;
+  __device__ __forceinline__ explicit Run(long long n) : pieces(static_cast<int>(n)), blocks(static_cast<int>(min(n, static_cast<long long>(gridDim.x)))) {
+    const long long b = min(static_cast<int>(blockIdx.x), blocks);
+    lo = static_cast<int>(b * n / blocks);
+    hi = static_cast<int>(min(b + 1, static_cast<long long>(blocks)) * n / blocks);
+  }
+};
+
+template <typename T, bool f8, int NT>
+__global__ void __launch_bounds__(kThreads, 1) ep_few_experts_kernel(const FewParams p) {
+  __shared__ Choice c;
+  extern __shared__ float red[];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  choose_experts(p, c, warp, lane);
+  if (c.num_used == 0) {
+    for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < static_cast<long long>(p.T) * p.H; i += static_cast<long long>(gridDim.x) * kThreads)
+      static_cast<T*>(p.out)[i] = from_f32<T>(0.0f);
+    return;
+  }
+  {
+    const Run run(static_cast<long long>(c.num_used) * (p.F / 8));
+    run_pieces<T, f8, NT, false>(p, c, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, 0});
+  }
+  {
+    const Run run(static_cast<long long>(c.num_used) * ((p.H + kFewRows - 1) / kFewRows));
+    run_pieces<T, f8, NT, true>(p, c, run.lo, run.hi, warp, lane, DownDone<T, NT>{p, c, red, warp, lane, run.lo, run.pieces, run.blocks});
+  }
+}
+
+// The second kernel's blocks: one per SM that can hold one, all at once.
+template <typename T, bool f8, int NT>
 cudaError_t launch_experts(const FewParams& p, int num_sms, cudaStream_t s) {
-  return launch_pdl_ex(ep_few_experts_kernel<T, f8>, dim3(num_sms), dim3(kThreads), 0, s, 0, true, p);
+  constexpr size_t smem = sizeof(float) * 2 * kWarps * 16 * 8 * NT;
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  const auto kern = ep_few_experts_kernel<T, f8, NT>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  int blocks = known[dev].load(std::memory_order_acquire);
+  if (blocks == 0) {
+    int per_sm = 0;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorLaunchOutOfResources;
+    blocks = std::min(num_sms, kFewBlocksMax);
+    known[dev].store(blocks, std::memory_order_release);
+  }
+  return launch_pdl_ex(kern, dim3(blocks), dim3(kThreads), smem, s, 0, true, p);
+}
+
+template <typename T, bool f8>
+cudaError_t launch_sized(const FewParams& p, int num_sms, cudaStream_t s) {
+  if (p.T <= 8) return launch_experts<T, f8, 1>(p, num_sms, s);
+  if (p.T <= 16) return launch_experts<T, f8, 2>(p, num_sms, s);
+  return launch_experts<T, f8, 4>(p, num_sms, s);
 }
 
 template <typename T>
 cudaError_t launch_typed(const FewParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid(p.E + (p.f8 ? p.T : 0)), block(kThreads);
+  const dim3 grid(p.E + (p.f8 ? p.T : 0)), block(kGateThreads);
   const cudaError_t e = p.gate_dtype == EP_DTYPE_FP32   ? launch_pdl(ep_few_gate_kernel<float, T>, grid, block, 0, s, 0, p)
                         : p.gate_dtype == EP_DTYPE_FP16 ? launch_pdl(ep_few_gate_kernel<__half, T>, grid, block, 0, s, 0, p)
                                                         : launch_pdl(ep_few_gate_kernel<__nv_bfloat16, T>, grid, block, 0, s, 0, p);
   if (e != cudaSuccess) return e;
-  return p.f8 ? launch_experts<T, true>(p, num_sms, s) : launch_experts<T, false>(p, num_sms, s);
+  return p.f8 ? launch_sized<T, true>(p, num_sms, s) : launch_sized<T, false>(p, num_sms, s);
 }
 
 }  // namespace
