@@ -12,15 +12,16 @@
 // arranged to keep loads in flight and all SMs busy to the end.
 // - A piece of work is 16 weight rows (8 gate rows and their 8 up rows, or 16
 //   output rows of one expert) times the whole reduction; the pieces are dealt
-//   out in even runs.  The 16 warps of a block split the reduction: each lane
-//   loads 16 bytes of row lane / 4 and of row lane / 4 + 8, four such pairs ahead
-//   of their use and across the ends of pieces.
+//   out in even runs.  The 16 warps of a block split the reduction in steps of
+//   128 bytes: each lane loads 16 bytes of either half of it from row lane / 4
+//   and from row lane / 4 + 8, two or three steps ahead of their use and across
+//   the ends of pieces.
 // - They are the 16 x K side of mma.sync as they lie: a sum does not depend on
 //   its order, so a lane's 16 bytes may count as any of the fragment's columns,
 //   if the tokens' operand (the same 16 bytes of token lane / 4) does too.
 // - Up to eight tokens of an expert, side by side, are one n-tile.  8-bit
-//   operands are multiplied as e4m3; a step of 64 elements lies within a block
-//   of 128 and its sum is scaled in float32.
+//   operands are multiplied as e4m3; a step is then one block of 128, and its
+//   sum is scaled in float32.
 // - A tile of outputs sums over experts in registers and shared memory.  Where
 //   the run of a block ends inside a tile, the parts go to the workspace and
 //   the block that comes last adds them in the blocks' order: no output depends
@@ -37,7 +38,6 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kGateThreads = 256, kGateWarps = kGateThreads / 32;
 constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kAhead = 4;  // steps whose weights are in flight
 
 template <typename G, typename T>
 __global__ void __launch_bounds__(kGateThreads) ep_few_gate_kernel(const FewParams p) {
@@ -272,111 +272,167 @@ struct Walk {
   }
 };
 
-// A block's run [lo, hi) of `pieces`: of each piece, warp w takes the steps w,
-// w + 16, ... of the reduction.  done(piece, sums, last step's index) is called
-// by all warps when a piece's steps are over.
+// What follows from the number of n-tiles: steps in flight, and pieces of the
+// gated products that are joined at a time.  With four n-tiles the registers
+// hold the tokens' operand of one step alone.
+template <int NT>
+struct Depth {
+  static constexpr int kAhead = NT == 1 ? 3 : 2;
+  static constexpr bool kTokensAhead = NT < 4;
+  static constexpr int kBatch = 4 / NT;
+};
+
+// A block's run [lo, hi) of pieces: of each piece, warp w takes the steps w,
+// w + 16, ... of the reduction (128 bytes of a row each).  done(piece, sums,
+// whether it is the run's last) is called by all warps when a piece's steps
+// are over; done.wait() when the weights' first steps are on their way.
 template <typename T, bool f8, int NT, bool down, typename Done>
 __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, int lo, int hi, int warp, int lane, Done done) {
   using E = typename std::conditional<f8, uint8_t, T>::type;
-  constexpr int kVec = 16 / sizeof(E), kStep = 4 * kVec;  // elements of a lane's load and of a step
-  const int red = down ? p.F : p.H, rows = down ? p.H : 2 * p.F;
-  const int steps = (red + kStep - 1) / kStep, turns = (steps + kWarps - 1) / kWarps;
+  constexpr int kAhead = Depth<NT>::kAhead, kTokens = Depth<NT>::kTokensAhead ? kAhead : 1;
+  constexpr int kStepBytes = 128;
+  const int red = (down ? p.F : p.H) * static_cast<int>(sizeof(E)), rows = down ? p.H : 2 * p.F;  // red in bytes
+  const int turns = ((red + kStepBytes - 1) / kStepBytes + kWarps - 1) / kWarps;
   const int total = (hi - lo) * turns;
   const int g = lane >> 2, t = lane & 3;
-  const E* w = static_cast<const E*>(down ? p.w2 : p.w13);
-  const float* ws = down ? p.s2 : p.s13;
-  const E* x = f8 ? reinterpret_cast<const E*>(down ? p.aq : p.xq) : static_cast<const E*>(down ? p.act : p.x);
+  const int k0 = warp * kStepBytes + t * 16;  // this lane's first byte of a row
+  const char* w = static_cast<const char*>(down ? p.w2 : p.w13);
+  const char* x = static_cast<const char*>(f8 ? (down ? p.aq : p.xq) : down ? p.act : p.x);
   const float* xs = down ? p.as : p.xs;
-  const int xcols = scale_columns(red), wcols = f8_blocks(red), wblocks = f8_blocks(rows);
-  uint4 a[kAhead][2], b[2][NT];
-  float sw[2][2], sx[2][NT][2];
+  const int xcols = f8 ? scale_columns(red) : 0, wcols = f8 ? f8_blocks(red) : 0, wblocks = f8 ? f8_blocks(rows) : 0;
+  const long long delta = static_cast<long long>(down ? 8 : p.F) * red;  // from a piece's first eight rows to its second
+  uint4 a[kAhead][4], b[kTokens][NT][2];
+  float sw[kTokens][2], sx[kTokens][NT][2];
+  // The weights' place.
+  struct {
+    const char* row;
+    bool second;
+    int turn;
+  } at_a;
+  // The tokens': byte offsets of their rows and of their scales' rows, -1: none.
+  struct {
+    int row[NT], scale[NT][2], turn;
+    const float *w0, *w1;
+  } at_b;
   Walk<down> walk_a(p, c, lo), walk_b(p, c, lo), walk_c(p, c, lo);
-  Piece pa, pb, pc;
-  int ja = 0, jb = 0, jc = 0;
-  if (total > 0) pa = pb = pc = walk_a.at();
-  auto load_a = [&](uint4 (&to)[2]) {
-    const int k = (warp + ja * kWarps) * kStep + t * kVec;
-    to[0] = to[1] = make_uint4(0, 0, 0, 0);
-    if (k < red) {
-      const E* base = w + static_cast<long long>(pa.e) * rows * red + k;
-      to[0] = load_stream(base + static_cast<long long>(pa.row0 + g) * red);
-      if (!down || pa.row1 >= 0) to[1] = load_stream(base + static_cast<long long>(pa.row1 + g) * red);
-    }
-    if (++ja == turns) {
-      ja = 0;
-      walk_a.next();
-      if (walk_a.u < c.num_used && walk_a.tile < walk_a.tiles) pa = walk_a.at();
-    }
+  auto place_a = [&]() {
+    const Piece o = walk_a.at();
+    at_a.row = w + (static_cast<long long>(o.e) * rows + o.row0 + g) * red + k0;
+    at_a.second = !down || o.row1 >= 0;
+    at_a.turn = 0;
   };
-  auto load_b = [&](int to) {
-    const int step = warp + jb * kWarps, k = step * kStep + t * kVec;
+  auto place_b = [&]() {
+    const Piece o = walk_b.at();
+    at_b.turn = 0;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      b[to][i] = make_uint4(0, 0, 0, 0);
-      if (8 * i + g < pb.n && k < red) {
-        const int row = down ? pb.pos + 8 * i + g : c.token[pb.pos + 8 * i + g];
-        const E* at = x + static_cast<long long>(row) * red + k;
-        // act is written in this kernel: not through the read-only path
-        b[to][i] = down ? __ldcg(reinterpret_cast<const uint4*>(at)) : __ldg(reinterpret_cast<const uint4*>(at));
+      const int col = 8 * i + g;
+      at_b.row[i] = col < o.n ? (down ? o.pos + col : c.token[o.pos + col]) * red + k0 : -1;
+      if constexpr (f8) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int col2 = 8 * i + 2 * t + q;
+          at_b.scale[i][q] = col2 < o.n ? (down ? o.pos + col2 : c.token[o.pos + col2]) * xcols : -1;
+        }
       }
     }
     if constexpr (f8) {
-      const int block = min(step * kStep / kF8Block, wcols - 1);
-      const float* s = ws + static_cast<long long>(pb.e) * wblocks * wcols + block;
-      sw[to][0] = __ldg(s + static_cast<long long>(pb.row0 / kF8Block) * wcols);
-      sw[to][1] = down ? sw[to][0] : __ldg(s + static_cast<long long>(pb.row1 / kF8Block) * wcols);
+      const float* s = p.s13;
+      if (down) s = p.s2;
+      at_b.w0 = s + (static_cast<long long>(o.e) * wblocks + o.row0 / kF8Block) * wcols;
+      at_b.w1 = down ? at_b.w0 : s + (static_cast<long long>(o.e) * wblocks + o.row1 / kF8Block) * wcols;
+    }
+  };
+  auto load_a = [&](uint4 (&to)[4]) {
+    const int k = at_a.turn * (kWarps * kStepBytes);
+    const bool in0 = k + k0 < red, in1 = k + k0 + 64 < red;
+    const char* at = at_a.row + k;
+    to[0] = to[1] = to[2] = to[3] = make_uint4(0, 0, 0, 0);
+    if (in0) to[0] = load_stream(at);
+    if (in0 && at_a.second) to[1] = load_stream(at + delta);
+    if (in1) to[2] = load_stream(at + 64);
+    if (in1 && at_a.second) to[3] = load_stream(at + delta + 64);
+    if (++at_a.turn == turns) {
+      walk_a.next();
+      if (walk_a.u < c.num_used && walk_a.tile < walk_a.tiles) place_a();
+    }
+  };
+  auto load_b = [&](int to) {
+    const int k = at_b.turn * (kWarps * kStepBytes);
+    const bool in0 = k + k0 < red, in1 = k + k0 + 64 < red;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      b[to][i][0] = b[to][i][1] = make_uint4(0, 0, 0, 0);
+      if (at_b.row[i] >= 0) {
+        const uint4* at = reinterpret_cast<const uint4*>(x + at_b.row[i] + k);
+        // act is written in this kernel: not through the read-only path
+        if (in0) b[to][i][0] = down ? __ldcg(at) : __ldg(at);
+        if (in1) b[to][i][1] = down ? __ldcg(at + 4) : __ldg(at + 4);
+      }
+    }
+    if constexpr (f8) {
+      // One block of 128 a step.  A step past the end has zeros, times the last block's scale.
+      const int block = min(warp + at_b.turn * kWarps, wcols - 1);
+      sw[to][0] = __ldg(at_b.w0 + block);
+      sw[to][1] = down ? sw[to][0] : __ldg(at_b.w1 + block);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int col = 8 * i + 2 * t + q;
-          sx[to][i][q] = 0.0f;
-          if (col < pb.n) {
-            const int row = down ? pb.pos + col : c.token[pb.pos + col];
-            sx[to][i][q] = __ldcg(xs + static_cast<long long>(row) * xcols + block);
-          }
-        }
+        for (int q = 0; q < 2; ++q) sx[to][i][q] = at_b.scale[i][q] >= 0 ? __ldcg(xs + at_b.scale[i][q] + block) : 0.0f;
     }
-    if (++jb == turns) {
-      jb = 0;
+    if (++at_b.turn == turns) {
       walk_b.next();
-      if (walk_b.u < c.num_used && walk_b.tile < walk_b.tiles) pb = walk_b.at();
+      if (walk_b.u < c.num_used && walk_b.tile < walk_b.tiles) place_b();
     }
   };
+  if (total > 0) place_a();
 #pragma unroll
   for (int q = 0; q < kAhead; ++q)
     if (q < total) load_a(a[q]);
-  if constexpr (down) done.wait();  // the weights are on their way while the blocks wait for act
-  if (total > 0) load_b(0);
+  done.wait();
+  if (total > 0) place_b();
+  if constexpr (Depth<NT>::kTokensAhead) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (q < total) load_b(q);
+  }
   float sum[NT][4] = {};
+  int turn = 0;
+  int n_tokens = 0;
+  if (total > 0) n_tokens = walk_c.at().n;
   for (int n0 = 0; n0 < total; n0 += kAhead) {
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
       const int n = n0 + q;
       if (n >= total) break;
-      if (n + 1 < total) load_b((q + 1) & 1);
+      constexpr bool ahead = Depth<NT>::kTokensAhead;
+      const int from = ahead ? q : 0;
+      if (!ahead) load_b(0);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        if (8 * i >= pc.n) break;
-        const uint4 &u = a[q][0], &v = a[q][1], &y = b[q & 1][i];
-        if constexpr (f8) {
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma<E>(d, u.x, v.x, u.y, v.y, y.x, y.y);
-          mma<E>(d, u.z, v.z, u.w, v.w, y.z, y.w);
-          // A step without elements has zeros times whatever scale the block before has.
+        if (NT > 1 && 8 * i >= n_tokens) break;
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float (&to)[4] = f8 ? d : sum[i];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[j], sw[q & 1][j >> 1] * sx[q & 1][i][j & 1], sum[i][j]);
-        } else {
-          mma<E>(sum[i], u.x, v.x, u.y, v.y, y.x, y.y);
-          mma<E>(sum[i], u.z, v.z, u.w, v.w, y.z, y.w);
+        for (int h = 0; h < 2; ++h) {
+          const uint4 &u = a[q][2 * h], &v = a[q][2 * h + 1], &y = b[from][i][h];
+          mma<E>(to, u.x, v.x, u.y, v.y, y.x, y.y);
+          mma<E>(to, u.z, v.z, u.w, v.w, y.z, y.w);
+        }
+        if constexpr (f8) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[j], sw[from][j >> 1] * sx[from][i][j & 1], sum[i][j]);
         }
       }
-      if (n + kAhead < total) load_a(a[q]);
-      if (++jc == turns) {
-        jc = 0;
+      if (n + kAhead < total) {
+        load_a(a[q]);
+        if (ahead) load_b(q);
+      }
+      if (++turn == turns) {
+        turn = 0;
+        done(walk_c.at(), sum, n + 1 == total);
         walk_c.next();
-        done(pc, sum, n + 1 == total);
-        if (n + 1 < total) pc = walk_c.at();
+        if (n + 1 < total) n_tokens = walk_c.at().n;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -386,19 +442,20 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
   }
 }
 
-// After a piece of the gated products: its 16 warps' sums are joined, the
-// activation taken and written; with 8-bit weights the last piece of 128
-// features quantises them.
+// After a piece of the gated products its warps' sums go to shared memory;
+// after kBatch of them they are joined, the activation is taken and written,
+// and with 8-bit weights the last piece of 128 features quantises those.
 template <typename T, bool f8, int NT>
 struct UpDone {
+  static constexpr int kCols = 8 * NT, kBatch = Depth<NT>::kBatch;
+  static constexpr int kPieceFloats = kWarps * 16 * kCols;
   const FewParams& p;
   Choice& c;
-  float* red;  // [2][kWarps][16][8 NT]
-  int warp, lane, turn;
+  float* red;  // [2][kBatch][kWarps][16][kCols]
+  int warp, lane, first, have, turn;  // first: the batch's first piece
   __device__ __forceinline__ void wait() const {}
-  __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool) {
-    constexpr int kCols = 8 * NT;
-    float* mine = red + (turn * kWarps + warp) * 16 * kCols;
+  __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool end) {
+    float* mine = red + (turn * kBatch + have) * kPieceFloats + warp * 16 * kCols;
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -406,43 +463,53 @@ struct UpDone {
       *reinterpret_cast<float2*>(mine + g * kCols + 8 * i + 2 * t) = make_float2(sum[i][0], sum[i][1]);
       *reinterpret_cast<float2*>(mine + (g + 8) * kCols + 8 * i + 2 * t) = make_float2(sum[i][2], sum[i][3]);
     }
+    if (++have < kBatch && !end) return;
     __syncthreads();
-    const int f = threadIdx.x & 7, col = threadIdx.x >> 3;
-    if (col < o.n) {
-      const float* at = red + turn * kWarps * 16 * kCols + f * kCols + col;
-      float gate = 0.0f, up = 0.0f;
+    const int col = threadIdx.x % kCols, f = threadIdx.x / kCols % 8, b = threadIdx.x / (8 * kCols);
+    if (b < have) {
+      const Piece q = Walk<false>(p, c, first + b).at();
+      if (col < q.n) {
+        const float* at = red + (turn * kBatch + b) * kPieceFloats + f * kCols + col;
+        float gate = 0.0f, up = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        gate += at[w * 16 * kCols];
-        up += at[w * 16 * kCols + 8 * kCols];
+        for (int w = 0; w < kWarps; ++w) {
+          gate += at[w * 16 * kCols];
+          up += at[w * 16 * kCols + 8 * kCols];
+        }
+        const float a = swiglu(gate, up);
+        const long long i = static_cast<long long>(q.pos + col) * p.F + q.tile * 8 + f;
+        if constexpr (f8) static_cast<float*>(p.act)[i] = a;
+        else static_cast<T*>(p.act)[i] = from_f32<T>(a);
       }
-      const float a = swiglu(gate, up);
-      const long long i = static_cast<long long>(o.pos + col) * p.F + o.tile * 8 + f;
-      if constexpr (f8) static_cast<float*>(p.act)[i] = a;
-      else static_cast<T*>(p.act)[i] = from_f32<T>(a);
     }
-    turn ^= 1;  // the other buffer next: the sums here are still being read
     if constexpr (f8) {
-      const int block = o.tile / (kF8Block / 8);
       __threadfence();
+      if (threadIdx.x == 0) c.last = 0;
       __syncthreads();
-      if (threadIdx.x == 0) {
-        c.last = atomicAdd(p.written + o.u * f8_blocks(p.F) + block, 1) == kF8Block / 8 - 1;
+      if (threadIdx.x < have) {
+        const Piece q = Walk<false>(p, c, first + threadIdx.x).at();
+        const int block = q.tile / (kF8Block / 8);
+        if (atomicAdd(p.written + q.u * f8_blocks(p.F) + block, 1) == kF8Block / 8 - 1) atomicOr(&c.last, 1 << threadIdx.x);
         __threadfence();
       }
       __syncthreads();
-      if (c.last) {
-        for (int col8 = warp; col8 < o.n; col8 += kWarps) {
-          const long long at = static_cast<long long>(o.pos + col8) * p.F + block * kF8Block + lane * 4;
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(p.act) + at));
-          float m = max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
+      for (int left = c.last; left; left &= left - 1) quantize(Walk<false>(p, c, first + __ffs(left) - 1).at());
+    }
+    turn ^= 1;  // the other buffer next: the sums here are still being read
+    first += have;
+    have = 0;
+  }
+  __device__ __forceinline__ void quantize(const Piece& o) const {
+    const int block = o.tile / (kF8Block / 8);
+    for (int col = warp; col < o.n; col += kWarps) {
+      const long long at = static_cast<long long>(o.pos + col) * p.F + block * kF8Block + lane * 4;
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(p.act) + at));
+      float m = max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, d));
-          const BlockScale s = block_scale(m);
-          *reinterpret_cast<uint32_t*>(p.aq + at) = e4m3x4(v.x * s.inv, v.y * s.inv, v.z * s.inv, v.w * s.inv);
-          if (lane == 0) p.as[static_cast<long long>(o.pos + col8) * scale_columns(p.F) + block] = s.scale;
-        }
-      }
+      for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, d));
+      const BlockScale s = block_scale(m);
+      *reinterpret_cast<uint32_t*>(p.aq + at) = e4m3x4(v.x * s.inv, v.y * s.inv, v.z * s.inv, v.w * s.inv);
+      if (lane == 0) p.as[static_cast<long long>(o.pos + col) * scale_columns(p.F) + block] = s.scale;
     }
   }
 };
@@ -550,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) ep_few_experts_kernel(const FewPa
   }
   {
     const Run run(static_cast<long long>(c.num_used) * (p.F / 8));
-    run_pieces<T, f8, NT, false>(p, c, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, 0});
+    run_pieces<T, f8, NT, false>(p, c, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, run.lo, 0, 0});
   }
   {
     const Run run(static_cast<long long>(c.num_used) * ((p.H + kFewRows - 1) / kFewRows));
@@ -561,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) ep_few_experts_kernel(const FewPa
 // The second kernel's blocks: one per SM that can hold one, all at once.
 template <typename T, bool f8, int NT>
 cudaError_t launch_experts(const FewParams& p, int num_sms, cudaStream_t s) {
-  constexpr size_t smem = sizeof(float) * 2 * kWarps * 16 * 8 * NT;
+  constexpr size_t smem = sizeof(float) * 2 * UpDone<T, f8, NT>::kBatch * UpDone<T, f8, NT>::kPieceFloats;
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices];
   const auto kern = ep_few_experts_kernel<T, f8, NT>;
