@@ -359,9 +359,9 @@ ep_status_t ep_moe_few(ep_moe_few_config_t config, const void* x, const void* ga
   p.zeros = l.zeros;
   p.logits = at<float>(workspace, l.logits);
   p.act = at<char>(workspace, l.act);
-  p.xq = at<uint8_t>(workspace, l.xq);
+  p.xq = at<__half>(workspace, l.xq);
   p.xs = at<float>(workspace, l.xs);
-  p.aq = at<uint8_t>(workspace, l.aq);
+  p.aq = at<__half>(workspace, l.aq);
   p.as = at<float>(workspace, l.as);
   p.part = at<float>(workspace, l.part);
   p.router.logits = p.logits;

@@ -20,8 +20,10 @@
 //   its order, so a lane's 16 bytes may count as any of the fragment's columns,
 //   if the tokens' operand (the same 16 bytes of token lane / 4) does too.
 // - Up to eight tokens of an expert, side by side, are one n-tile.  8-bit
-//   operands are multiplied as e4m3; a step is then one block of 128, and its
-//   sum is scaled in float32.
+//   weights become fp16 (exactly) on the way to the tensor cores, the tokens'
+//   8-bit values are kept in fp16: mma.sync on e4m3 itself converts both
+//   operands anew for every n-tile (16 tokens, 7168 -> 2 x 2048 of 64 experts:
+//   1,056 us).  A step is then one block of 128, its sum scaled in float32.
 // - A tile of outputs sums over experts in registers and shared memory.  Where
 //   the run of a block ends inside a tile, the parts go to the workspace and
 //   the block that comes last adds them in the blocks' order: no output depends
@@ -39,49 +41,67 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kGateThreads = 256, kGateWarps = kGateThreads / 32;
 constexpr int kWarps = 16, kThreads = kWarps * 32;
 
+constexpr int kGateTokens = 8;  // of a block
+
+// Four e4m3 values as fp16: elements 0 and 1, 2 and 3.
+__device__ __forceinline__ void fp16_of(uint32_t q, uint32_t* lo, uint32_t* hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n" : "=r"(*lo), "=r"(*hi) : "r"(q));
+}
+__device__ __forceinline__ uint4 fp16_of(const uint2& q) {
+  uint4 r;
+  fp16_of(q.x, &r.x, &r.y);
+  fp16_of(q.y, &r.z, &r.w);
+  return r;
+}
+
+// Block (e, y): the logits of expert e and tokens 8 y to 8 y + 7; blocks (E + t,
+// 0): token t's row in 8 bits, its values kept in fp16, which holds them exactly.
 template <typename G, typename T>
 __global__ void __launch_bounds__(kGateThreads) ep_few_gate_kernel(const FewParams p) {
-  __shared__ float part[kGateWarps][EP_MAX_FEW_TOKENS];
+  __shared__ float part[kGateWarps][kGateTokens];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = blockIdx.x * kGateThreads + threadIdx.x; i < p.zeros; i += gridDim.x * kGateThreads) p.hdr[i] = 0;
+  for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * kGateThreads + threadIdx.x; i < p.zeros; i += gridDim.x * gridDim.y * kGateThreads)
+    p.hdr[i] = 0;
   if (static_cast<int>(blockIdx.x) < p.E) {
-    const int e = blockIdx.x;
-    float acc[EP_MAX_FEW_TOKENS];
+    const int e = blockIdx.x, t0 = blockIdx.y * kGateTokens;
+    float acc[kGateTokens];
 #pragma unroll
-    for (int t = 0; t < EP_MAX_FEW_TOKENS; ++t) acc[t] = 0.0f;
+    for (int t = 0; t < kGateTokens; ++t) acc[t] = 0.0f;
     for (int k = threadIdx.x * 8; k < p.H; k += kGateThreads * 8) {
       Raw8<G> g;
-      float gv[8];
+      Raw8<T> x[kGateTokens];
       g.load(static_cast<const G*>(p.gate) + static_cast<long long>(e) * p.H + k);
+#pragma unroll
+      for (int t = 0; t < kGateTokens; ++t)
+        if (t0 + t < p.T) x[t].load(static_cast<const T*>(p.x) + static_cast<long long>(t0 + t) * p.H + k);
+      float gv[8];
       g.get(gv);
 #pragma unroll
-      for (int t = 0; t < EP_MAX_FEW_TOKENS; ++t) {
-        if (t < p.T) {
-          Raw8<T> x;
+      for (int t = 0; t < kGateTokens; ++t) {
+        if (t0 + t < p.T) {
           float xv[8];
-          x.load(static_cast<const T*>(p.x) + static_cast<long long>(t) * p.H + k);
-          x.get(xv);
+          x[t].get(xv);
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[t] = fmaf(gv[j], xv[j], acc[t]);
         }
       }
     }
 #pragma unroll
-    for (int t = 0; t < EP_MAX_FEW_TOKENS; ++t) {
-      if (t < p.T) {
+    for (int t = 0; t < kGateTokens; ++t) {
+      if (t0 + t < p.T) {
         const float s = route::warp_sum(acc[t]);
         if (lane == 0) part[warp][t] = s;
       }
     }
     __syncthreads();
-    if (threadIdx.x < p.T) {
+    if (threadIdx.x < kGateTokens && t0 + threadIdx.x < p.T) {
       float s = 0.0f;
       for (int w = 0; w < kGateWarps; ++w) s += part[w][threadIdx.x];
-      p.logits[threadIdx.x * p.E + e] = s;
+      p.logits[(t0 + threadIdx.x) * p.E + e] = s;
     }
-  } else {  // a token's row in 8 bits
+  } else if (blockIdx.y == 0) {
     const int t = blockIdx.x - p.E, cols = scale_columns(p.H);
     for (int b = warp * 2; b < cols; b += kGateWarps * 2) {
       const int k = b * kF8Block + lane * 8;
@@ -93,7 +113,7 @@ __global__ void __launch_bounds__(kGateThreads) ep_few_gate_kernel(const FewPara
       }
       uint2 q;
       const float s = quantize8(v, &q);
-      if (k < p.H) *reinterpret_cast<uint2*>(p.xq + static_cast<long long>(t) * p.H + k) = q;
+      if (k < p.H) *reinterpret_cast<uint4*>(p.xq + static_cast<long long>(t) * p.H + k) = fp16_of(q);
       if ((lane & 15) == 0) p.xs[t * cols + b + (lane >> 4)] = k < p.H ? s : 0.0f;
     }
   }
@@ -204,8 +224,7 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
   return v;
 }
 
-// d += a b: a the 16 weight rows' words, b the 8 tokens' (T: bf16, fp16, or
-// uint8_t for e4m3).
+// d += a b: a the 16 weight rows' words, b the 8 tokens'.
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1);
 template <>
@@ -218,12 +237,6 @@ __device__ __forceinline__ void mma<__half>(float (&d)[4], uint32_t a0, uint32_t
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-template <>
-__device__ __forceinline__ void mma<uint8_t>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // Where a piece of work lies: its expert, its two eights of weight rows and the
 // rows of the tokens' operand.
 struct Piece {
@@ -272,15 +285,17 @@ struct Walk {
   }
 };
 
-// What follows from the number of n-tiles: steps in flight, and pieces of the
-// gated products that are joined at a time.  With four n-tiles the registers
-// hold the tokens' operand of one step alone.
-template <int NT>
+// What the registers allow: steps of weights in flight, whether the tokens'
+// operand comes as far ahead or half a step at a time, just before its use, and
+// how many pieces of the gated products are joined at a time.
+template <bool f8, int NT>
 struct Depth {
-  static constexpr int kAhead = NT == 1 ? 3 : 2;
-  static constexpr bool kTokensAhead = NT < 4;
+  static constexpr int kAhead = NT == 1 && !f8 ? 3 : 2;
+  static constexpr bool kTokensAhead = NT == 1 || (NT == 2 && !f8);
   static constexpr int kBatch = 4 / NT;
 };
+
+constexpr int kRedFloats = 2 * 4 * kWarps * 16 * 8;  // two batches' sums
 
 // A block's run [lo, hi) of pieces: of each piece, warp w takes the steps w,
 // w + 16, ... of the reduction (128 bytes of a row each).  done(piece, sums,
@@ -289,19 +304,20 @@ struct Depth {
 template <typename T, bool f8, int NT, bool down, typename Done>
 __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, int lo, int hi, int warp, int lane, Done done) {
   using E = typename std::conditional<f8, uint8_t, T>::type;
-  constexpr int kAhead = Depth<NT>::kAhead, kTokens = Depth<NT>::kTokensAhead ? kAhead : 1;
-  constexpr int kStepBytes = 128;
+  constexpr int kAhead = Depth<f8, NT>::kAhead, kTokens = Depth<f8, NT>::kTokensAhead ? kAhead : 1;
+  constexpr bool ahead = Depth<f8, NT>::kTokensAhead;
+  constexpr int kStepBytes = 128, kWords = f8 ? 4 : 2;  // of a row of weights; the tokens' 16-byte words for a lane's share of it
   const int red = (down ? p.F : p.H) * static_cast<int>(sizeof(E)), rows = down ? p.H : 2 * p.F;  // red in bytes
   const int turns = ((red + kStepBytes - 1) / kStepBytes + kWarps - 1) / kWarps;
   const int total = (hi - lo) * turns;
   const int g = lane >> 2, t = lane & 3;
   const int k0 = warp * kStepBytes + t * 16;  // this lane's first byte of a row
   const char* w = static_cast<const char*>(down ? p.w2 : p.w13);
-  const char* x = static_cast<const char*>(f8 ? (down ? p.aq : p.xq) : down ? p.act : p.x);
-  const float* xs = down ? p.as : p.xs;
+  const char* x = f8 ? reinterpret_cast<const char*>(down ? p.aq : p.xq) : static_cast<const char*>(down ? p.act : p.x);
+  const float* xs = down ? p.as : done.token_scales();
   const int xcols = f8 ? scale_columns(red) : 0, wcols = f8 ? f8_blocks(red) : 0, wblocks = f8 ? f8_blocks(rows) : 0;
   const long long delta = static_cast<long long>(down ? 8 : p.F) * red;  // from a piece's first eight rows to its second
-  uint4 a[kAhead][4], b[kTokens][NT][2];
+  uint4 a[kAhead][4], b[kTokens][NT][ahead ? kWords : kWords / 2];
   float sw[kTokens][2], sx[kTokens][NT][2];
   // The weights' place.
   struct {
@@ -327,7 +343,7 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int col = 8 * i + g;
-      at_b.row[i] = col < o.n ? (down ? o.pos + col : c.token[o.pos + col]) * red + k0 : -1;
+      at_b.row[i] = col < o.n ? ((down ? o.pos + col : c.token[o.pos + col]) * red + k0) * (f8 ? 2 : 1) : -1;
       if constexpr (f8) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -357,19 +373,26 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
       if (walk_a.u < c.num_used && walk_a.tile < walk_a.tiles) place_a();
     }
   };
-  auto load_b = [&](int to) {
+  // Words [from, from + count) of the step's tokens' operand.
+  auto load_words = [&](int to, int from, int count) {
     const int k = at_b.turn * (kWarps * kStepBytes);
     const bool in0 = k + k0 < red, in1 = k + k0 + 64 < red;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      b[to][i][0] = b[to][i][1] = make_uint4(0, 0, 0, 0);
-      if (at_b.row[i] >= 0) {
-        const uint4* at = reinterpret_cast<const uint4*>(x + at_b.row[i] + k);
-        // act is written in this kernel: not through the read-only path
-        if (in0) b[to][i][0] = down ? __ldcg(at) : __ldg(at);
-        if (in1) b[to][i][1] = down ? __ldcg(at + 4) : __ldg(at + 4);
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        if (j >= count) break;
+        const int half = (from + j) / (kWords / 2), word = 4 * half * (kWords / 2) + (from + j) % (kWords / 2);
+        b[to][i][j] = make_uint4(0, 0, 0, 0);
+        if (at_b.row[i] >= 0 && (half == 0 ? in0 : in1)) {
+          const uint4* at = reinterpret_cast<const uint4*>(x + at_b.row[i] + k * (f8 ? 2 : 1)) + word;
+          b[to][i][j] = down ? __ldcg(at) : __ldg(at);  // act is written in this kernel: not through the read-only path
+        }
       }
     }
+  };
+  // The step's scales, and on to the next.
+  auto load_scales = [&](int to) {
     if constexpr (f8) {
       // One block of 128 a step.  A step past the end has zeros, times the last block's scale.
       const int block = min(warp + at_b.turn * kWarps, wcols - 1);
@@ -378,12 +401,20 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) sx[to][i][q] = at_b.scale[i][q] >= 0 ? __ldcg(xs + at_b.scale[i][q] + block) : 0.0f;
+        for (int q = 0; q < 2; ++q)
+          sx[to][i][q] = at_b.scale[i][q] < 0 ? 0.0f : down ? __ldcg(xs + at_b.scale[i][q] + block) : xs[at_b.scale[i][q] + block];
     }
+  };
+  auto next_b = [&]() {
     if (++at_b.turn == turns) {
       walk_b.next();
       if (walk_b.u < c.num_used && walk_b.tile < walk_b.tiles) place_b();
     }
+  };
+  auto load_b = [&](int to) {
+    load_words(to, 0, kWords);
+    load_scales(to);
+    next_b();
   };
   if (total > 0) place_a();
 #pragma unroll
@@ -391,7 +422,7 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
     if (q < total) load_a(a[q]);
   done.wait();
   if (total > 0) place_b();
-  if constexpr (Depth<NT>::kTokensAhead) {
+  if constexpr (ahead) {
 #pragma unroll
     for (int q = 0; q < kAhead; ++q)
       if (q < total) load_b(q);
@@ -405,25 +436,36 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
     for (int q = 0; q < kAhead; ++q) {
       const int n = n0 + q;
       if (n >= total) break;
-      constexpr bool ahead = Depth<NT>::kTokensAhead;
       const int from = ahead ? q : 0;
-      if (!ahead) load_b(0);
+      if (!ahead) load_scales(0);
+      float d[NT][4] = {};
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if (NT > 1 && 8 * i >= n_tokens) break;
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        float (&to)[4] = f8 ? d : sum[i];
+      for (int h = 0; h < 2; ++h) {
+        if (!ahead) load_words(0, h * kWords / 2, kWords / 2);
+        const uint4 &u4 = a[q][2 * h], &v4 = a[q][2 * h + 1];
+        const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 &u = a[q][2 * h], &v = a[q][2 * h + 1], &y = b[from][i][h];
-          mma<E>(to, u.x, v.x, u.y, v.y, y.x, y.y);
-          mma<E>(to, u.z, v.z, u.w, v.w, y.z, y.w);
-        }
-        if constexpr (f8) {
+        for (int j = 0; j < (f8 ? 4 : 2); ++j) {
+          uint32_t u0 = u[2 * j & 3], u1 = u[(2 * j + 1) & 3], v0 = v[2 * j & 3], v1 = v[(2 * j + 1) & 3];
+          if constexpr (f8) {
+            fp16_of(u[j], &u0, &u1);
+            fp16_of(v[j], &v0, &v1);
+          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[j], sw[from][j >> 1] * sx[from][i][j & 1], sum[i][j]);
+          for (int i = 0; i < NT; ++i) {
+            if (NT > 1 && 8 * i >= n_tokens) break;
+            const uint4& y = b[from][i][(ahead ? h * kWords / 2 : 0) + j / 2];
+            mma<typename std::conditional<f8, __half, T>::type>(f8 ? d[i] : sum[i], u0, v0, u1, v1, j & 1 ? y.z : y.x, j & 1 ? y.w : y.y);
+          }
         }
       }
+      if constexpr (f8) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[i][j], sw[from][j >> 1] * sx[from][i][j & 1], sum[i][j]);
+      }
+      if (!ahead) next_b();
       if (n + kAhead < total) {
         load_a(a[q]);
         if (ahead) load_b(q);
@@ -447,12 +489,15 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
 // and with 8-bit weights the last piece of 128 features quantises those.
 template <typename T, bool f8, int NT>
 struct UpDone {
-  static constexpr int kCols = 8 * NT, kBatch = Depth<NT>::kBatch;
+  static constexpr int kCols = 8 * NT, kBatch = Depth<f8, NT>::kBatch;
   static constexpr int kPieceFloats = kWarps * 16 * kCols;
+  static_assert(2 * kBatch * kPieceFloats == kRedFloats, "shared memory");
   const FewParams& p;
   Choice& c;
   float* red;  // [2][kBatch][kWarps][16][kCols]
   int warp, lane, first, have, turn;  // first: the batch's first piece
+  const float* scales;  // 8-bit weights: the tokens', in shared memory
+  __device__ __forceinline__ const float* token_scales() const { return scales; }
   __device__ __forceinline__ void wait() const {}
   __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool end) {
     float* mine = red + (turn * kBatch + have) * kPieceFloats + warp * 16 * kCols;
@@ -508,7 +553,9 @@ struct UpDone {
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, d));
       const BlockScale s = block_scale(m);
-      *reinterpret_cast<uint32_t*>(p.aq + at) = e4m3x4(v.x * s.inv, v.y * s.inv, v.z * s.inv, v.w * s.inv);
+      uint2 q;
+      fp16_of(e4m3x4(v.x * s.inv, v.y * s.inv, v.z * s.inv, v.w * s.inv), &q.x, &q.y);
+      *reinterpret_cast<uint2*>(p.aq + at) = q;
       if (lane == 0) p.as[static_cast<long long>(o.pos + col) * scale_columns(p.F) + block] = s.scale;
     }
   }
@@ -523,6 +570,7 @@ struct DownDone {
   Choice& c;
   float* red;  // [kWarps][16][T]
   int warp, lane, lo, pieces, blocks;  // blocks: those that have pieces
+  __device__ __forceinline__ const float* token_scales() const { return nullptr; }
   __device__ __forceinline__ void zero() const {
     for (int i = lane; i < 16 * p.T; i += 32) red[warp * 16 * p.T + i] = 0.0f;
     __syncwarp();
@@ -555,36 +603,45 @@ struct DownDone {
     __syncwarp();  // an expert's columns are other lanes' in the next piece
     if (!end && o.u + 1 < c.num_used) return;
     __syncthreads();
-    const int first = block_of(static_cast<long long>(o.tile) * c.num_used);
-    const int last = block_of(static_cast<long long>(o.tile + 1) * c.num_used - 1);
-    const bool alone = first == last;
-    float* part = p.part + (static_cast<long long>(blockIdx.x) * 2 + (lo / c.num_used == o.tile ? 0 : 1)) * 16 * p.T;
+    const bool alone = first_block(o.tile) == last_block(o.tile);
     for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
       float s = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) s += red[w * 16 * p.T + i];
       if (alone) put(o.tile, i, s);
-      else part[i] = s;
+      else part_of(blockIdx.x, o.tile)[i] = s;
     }
-    if (!alone) {
+    if (end) {
+      // This block's first and last tile may be others' too: it says that its
+      // parts are there, and adds up the tiles of which it is the last to say so.
+      const int begins = lo / c.num_used;
       __threadfence();
+      if (threadIdx.x == 0) c.last = 0;
       __syncthreads();
-      if (threadIdx.x == 0) {
-        c.last = atomicAdd(p.done + o.tile, 1) == last - first;
+      if (threadIdx.x < 2) {
+        const int tile = threadIdx.x == 0 ? begins : o.tile, others = last_block(tile) - first_block(tile);
+        if (others > 0 && (threadIdx.x == 0 || tile != begins) && atomicAdd(p.done + tile, 1) == others) atomicOr(&c.last, 1 << threadIdx.x);
         __threadfence();
       }
       __syncthreads();
-      if (c.last) {
+      for (int left = c.last; left; left &= left - 1) {
+        const int tile = left & 1 ? begins : o.tile;
         for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
           float s = 0.0f;
-          for (int b = first; b <= last; ++b)
-            s += __ldcg(p.part + (static_cast<long long>(b) * 2 + (start_of(b) / c.num_used == o.tile ? 0 : 1)) * 16 * p.T + i);
-          put(o.tile, i, s);
+          for (int b = first_block(tile); b <= last_block(tile); ++b) s += __ldcg(part_of(b, tile) + i);
+          put(tile, i, s);
         }
       }
+      return;
     }
     __syncthreads();  // read: the sums begin again
     zero();
+  }
+  __device__ __forceinline__ int first_block(int tile) const { return block_of(static_cast<long long>(tile) * c.num_used); }
+  __device__ __forceinline__ int last_block(int tile) const { return block_of(static_cast<long long>(tile + 1) * c.num_used - 1); }
+  // A block has a place for its first tile's part and one for its last tile's.
+  __device__ __forceinline__ float* part_of(int block, int tile) const {
+    return p.part + (static_cast<long long>(block) * 2 + (start_of(block) / c.num_used == tile ? 0 : 1)) * 16 * p.T;
   }
   __device__ __forceinline__ void put(int tile, int i, float s) const {
     const int h = tile * kFewRows + i / p.T;
@@ -609,7 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1) ep_few_experts_kernel(const FewPa
   extern __shared__ float red[];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  choose_experts(p, c, warp, lane);
+  float* scales = red + kRedFloats;
+  if constexpr (f8)
+    for (int i = threadIdx.x; i < p.T * scale_columns(p.H); i += kThreads) scales[i] = p.xs[i];
+  choose_experts(p, c, warp, lane);  // has barriers
   if (c.num_used == 0) {
     for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < static_cast<long long>(p.T) * p.H; i += static_cast<long long>(gridDim.x) * kThreads)
       static_cast<T*>(p.out)[i] = from_f32<T>(0.0f);
@@ -617,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) ep_few_experts_kernel(const FewPa
   }
   {
     const Run run(static_cast<long long>(c.num_used) * (p.F / 8));
-    run_pieces<T, f8, NT, false>(p, c, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, run.lo, 0, 0});
+    run_pieces<T, f8, NT, false>(p, c, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, run.lo, 0, 0, scales});
   }
   {
     const Run run(static_cast<long long>(c.num_used) * ((p.H + kFewRows - 1) / kFewRows));
@@ -628,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1) ep_few_experts_kernel(const FewPa
 // The second kernel's blocks: one per SM that can hold one, all at once.
 template <typename T, bool f8, int NT>
 cudaError_t launch_experts(const FewParams& p, int num_sms, cudaStream_t s) {
-  constexpr size_t smem = sizeof(float) * 2 * UpDone<T, f8, NT>::kBatch * UpDone<T, f8, NT>::kPieceFloats;
+  constexpr size_t most = sizeof(float) * (kRedFloats + (f8 ? 8 * NT * (EP_MAX_NORM_HIDDEN / kF8Block) : 0));
+  const size_t smem = sizeof(float) * (kRedFloats + (f8 ? p.T * scale_columns(p.H) : 0));
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices];
   const auto kern = ep_few_experts_kernel<T, f8, NT>;
@@ -637,8 +698,8 @@ cudaError_t launch_experts(const FewParams& p, int num_sms, cudaStream_t s) {
   int blocks = known[dev].load(std::memory_order_acquire);
   if (blocks == 0) {
     int per_sm = 0;
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem);
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, most);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorLaunchOutOfResources;
     blocks = std::min(num_sms, kFewBlocksMax);
@@ -656,7 +717,7 @@ cudaError_t launch_sized(const FewParams& p, int num_sms, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_typed(const FewParams& p, int num_sms, cudaStream_t s) {
-  const dim3 grid(p.E + (p.f8 ? p.T : 0)), block(kGateThreads);
+  const dim3 grid(p.E + (p.f8 ? p.T : 0), (p.T + kGateTokens - 1) / kGateTokens), block(kGateThreads);
   const cudaError_t e = p.gate_dtype == EP_DTYPE_FP32   ? launch_pdl(ep_few_gate_kernel<float, T>, grid, block, 0, s, 0, p)
                         : p.gate_dtype == EP_DTYPE_FP16 ? launch_pdl(ep_few_gate_kernel<__half, T>, grid, block, 0, s, 0, p)
                                                         : launch_pdl(ep_few_gate_kernel<__nv_bfloat16, T>, grid, block, 0, s, 0, p);

@@ -27,9 +27,9 @@ struct FewParams {
   int zeros;             // ints from hdr on that the first kernel zeroes
   float* logits;         // [T][E]
   void* act;             // [routes][F], an expert's routes side by side: payload, or float32 with 8-bit weights
-  uint8_t* xq;           // 8-bit weights: [T][H]
+  __half* xq;            // 8-bit weights: [T][H], e4m3 values in fp16
   float* xs;             // [T][scale_columns(H)]
-  uint8_t* aq;           // [routes][F]
+  __half* aq;            // [routes][F], the same
   float* as;             // [routes][scale_columns(F)]
   float* part;           // [blocks][2][16][T]: sums of the outputs that several blocks share
 };
@@ -56,11 +56,11 @@ inline FewLayout few_layout(long long T, long long E, long long K, long long H, 
   l.part = at;
   at = up(at + static_cast<size_t>(kFewBlocksMax) * 2 * kFewRows * T * 4);
   l.xq = at;
-  if (f8) at = up(at + T * H);
+  if (f8) at = up(at + T * H * 2);
   l.xs = at;
   if (f8) at = up(at + T * scale_columns(static_cast<int>(H)) * 4);
   l.aq = at;
-  if (f8) at = up(at + routes * F);
+  if (f8) at = up(at + routes * F * 2);
   l.as = at;
   if (f8) at = up(at + routes * scale_columns(static_cast<int>(F)) * 4);
   l.total = at;
