@@ -13,12 +13,12 @@
 // - A piece of work is 16 weight rows (8 gate rows and their 8 up rows, or 16
 //   output rows of one expert) times the whole reduction; the pieces are dealt
 //   out in even runs.  The 16 warps of a block split the reduction in steps of
-//   128 bytes: each lane loads 16 bytes of either half of it from row lane / 4
-//   and from row lane / 4 + 8, two or three steps ahead of their use and across
-//   the ends of pieces.
+//   128 bytes; each has its steps brought by TMA, three ahead of their use and
+//   across the ends of pieces, the down products' first ones before the wait.
 // - They are the 16 x K side of mma.sync as they lie: a sum does not depend on
-//   its order, so a lane's 16 bytes may count as any of the fragment's columns,
-//   if the tokens' operand (the same 16 bytes of token lane / 4) does too.
+//   its order, so 16 bytes of a row, a lane's in one load, may count as any of
+//   the fragment's columns, if the tokens' operand (the same 16 bytes of token
+//   lane / 4) does too.
 // - Up to eight tokens of an expert, side by side, are one n-tile.  8-bit
 //   weights become fp16 (exactly) on the way to the tensor cores, the tokens'
 //   8-bit values are kept in fp16: mma.sync on e4m3 itself converts both
@@ -33,6 +33,7 @@
 
 #include "ep_moe_few.cuh"
 #include "ep_router.cuh"
+#include "ep_tc.cuh"
 
 namespace ep {
 namespace {
@@ -217,11 +218,15 @@ __device__ __forceinline__ void choose_experts(const FewParams& p, Choice& c, in
   __syncthreads();
 }
 
-// Sixteen bytes read once.
-__device__ __forceinline__ uint4 load_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// One box of weights to this block's shared memory.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, uint32_t bar, bool down, int x, int row, int e) {
+  if (down)
+    tc::tma_load_3d(dst, m, bar, x, row, e);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(x), "r"(row), "r"(0), "r"(e)
+        : "memory");
 }
 
 // d += a b: a the 16 weight rows' words, b the 8 tokens'.
@@ -285,16 +290,38 @@ struct Walk {
   }
 };
 
-// What the registers allow: steps of weights in flight, whether the tokens'
-// operand comes as far ahead or half a step at a time, just before its use, and
-// how many pieces of the gated products are joined at a time.
+// Steps of weights in flight: boxes of 16 rows x 128 bytes that a warp's first
+// lane has brought to the warp's own slots of shared memory.  (Loads by the
+// lanes themselves touch eight lines each, 64 bytes of them; two or three steps
+// of them in registers took 127 and 104 us for one token, 7168 -> 2 x 2048, in
+// 16 and in 8 bits, cp.async 157 and 130.)
+constexpr int kAhead = 3, kStepBytes = 128, kSlotBytes = kFewRows * kStepBytes;
+constexpr int kRingBytes = kWarps * kAhead * kSlotBytes;
+struct Ring {
+  uint32_t data, full;  // this warp's slots and their barriers
+  volatile int* gave_up;
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ void next() {
+    if (++slot == kAhead) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+// The place in a box of the fragment's row g: rows of neighbouring lanes differ
+// in the bit that makes the 128-byte swizzle swap a row's halves, so that a
+// warp's 16-byte loads meet all banks.
+__device__ __forceinline__ int box_row(int g) { return (g >> 1) | (g & 1) << 2; }
+
+// Whether the tokens' operand comes a step ahead or half a step at a time, just
+// before its use (registers), and the pieces of the gated products that are
+// joined at a time.
 template <bool f8, int NT>
 struct Depth {
-  static constexpr int kAhead = NT == 1 && !f8 ? 3 : 2;
   static constexpr bool kTokensAhead = NT == 1 || (NT == 2 && !f8);
   static constexpr int kBatch = 4 / NT;
 };
-
 constexpr int kRedFloats = 2 * 4 * kWarps * 16 * 8;  // two batches' sums
 
 // A block's run [lo, hi) of pieces: of each piece, warp w takes the steps w,
@@ -302,53 +329,53 @@ constexpr int kRedFloats = 2 * 4 * kWarps * 16 * 8;  // two batches' sums
 // whether it is the run's last) is called by all warps when a piece's steps
 // are over; done.wait() when the weights' first steps are on their way.
 template <typename T, bool f8, int NT, bool down, typename Done>
-__device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, int lo, int hi, int warp, int lane, Done done) {
+__device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, const CUtensorMap& map, Ring& ring, int lo, int hi, int warp,
+                                           int lane, Done done) {
   using E = typename std::conditional<f8, uint8_t, T>::type;
-  constexpr int kAhead = Depth<f8, NT>::kAhead, kTokens = Depth<f8, NT>::kTokensAhead ? kAhead : 1;
+  constexpr int kWords = f8 ? 4 : 2;  // 16-byte words of a token that meet a lane's two of a weight row
   constexpr bool ahead = Depth<f8, NT>::kTokensAhead;
-  constexpr int kStepBytes = 128, kWords = f8 ? 4 : 2;  // of a row of weights; the tokens' 16-byte words for a lane's share of it
+  constexpr int kTokens = ahead ? 2 : 1;
   const int red = (down ? p.F : p.H) * static_cast<int>(sizeof(E)), rows = down ? p.H : 2 * p.F;  // red in bytes
   const int turns = ((red + kStepBytes - 1) / kStepBytes + kWarps - 1) / kWarps;
   const int total = (hi - lo) * turns;
   const int g = lane >> 2, t = lane & 3;
   const int k0 = warp * kStepBytes + t * 16;  // this lane's first byte of a row
-  const char* w = static_cast<const char*>(down ? p.w2 : p.w13);
   const char* x = f8 ? reinterpret_cast<const char*>(down ? p.aq : p.xq) : static_cast<const char*>(down ? p.act : p.x);
   const float* xs = down ? p.as : done.token_scales();
   const int xcols = f8 ? scale_columns(red) : 0, wcols = f8 ? f8_blocks(red) : 0, wblocks = f8 ? f8_blocks(rows) : 0;
-  const long long delta = static_cast<long long>(down ? 8 : p.F) * red;  // from a piece's first eight rows to its second
-  uint4 a[kAhead][4], b[kTokens][NT][ahead ? kWords : kWords / 2];
+  const uint32_t in_box = box_row(g) * kStepBytes + ((t ^ box_row(g)) & 7) * 16;  // the lane's first word; the other half's: bit 6 the other way
+  uint4 b[kTokens][NT][ahead ? kWords : kWords / 2];
   float sw[kTokens][2], sx[kTokens][NT][2];
   // The weights' place.
   struct {
-    const char* row;
-    bool second;
-    int turn;
+    int row, e, turn;
   } at_a;
-  // The tokens': byte offsets of their rows and of their scales' rows, -1: none.
+  // The tokens': byte offsets of their rows and of their scales' rows.  Columns
+  // past the last token repeat it: nothing reads their sums.
   struct {
-    int row[NT], scale[NT][2], turn;
+    int row[NT], scale[NT][2], turn, n;
     const float *w0, *w1;
   } at_b;
   Walk<down> walk_a(p, c, lo), walk_b(p, c, lo), walk_c(p, c, lo);
   auto place_a = [&]() {
     const Piece o = walk_a.at();
-    at_a.row = w + (static_cast<long long>(o.e) * rows + o.row0 + g) * red + k0;
-    at_a.second = !down || o.row1 >= 0;
+    at_a.row = o.row0;
+    at_a.e = o.e;
     at_a.turn = 0;
   };
   auto place_b = [&]() {
     const Piece o = walk_b.at();
     at_b.turn = 0;
+    at_b.n = o.n;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int col = 8 * i + g;
-      at_b.row[i] = col < o.n ? ((down ? o.pos + col : c.token[o.pos + col]) * red + k0) * (f8 ? 2 : 1) : -1;
+      const int col = min(8 * i + g, o.n - 1);
+      at_b.row[i] = ((down ? o.pos + col : c.token[o.pos + col]) * red + k0) * (f8 ? 2 : 1);
       if constexpr (f8) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int col2 = 8 * i + 2 * t + q;
-          at_b.scale[i][q] = col2 < o.n ? (down ? o.pos + col2 : c.token[o.pos + col2]) * xcols : -1;
+          const int col2 = min(8 * i + 2 * t + q, o.n - 1);
+          at_b.scale[i][q] = (down ? o.pos + col2 : c.token[o.pos + col2]) * xcols;
         }
       }
     }
@@ -359,15 +386,11 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
       at_b.w1 = down ? at_b.w0 : s + (static_cast<long long>(o.e) * wblocks + o.row1 / kF8Block) * wcols;
     }
   };
-  auto load_a = [&](uint4 (&to)[4]) {
-    const int k = at_a.turn * (kWarps * kStepBytes);
-    const bool in0 = k + k0 < red, in1 = k + k0 + 64 < red;
-    const char* at = at_a.row + k;
-    to[0] = to[1] = to[2] = to[3] = make_uint4(0, 0, 0, 0);
-    if (in0) to[0] = load_stream(at);
-    if (in0 && at_a.second) to[1] = load_stream(at + delta);
-    if (in1) to[2] = load_stream(at + 64);
-    if (in1 && at_a.second) to[3] = load_stream(at + delta + 64);
+  // By the first lane alone; what lies past a row's or the matrix's end comes as zeros.
+  auto load_a = [&](int slot) {
+    const uint32_t bar = ring.full + 8 * slot;
+    tc::mbar_expect(bar, kSlotBytes);
+    load_box(ring.data + slot * kSlotBytes, &map, bar, down, (warp + at_a.turn * kWarps) * kStepBytes, at_a.row, at_a.e);
     if (++at_a.turn == turns) {
       walk_a.next();
       if (walk_a.u < c.num_used && walk_a.tile < walk_a.tiles) place_a();
@@ -376,17 +399,23 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
   // Words [from, from + count) of the step's tokens' operand.
   auto load_words = [&](int to, int from, int count) {
     const int k = at_b.turn * (kWarps * kStepBytes);
+    const bool whole = k + (warp + 1) * kStepBytes <= red;
     const bool in0 = k + k0 < red, in1 = k + k0 + 64 < red;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
+      if (NT > 1 && 8 * i >= at_b.n) break;
+      const uint4* row = reinterpret_cast<const uint4*>(x + at_b.row[i] + k * (f8 ? 2 : 1));
 #pragma unroll
       for (int j = 0; j < kWords; ++j) {
         if (j >= count) break;
-        const int half = (from + j) / (kWords / 2), word = 4 * half * (kWords / 2) + (from + j) % (kWords / 2);
-        b[to][i][j] = make_uint4(0, 0, 0, 0);
-        if (at_b.row[i] >= 0 && (half == 0 ? in0 : in1)) {
-          const uint4* at = reinterpret_cast<const uint4*>(x + at_b.row[i] + k * (f8 ? 2 : 1)) + word;
-          b[to][i][j] = down ? __ldcg(at) : __ldg(at);  // act is written in this kernel: not through the read-only path
+        const int half = (from + j) / (kWords / 2);
+        const uint4* at = row + 4 * half * (kWords / 2) + (from + j) % (kWords / 2);
+        // act is written in this kernel: not through the read-only path
+        if (whole) {
+          b[to][i][j] = down ? __ldcg(at) : __ldg(at);
+        } else {
+          b[to][i][j] = make_uint4(0, 0, 0, 0);
+          if (half == 0 ? in0 : in1) b[to][i][j] = down ? __ldcg(at) : __ldg(at);
         }
       }
     }
@@ -402,7 +431,7 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-          sx[to][i][q] = at_b.scale[i][q] < 0 ? 0.0f : down ? __ldcg(xs + at_b.scale[i][q] + block) : xs[at_b.scale[i][q] + block];
+          sx[to][i][q] = down ? __ldcg(xs + at_b.scale[i][q] + block) : xs[at_b.scale[i][q] + block];
     }
   };
   auto next_b = [&]() {
@@ -417,33 +446,38 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
     next_b();
   };
   if (total > 0) place_a();
-#pragma unroll
-  for (int q = 0; q < kAhead; ++q)
-    if (q < total) load_a(a[q]);
+  if (lane == 0)
+    for (int q = 0, slot = ring.slot; q < min(kAhead, total); ++q) {
+      load_a(slot);
+      slot = slot + 1 == kAhead ? 0 : slot + 1;
+    }
   done.wait();
   if (total > 0) place_b();
-  if constexpr (ahead) {
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q)
-      if (q < total) load_b(q);
-  }
+  if (ahead && total > 0) load_b(0);
   float sum[NT][4] = {};
   int turn = 0;
   int n_tokens = 0;
   if (total > 0) n_tokens = walk_c.at().n;
-  for (int n0 = 0; n0 < total; n0 += kAhead) {
+  for (int n0 = 0; n0 < total; n0 += kTokens) {
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
+    for (int q = 0; q < kTokens; ++q) {
       const int n = n0 + q;
       if (n >= total) break;
       const int from = ahead ? q : 0;
-      if (!ahead) load_scales(0);
+      if (ahead) {
+        if (n + 1 < total) load_b(q ^ 1);
+      } else {
+        load_scales(0);
+      }
+      tc::mbar_wait(ring.full + 8 * ring.slot, ring.phase, ring.gave_up);
+      const uint32_t in = ring.data + ring.slot * kSlotBytes + in_box;
       float d[NT][4] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!ahead) load_words(0, h * kWords / 2, kWords / 2);
-        const uint4 &u4 = a[q][2 * h], &v4 = a[q][2 * h + 1];
-        const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
+        uint32_t u[4], v[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(in ^ (h * 64)) : "memory");
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"((in ^ (h * 64)) + 1024) : "memory");
 #pragma unroll
         for (int j = 0; j < (f8 ? 4 : 2); ++j) {
           uint32_t u0 = u[2 * j & 3], u1 = u[(2 * j + 1) & 3], v0 = v[2 * j & 3], v1 = v[(2 * j + 1) & 3];
@@ -466,10 +500,9 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
           for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[i][j], sw[from][j >> 1] * sx[from][i][j & 1], sum[i][j]);
       }
       if (!ahead) next_b();
-      if (n + kAhead < total) {
-        load_a(a[q]);
-        if (ahead) load_b(q);
-      }
+      __syncwarp();  // read by all lanes: the slot may be written again
+      if (n + kAhead < total && lane == 0) load_a(ring.slot);
+      ring.next();
       if (++turn == turns) {
         turn = 0;
         done(walk_c.at(), sum, n + 1 == total);
@@ -501,7 +534,7 @@ struct UpDone {
   __device__ __forceinline__ void wait() const {}
   __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool end) {
     float* mine = red + (turn * kBatch + have) * kPieceFloats + warp * 16 * kCols;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = box_row(lane >> 2), t = lane & 3;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       if (8 * i >= o.n) break;
@@ -585,7 +618,7 @@ struct DownDone {
   __device__ __forceinline__ int start_of(long long block) const { return static_cast<int>(block * pieces / blocks); }
   __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool end) {
     float* mine = red + warp * 16 * p.T;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = box_row(lane >> 2), t = lane & 3;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       if (8 * i >= o.n) break;
@@ -661,11 +694,24 @@ struct Run {
 };
 
 template <typename T, bool f8, int NT>
-__global__ void __launch_bounds__(kThreads, 1) ep_few_experts_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    ep_few_experts_kernel(const __grid_constant__ CUtensorMap map13, const __grid_constant__ CUtensorMap map2, const FewParams p) {
   __shared__ Choice c;
-  extern __shared__ float red[];
+  __shared__ uint64_t full[kWarps * kAhead];
+  __shared__ int gave_up;
+  extern __shared__ unsigned char raw[];
+  unsigned char* memory = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
+  float* red = reinterpret_cast<float*>(memory + kRingBytes);
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch_desc(&map13);
+    tc::tma_prefetch_desc(&map2);
+    for (int i = 0; i < kWarps * kAhead; ++i) tc::mbar_init(tc::smem_addr(&full[i]), 1);
+    tc::mbar_init_fence();
+    gave_up = 0;
+  }
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Ring ring{tc::smem_addr(memory) + warp * (kAhead * kSlotBytes), tc::smem_addr(&full[warp * kAhead]), &gave_up, 0, 0};
   float* scales = red + kRedFloats;
   if constexpr (f8)
     for (int i = threadIdx.x; i < p.T * scale_columns(p.H); i += kThreads) scales[i] = p.xs[i];
@@ -677,19 +723,44 @@ __global__ void __launch_bounds__(kThreads, 1) ep_few_experts_kernel(const FewPa
   }
   {
     const Run run(static_cast<long long>(c.num_used) * (p.F / 8));
-    run_pieces<T, f8, NT, false>(p, c, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, run.lo, 0, 0, scales});
+    run_pieces<T, f8, NT, false>(p, c, map13, ring, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, run.lo, 0, 0, scales});
   }
   {
     const Run run(static_cast<long long>(c.num_used) * ((p.H + kFewRows - 1) / kFewRows));
-    run_pieces<T, f8, NT, true>(p, c, run.lo, run.hi, warp, lane, DownDone<T, NT>{p, c, red, warp, lane, run.lo, run.pieces, run.blocks});
+    run_pieces<T, f8, NT, true>(p, c, map2, ring, run.lo, run.hi, warp, lane, DownDone<T, NT>{p, c, red, warp, lane, run.lo, run.pieces, run.blocks});
   }
+  __syncthreads();
+  if (threadIdx.x == 0 && gave_up) {
+    *p.hdr = static_cast<int>(EP_ST_TIMEOUT);
+    // Copies in flight land before the block's shared memory goes; one takes microseconds.
+    const unsigned long long start = tc::now_ns();
+    while (tc::now_ns() - start < tc::kWaitNs / 100) {
+    }
+  }
+}
+
+// A map of [dim 3]..[dim 1][dim 0] bytes, strides of the dimensions from 1 on.
+bool byte_map(CUtensorMap* m, const void* base, int dims, const long long (&size)[4], const long long (&stride)[3], const int (&box)[4]) {
+  const tc::EncodeFn f = tc::tensor_map_encoder();
+  if (f == nullptr) return false;
+  cuuint64_t sz[4], st[3];
+  cuuint32_t bx[4];
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < dims; ++i) {
+    sz[i] = static_cast<cuuint64_t>(size[i]);
+    bx[i] = static_cast<cuuint32_t>(box[i]);
+    if (i + 1 < dims) st[i] = static_cast<cuuint64_t>(stride[i]);
+  }
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(dims), const_cast<void*>(base), sz, st, bx, one,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The second kernel's blocks: one per SM that can hold one, all at once.
 template <typename T, bool f8, int NT>
 cudaError_t launch_experts(const FewParams& p, int num_sms, cudaStream_t s) {
-  constexpr size_t most = sizeof(float) * (kRedFloats + (f8 ? 8 * NT * (EP_MAX_NORM_HIDDEN / kF8Block) : 0));
-  const size_t smem = sizeof(float) * (kRedFloats + (f8 ? p.T * scale_columns(p.H) : 0));
+  constexpr size_t most = 1024 + kRingBytes + sizeof(float) * (kRedFloats + (f8 ? 8 * NT * (EP_MAX_NORM_HIDDEN / kF8Block) : 0));
+  const size_t smem = 1024 + kRingBytes + sizeof(float) * (kRedFloats + (f8 ? p.T * scale_columns(p.H) : 0));
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices];
   const auto kern = ep_few_experts_kernel<T, f8, NT>;
@@ -705,7 +776,12 @@ cudaError_t launch_experts(const FewParams& p, int num_sms, cudaStream_t s) {
     blocks = std::min(num_sms, kFewBlocksMax);
     known[dev].store(blocks, std::memory_order_release);
   }
-  return launch_pdl_ex(kern, dim3(blocks), dim3(kThreads), smem, s, 0, true, p);
+  const long long es = f8 ? 1 : 2, h = p.H * es, f = p.F * es;  // rows in bytes
+  CUtensorMap map13, map2;
+  if (!byte_map(&map13, p.w13, 4, {h, p.F, 2, p.E}, {h, h * p.F, h * 2 * p.F}, {kStepBytes, 8, 2, 1}) ||
+      !byte_map(&map2, p.w2, 3, {f, p.H, p.E, 1}, {f, f * p.H, 0}, {kStepBytes, kFewRows, 1, 1}))
+    return cudaErrorInvalidValue;
+  return launch_pdl_ex(kern, dim3(blocks), dim3(kThreads), smem, s, 0, true, map13, map2, p);
 }
 
 template <typename T, bool f8>
