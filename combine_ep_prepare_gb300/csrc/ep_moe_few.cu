@@ -453,19 +453,26 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
     }
   done.wait();
   if (total > 0) place_b();
-  if (ahead && total > 0) load_b(0);
-  float sum[NT][4] = {};
-  int turn = 0;
-  int n_tokens = 0;
-  if (total > 0) n_tokens = walk_c.at().n;
-  for (int n0 = 0; n0 < total; n0 += kTokens) {
+  if (ahead && total > 0) load_b(kTokens - 1);
+  int n = 0;
+  for (int i0 = lo; i0 < hi; ++i0) {
+    const Piece o = walk_c.at();
+    float sum[NT][4] = {};
+    // One copy of a step and of a piece's end: two of each, for two buffers of
+    // the tokens' words, missed the instruction cache.
+#pragma unroll 1
+    for (int turn = 0; turn < turns; ++turn, ++n) {
+      if constexpr (ahead) {
 #pragma unroll
-    for (int q = 0; q < kTokens; ++q) {
-      const int n = n0 + q;
-      if (n >= total) break;
-      const int from = ahead ? q : 0;
-      if (ahead) {
-        if (n + 1 < total) load_b(q ^ 1);
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) b[0][i][j] = b[1][i][j];
+          sx[0][i][0] = sx[1][i][0];
+          sx[0][i][1] = sx[1][i][1];
+        }
+        sw[0][0] = sw[1][0];
+        sw[0][1] = sw[1][1];
+        if (n + 1 < total) load_b(1);
       } else {
         load_scales(0);
       }
@@ -487,39 +494,31 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
           }
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            if (NT > 1 && 8 * i >= n_tokens) break;
-            const uint4& y = b[from][i][(ahead ? h * kWords / 2 : 0) + j / 2];
+            if (NT > 1 && 8 * i >= o.n) break;
+            const uint4& y = b[0][i][(ahead ? h * kWords / 2 : 0) + j / 2];
             mma<typename std::conditional<f8, __half, T>::type>(f8 ? d[i] : sum[i], u0, v0, u1, v1, j & 1 ? y.z : y.x, j & 1 ? y.w : y.y);
           }
         }
       }
+      __syncwarp();  // read by all lanes: the slot may be written again
+      if (n + kAhead < total && lane == 0) load_a(ring.slot);
+      ring.next();
       if constexpr (f8) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[i][j], sw[from][j >> 1] * sx[from][i][j & 1], sum[i][j]);
+          for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[i][j], sw[0][j >> 1] * sx[0][i][j & 1], sum[i][j]);
       }
       if (!ahead) next_b();
-      __syncwarp();  // read by all lanes: the slot may be written again
-      if (n + kAhead < total && lane == 0) load_a(ring.slot);
-      ring.next();
-      if (++turn == turns) {
-        turn = 0;
-        done(walk_c.at(), sum, n + 1 == total);
-        walk_c.next();
-        if (n + 1 < total) n_tokens = walk_c.at().n;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum[i][j] = 0.0f;
-      }
     }
+    done(o, sum, i0 + 1 == hi);
+    walk_c.next();
   }
 }
 
 // After a piece of the gated products its warps' sums go to shared memory;
-// after kBatch of them they are joined, the activation is taken and written,
-// and with 8-bit weights the last piece of 128 features quantises those.
+// after kBatch of them they are joined and the activation is taken and written;
+// with 8-bit weights it is quantised at the end of the run.
 template <typename T, bool f8, int NT>
 struct UpDone {
   static constexpr int kCols = 8 * NT, kBatch = Depth<f8, NT>::kBatch;
@@ -528,7 +527,7 @@ struct UpDone {
   const FewParams& p;
   Choice& c;
   float* red;  // [2][kBatch][kWarps][16][kCols]
-  int warp, lane, first, have, turn;  // first: the batch's first piece
+  int warp, lane, lo, first, have, turn;  // the run's and the batch's first piece
   const float* scales;  // 8-bit weights: the tokens', in shared memory
   __device__ __forceinline__ const float* token_scales() const { return scales; }
   __device__ __forceinline__ void wait() const {}
@@ -560,22 +559,31 @@ struct UpDone {
         else static_cast<T*>(p.act)[i] = from_f32<T>(a);
       }
     }
-    if constexpr (f8) {
-      __threadfence();
-      if (threadIdx.x == 0) c.last = 0;
-      __syncthreads();
-      if (threadIdx.x < have) {
-        const Piece q = Walk<false>(p, c, first + threadIdx.x).at();
-        const int block = q.tile / (kF8Block / 8);
-        if (atomicAdd(p.written + q.u * f8_blocks(p.F) + block, 1) == kF8Block / 8 - 1) atomicOr(&c.last, 1 << threadIdx.x);
-        __threadfence();
-      }
-      __syncthreads();
-      for (int left = c.last; left; left &= left - 1) quantize(Walk<false>(p, c, first + __ffs(left) - 1).at());
-    }
     turn ^= 1;  // the other buffer next: the sums here are still being read
     first += have;
     have = 0;
+    if constexpr (f8)
+      if (end) quantize_run();
+  }
+  // The run's features to 8 bits, a block of 128 (16 pieces) at a time.  The
+  // first and the last may be other blocks' too: who brings the last piece
+  // quantises them.
+  __device__ __forceinline__ void quantize_run() const {
+    constexpr int kPieces = kF8Block / 8;
+    const int hi = first, b0 = lo / kPieces, b1 = (hi - 1) / kPieces;
+    __threadfence();
+    if (threadIdx.x == 0) c.last = 0;
+    __syncthreads();
+    if (threadIdx.x < 2 && (threadIdx.x == 0 || b1 != b0)) {
+      const int b = threadIdx.x == 0 ? b0 : b1;
+      const int mine = min(hi, (b + 1) * kPieces) - max(lo, b * kPieces);
+      if (mine == kPieces || atomicAdd(p.written + b, mine) + mine == kPieces) atomicOr(&c.last, 1 << threadIdx.x);
+      __threadfence();
+    }
+    __syncthreads();
+    for (int b = b0; b <= b1; ++b) {
+      if (b == b0 ? c.last & 1 : b < b1 || (c.last & 2)) quantize(Walk<false>(p, c, b * kPieces).at());
+    }
   }
   __device__ __forceinline__ void quantize(const Piece& o) const {
     const int block = o.tile / (kF8Block / 8);
@@ -723,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   {
     const Run run(static_cast<long long>(c.num_used) * (p.F / 8));
-    run_pieces<T, f8, NT, false>(p, c, map13, ring, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, run.lo, 0, 0, scales});
+    run_pieces<T, f8, NT, false>(p, c, map13, ring, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, run.lo, run.lo, 0, 0, scales});
   }
   {
     const Run run(static_cast<long long>(c.num_used) * ((p.H + kFewRows - 1) / kFewRows));

@@ -23,7 +23,7 @@ struct FewParams {
   // workspace
   int* hdr;              // [0] status, [1] arrivals of the second kernel's blocks
   int* done;             // [tiles of 16 outputs] blocks that have added their part
-  int* written;          // 8-bit weights: [used expert][blocks of F] pieces of act there
+  int* written;          // 8-bit weights: [used expert][blocks of F] pieces of act there, where blocks share them
   int zeros;             // ints from hdr on that the first kernel zeroes
   float* logits;         // [T][E]
   void* act;             // [routes][F], an expert's routes side by side: payload, or float32 with 8-bit weights
