@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["ep_api.cu", "ep_route.cu", "ep_rows.cu", "ep_experts_api.cu", "ep_products.cu", "ep_products_tc.cu", "ep_w4.cu",
-           "ep_router.cu", "ep_norm.cu", "ep_products_f8.cu", "ep_moe_few.cu", "ep_f8_api.cu"]
+           "ep_router.cu", "ep_norm.cu", "ep_products_f8.cu", "ep_moe_few.cu", "ep_dispatch_f8.cu", "ep_f8_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "-I", os.path.join(ROOT, "include")]

@@ -641,23 +641,14 @@ ep_status_t ep_dispatch_f8(ep_handle_t h, const int64_t* topk_idx, int64_t T, co
   if ((st = check_f32(recv_topk_weights, "recv_topk_weights", true)) != EP_OK) return st;
   int sms = 0;
   if ((st = check_device(&sms)) != EP_OK) return st;
-  // Rows are moved as bytes: the 8-bit ones with the weights, then the scales.
   ep::RowParams p = row_params(L, h, T);
   p.rowbytes = static_cast<int>(L->cfg.hidden);
   p.src = tokens;
   p.dst = recv_tokens;
   p.w_in = topk_weights;
   p.w_out = recv_topk_weights;
-  cudaError_t e = ep::launch_scatter(p, true, static_cast<int>(L->lay.pad_cap), sms, static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) {
-    p.rowbytes = static_cast<int>((L->cfg.hidden + 511) / 512 * 16);
-    p.src = scales;
-    p.dst = recv_scales;
-    p.w_in = nullptr;
-    p.w_out = nullptr;
-    e = ep::launch_scatter(p, false, static_cast<int>(L->lay.pad_cap), sms, static_cast<cudaStream_t>(stream));
-  }
-  g_launches.fetch_add(2, std::memory_order_relaxed);
+  cudaError_t e = ep::launch_dispatch_f8(p, scales, recv_scales, static_cast<int>(L->lay.pad_cap), sms, static_cast<cudaStream_t>(stream));
+  g_launches.fetch_add(1, std::memory_order_relaxed);
   if (e != cudaSuccess) return cuda_fail(e, "ep_dispatch_f8 launch");
   return EP_OK;
 }

@@ -303,6 +303,9 @@ cudaError_t launch_scatter(const RowParams& p, bool weights, int npad_max, int n
 // The same for a sharded layer: rows go to their owner's buffer through
 // p.dst_tab (and weights through p.wout_tab); padding rows of this rank's own
 // buffer are zeroed.
+// 8-bit rows (p.rowbytes of them) with their scales.
+cudaError_t launch_dispatch_f8(const RowParams& p, const float* scales, float* recv_scales, int npad_max,
+                               int num_sms, cudaStream_t s);
 cudaError_t launch_scatter_sharded(const RowParams& p, bool weights, int npad_max, int num_sms,
                                    cudaStream_t s);
 // combine / dispatch_bwd of a sharded layer: rows read from their owner's

@@ -102,7 +102,27 @@ __global__ void __launch_bounds__(1024) ep_norm_kernel(const NormParams p) {
       p.scales[static_cast<long long>(blockIdx.x) * scale_columns(p.H) + b] = 0.0f;
 }
 
-// Blocks stride over the rows; a thread keeps its columns' share of dw.
+// A row's gradients and h, a thread's vectors of them.
+template <typename T, int NV>
+struct GradRow {
+  Raw8<T> dy[NV], h[NV], ds[NV];
+  __device__ __forceinline__ void load(const NormParams& p, int t) {
+    const long long row = static_cast<long long>(t) * p.H;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (t < p.T && v < p.H / 8) {
+        dy[i].load_rw(static_cast<const T*>(p.dy) + row + 8 * v);
+        h[i].load_rw(static_cast<const T*>(p.x) + row + 8 * v);
+        if (p.dsum != nullptr) ds[i].load_rw(static_cast<const T*>(p.dsum) + row + 8 * v);
+      }
+    }
+  }
+};
+
+// Blocks stride over the rows; a thread keeps its columns' share of dw.  The
+// next row is loaded before the sums over this one are joined: without that a
+// block waits for memory between its rows (8,192 x 7168 bf16: 119 us).
 template <typename T, int NV>
 __global__ void __launch_bounds__(1024) ep_norm_bwd_kernel(const NormParams p) {
   __shared__ float part[2][64];
@@ -114,19 +134,13 @@ __global__ void __launch_bounds__(1024) ep_norm_bwd_kernel(const NormParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   int turn = 0;
+  GradRow<T, NV> next;
+  next.load(p, blockIdx.x);
   for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
     const long long row = static_cast<long long>(t) * p.H;
-    Raw8<T> dy[NV], h[NV], ds[NV];
+    const GradRow<T, NV> at = next;
+    next.load(p, t + static_cast<int>(gridDim.x));
     float ss = 0.0f, inner = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < vectors) {
-        dy[i].load_rw(static_cast<const T*>(p.dy) + row + 8 * v);
-        h[i].load_rw(static_cast<const T*>(p.x) + row + 8 * v);
-        if (p.dsum != nullptr) ds[i].load_rw(static_cast<const T*>(p.dsum) + row + 8 * v);
-      }
-    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -135,8 +149,8 @@ __global__ void __launch_bounds__(1024) ep_norm_bwd_kernel(const NormParams p) {
         float a[8], b[8], w[8];
         wr.load(static_cast<const T*>(p.weight) + 8 * v);
         wr.get(w);
-        dy[i].get(a);
-        h[i].get(b);
+        at.dy[i].get(a);
+        at.h[i].get(b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           ss = fmaf(b[j], b[j], ss);
@@ -155,10 +169,10 @@ __global__ void __launch_bounds__(1024) ep_norm_bwd_kernel(const NormParams p) {
         float a[8], b[8], w[8], s[8];
         wr.load(static_cast<const T*>(p.weight) + 8 * v);
         wr.get(w);
-        dy[i].get(a);
-        h[i].get(b);
+        at.dy[i].get(a);
+        at.h[i].get(b);
         if (p.dsum != nullptr) {
-          ds[i].get(s);
+          at.ds[i].get(s);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) s[j] = 0.0f;
@@ -186,8 +200,10 @@ __global__ void __launch_bounds__(32 * kSumRows) ep_norm_dw_kernel(const NormPar
   pdl_wait();
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
   float s = 0.0f;
-  if (col < p.H)
+  if (col < p.H) {
+#pragma unroll 8
     for (int i = g; i < parts; i += kSumRows) s += p.partial[static_cast<long long>(i) * p.H + col];
+  }
   part[g][threadIdx.x & 31] = s;
   __syncthreads();
   if (g == 0 && col < p.H) {
@@ -217,9 +233,9 @@ cudaError_t norm_typed(const NormParams& p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t norm_bwd_typed(const NormParams& p, int parts, cudaStream_t s) {
-  int threads, nv;
-  shape(p.H, &threads, &nv);
-  const dim3 grid(parts), block(threads);
+  // One vector a thread as far as a block goes: the registers hold two rows.
+  const int vectors = p.H / 8, nv = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 4;
+  const dim3 grid(parts), block(std::min(1024, ((vectors + nv - 1) / nv + 31) / 32 * 32));
   if (nv == 1) return launch_pdl(ep_norm_bwd_kernel<T, 1>, grid, block, 0, s, 0, p);
   if (nv == 2) return launch_pdl(ep_norm_bwd_kernel<T, 2>, grid, block, 0, s, 0, p);
   return launch_pdl(ep_norm_bwd_kernel<T, 4>, grid, block, 0, s, 0, p);
@@ -293,7 +309,10 @@ cudaError_t quantize_typed(const QuantParams& p, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-int norm_bwd_parts(long long T, long long) { return static_cast<int>(std::min<long long>(T, 304)); }
+// One or two blocks for each of 152 SMs (rows over 4096 elements: a block of 513
+// to 1024 threads), whatever the device has, so that the order of dw's sum does
+// not depend on it.
+int norm_bwd_parts(long long T, long long H) { return static_cast<int>(std::min<long long>(T, H > 4096 ? 152 : 304)); }
 
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   if (p.dtype == EP_DTYPE_FP32) return norm_typed<float>(p, s);

@@ -376,56 +376,62 @@ struct Epilogue {
     }
   }
 
+  // Sixteen rows at a time go through shared memory, unrounded; the gate and up
+  // values of the next sixteen are loaded meanwhile.
   __device__ __forceinline__ void through_activation(const Tile& t, const Sums& a, int nh) const {
     const int f = t.f0 + rank * kHalfM + 4 * lane;
     const long long cols = 2LL * p.K;
     float2* put = reinterpret_cast<float2*>(stage) + (lane & 3) * kPairStride32 + w * 32 + (lane >> 2);
     const int stop = f < p.K ? min(t.cnt - t.r0, (half + 1) * nh) : 0;
+    const long long at0 = (static_cast<long long>(t.off) + t.r0 + half * nh + 4 * w) * cols + f;
+    const T* pre = static_cast<const T*>(p.pre_in) + at0;
+    T* out = static_cast<T*>(p.out) + at0;
+    uint2 g[2][4], u[2][4];
+    auto load = [&](int s, uint2 (&gs)[4], uint2 (&us)[4]) {
+      const int c0 = half * nh + 16 * s + 4 * w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (32 * i >= nh) break;
-#pragma unroll
-      for (int j2 = 0; j2 < 2; ++j2) {  // 16 rows at a time
-        const int c0 = half * nh + 32 * i + 16 * j2;
-        uint2 g[4], u[4];
-        const T* pre = static_cast<const T*>(p.pre_in) + (static_cast<long long>(t.off) + t.r0 + c0 + 4 * w) * cols + f;
-        T* out = static_cast<T*>(p.out) + (static_cast<long long>(t.off) + t.r0 + c0 + 4 * w) * cols + f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (c0 + 4 * w + r < stop) {
-            g[r] = __ldg(reinterpret_cast<const uint2*>(pre + r * cols));
-            u[r] = __ldg(reinterpret_cast<const uint2*>(pre + r * cols + p.K));
-          }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) put[j / 2 * 4 * kPairStride32 + h * 16 + (j & 1) * 8] = a.v[i][h][4 * j2 + j];
-        half_sync(half);
-        float x[4][4];
-#pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-          const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float2*>(stage) + (2 * w + r / 2) * kPairStride32 + 4 * lane);
-          const float4 lo = q[0], hi = q[1];
-          x[r][0] = lo.x; x[r + 1][0] = lo.y; x[r][1] = lo.z; x[r + 1][1] = lo.w;
-          x[r][2] = hi.x; x[r + 1][2] = hi.y; x[r][3] = hi.z; x[r + 1][3] = hi.w;
+      for (int r = 0; r < 4; ++r)
+        if (c0 + r < stop) {
+          gs[r] = __ldg(reinterpret_cast<const uint2*>(pre + (16 * s + r) * cols));
+          us[r] = __ldg(reinterpret_cast<const uint2*>(pre + (16 * s + r) * cols + p.K));
         }
-        half_sync(half);
+    };
+    load(0, g[0], u[0]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (c0 + 4 * w + r < stop) {
-            const float4 gv = unpack4<T>(g[r]), uv = unpack4<T>(u[r]);
-            const float gs[4] = {gv.x, gv.y, gv.z, gv.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
-            float dg[4], du[4];
+    for (int s = 0; s < 8; ++s) {
+      if (16 * s >= nh) break;
+      const int c0 = half * nh + 16 * s + 4 * w;
+      if (16 * (s + 1) < nh) load(s + 1, g[(s + 1) & 1], u[(s + 1) & 1]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float sg = fast_sigmoid(gs[k]);
-              dg[k] = x[r][k] * us[k] * sg * (1.0f + gs[k] * (1.0f - sg));
-              du[k] = x[r][k] * gs[k] * sg;
-            }
-            store4(out + r * cols, make_float4(dg[0], dg[1], dg[2], dg[3]));
-            store4(out + r * cols + p.K, make_float4(du[0], du[1], du[2], du[3]));
-          }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put[j / 2 * 4 * kPairStride32 + h * 16 + (j & 1) * 8] = a.v[s / 2][h][4 * (s & 1) + j];
+      half_sync(half);
+      float x[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; r += 2) {
+        const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float2*>(stage) + (2 * w + r / 2) * kPairStride32 + 4 * lane);
+        const float4 lo = q[0], hi = q[1];
+        x[r][0] = lo.x; x[r + 1][0] = lo.y; x[r][1] = lo.z; x[r + 1][1] = lo.w;
+        x[r][2] = hi.x; x[r + 1][2] = hi.y; x[r][3] = hi.z; x[r + 1][3] = hi.w;
       }
+      half_sync(half);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (c0 + r < stop) {
+          const float4 gv = unpack4<T>(g[s & 1][r]), uv = unpack4<T>(u[s & 1][r]);
+          const float gs[4] = {gv.x, gv.y, gv.z, gv.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
+          float dg[4], du[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float sg = fast_sigmoid(gs[k]);
+            dg[k] = x[r][k] * us[k] * sg * (1.0f + gs[k] * (1.0f - sg));
+            du[k] = x[r][k] * gs[k] * sg;
+          }
+          T* o = out + (16 * s + r) * cols;
+          store4(o, make_float4(dg[0], dg[1], dg[2], dg[3]));
+          store4(o + p.K, make_float4(du[0], du[1], du[2], du[3]));
+        }
     }
   }
 
