@@ -261,15 +261,11 @@ struct Walk {
     u = down ? i % max(1, c.num_used) : i / tiles;
     tile = down ? i / max(1, c.num_used) : i % tiles;
   }
-  __device__ __forceinline__ void next() {
+  __device__ __forceinline__ void advance(int by) {
     if (down) {
-      if (++u == c.num_used) {
-        u = 0;
-        ++tile;
-      }
-    } else if (++tile == tiles) {
-      tile = 0;
-      ++u;
+      for (u += by; u >= c.num_used; u -= c.num_used) ++tile;
+    } else {
+      for (tile += by; tile >= tiles; tile -= tiles) ++u;
     }
   }
   __device__ __forceinline__ Piece at() const {
@@ -309,6 +305,11 @@ struct Ring {
     }
   }
 };
+__device__ __forceinline__ float load_shared(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
 // The place in a box of the fragment's row g: rows of neighbouring lanes differ
 // in the bit that makes the 128-byte swizzle swap a row's halves, so that a
 // warp's 16-byte loads meet all banks.
@@ -324,24 +325,44 @@ struct Depth {
 };
 constexpr int kRedFloats = 2 * 4 * kWarps * 16 * 8;  // two batches' sums
 
-// A block's run [lo, hi) of pieces: of each piece, warp w takes the steps w,
-// w + 16, ... of the reduction (128 bytes of a row each).  done(piece, sums,
-// whether it is the run's last) is called by all warps when a piece's steps
-// are over; done.wait() when the weights' first steps are on their way.
+// How a block's warps share its run: groups of them take a piece each in turn,
+// and split its reduction among them.
+struct Team {
+  int groups, group, split, sub;  // groups, this warp's; warps of a group, this one's place
+  __device__ __forceinline__ Team(int pieces, int steps, int warp) {
+    // A piece costs a warp as much as a step or two beside its steps, so groups
+    // with more steps of fewer pieces are faster (7168 -> 2 x 2048 in 8 bits: 16
+    // tokens of 64 experts 717 us with one group, 672 with this rule; 32 tokens
+    // 1,331 and 1,010; 32 experts in 16 bits 720 and 621).  With few pieces the
+    // groups would not come out even (one token in 16 bits: 125 us with one,
+    // 128 where the rule asks for half as many pieces).
+    groups = 1;
+    while (groups < 4 && pieces >= 16 * groups && (steps * groups + kWarps - 1) / kWarps < 8) groups *= 2;
+    split = kWarps / groups;
+    group = warp / split;
+    sub = warp % split;
+  }
+};
+
+// A block's run [lo, hi) of pieces: of each of its group's pieces, warp w of
+// the group takes the steps w, w + split, ... of the reduction (128 bytes of a
+// row each).  put(piece, its place in the segment, sums) is called when a
+// piece's steps are over, join(segment) by all warps when a segment's pieces
+// are; wait() when the weights' first steps are on their way.
 template <typename T, bool f8, int NT, bool down, typename Done>
-__device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, const CUtensorMap& map, Ring& ring, int lo, int hi, int warp,
+__device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, const CUtensorMap& map, Ring& ring, int lo, int hi, const Team& team,
                                            int lane, Done done) {
   using E = typename std::conditional<f8, uint8_t, T>::type;
   constexpr int kWords = f8 ? 4 : 2;  // 16-byte words of a token that meet a lane's two of a weight row
   constexpr bool ahead = Depth<f8, NT>::kTokensAhead;
   constexpr int kTokens = ahead ? 2 : 1;
   const int red = (down ? p.F : p.H) * static_cast<int>(sizeof(E)), rows = down ? p.H : 2 * p.F;  // red in bytes
-  const int turns = ((red + kStepBytes - 1) / kStepBytes + kWarps - 1) / kWarps;
-  const int total = (hi - lo) * turns;
+  const int turns = ((red + kStepBytes - 1) / kStepBytes + team.split - 1) / team.split, stride = team.split * kStepBytes;
+  const int own = max(0, (hi - lo - team.group + team.groups - 1) / team.groups), total = own * turns;
   const int g = lane >> 2, t = lane & 3;
-  const int k0 = warp * kStepBytes + t * 16;  // this lane's first byte of a row
+  const int k0 = team.sub * kStepBytes + t * 16;  // this lane's first byte of a row
   const char* x = f8 ? reinterpret_cast<const char*>(down ? p.aq : p.xq) : static_cast<const char*>(down ? p.act : p.x);
-  const float* xs = down ? p.as : done.token_scales();
+  const uint32_t scales = done.token_scales();
   const int xcols = f8 ? scale_columns(red) : 0, wcols = f8 ? f8_blocks(red) : 0, wblocks = f8 ? f8_blocks(rows) : 0;
   const uint32_t in_box = box_row(g) * kStepBytes + ((t ^ box_row(g)) & 7) * 16;  // the lane's first word; the other half's: bit 6 the other way
   uint4 b[kTokens][NT][ahead ? kWords : kWords / 2];
@@ -356,7 +377,7 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
     int row[NT], scale[NT][2], turn, n;
     const float *w0, *w1;
   } at_b;
-  Walk<down> walk_a(p, c, lo), walk_b(p, c, lo), walk_c(p, c, lo);
+  Walk<down> walk_a(p, c, lo + team.group), walk_b(walk_a), walk_c(walk_a);
   auto place_a = [&]() {
     const Piece o = walk_a.at();
     at_a.row = o.row0;
@@ -390,32 +411,36 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
   auto load_a = [&](int slot) {
     const uint32_t bar = ring.full + 8 * slot;
     tc::mbar_expect(bar, kSlotBytes);
-    load_box(ring.data + slot * kSlotBytes, &map, bar, down, (warp + at_a.turn * kWarps) * kStepBytes, at_a.row, at_a.e);
+    load_box(ring.data + slot * kSlotBytes, &map, bar, down, team.sub * kStepBytes + at_a.turn * stride, at_a.row, at_a.e);
     if (++at_a.turn == turns) {
-      walk_a.next();
+      walk_a.advance(team.groups);
       if (walk_a.u < c.num_used && walk_a.tile < walk_a.tiles) place_a();
     }
   };
   // Words [from, from + count) of the step's tokens' operand.
   auto load_words = [&](int to, int from, int count) {
-    const int k = at_b.turn * (kWarps * kStepBytes);
-    const bool whole = k + (warp + 1) * kStepBytes <= red;
-    const bool in0 = k + k0 < red, in1 = k + k0 + 64 < red;
+    const int k = at_b.turn * stride;
+    // Word j of what is asked for, in 16-byte words from the lane's first on.
+    auto word = [&](int j) { return 4 * ((from + j) / (kWords / 2)) * (kWords / 2) + (from + j) % (kWords / 2); };
+    if (k + (team.sub + 1) * kStepBytes <= red) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      if (NT > 1 && 8 * i >= at_b.n) break;
-      const uint4* row = reinterpret_cast<const uint4*>(x + at_b.row[i] + k * (f8 ? 2 : 1));
+      for (int i = 0; i < NT; ++i) {
+        if (NT > 1 && 8 * i >= at_b.n) break;
+        const uint4* row = reinterpret_cast<const uint4*>(x + at_b.row[i] + k * (f8 ? 2 : 1));
 #pragma unroll
-      for (int j = 0; j < kWords; ++j) {
-        if (j >= count) break;
-        const int half = (from + j) / (kWords / 2);
-        const uint4* at = row + 4 * half * (kWords / 2) + (from + j) % (kWords / 2);
-        // act is written in this kernel: not through the read-only path
-        if (whole) {
-          b[to][i][j] = down ? __ldcg(at) : __ldg(at);
-        } else {
+        for (int j = 0; j < kWords; ++j)  // act is written in this kernel: not through the read-only path
+          if (j < count) b[to][i][j] = down ? __ldcg(row + word(j)) : __ldg(row + word(j));
+      }
+    } else {  // the row's end: zeros past it
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if (NT > 1 && 8 * i >= at_b.n) break;
+        const uint4* row = reinterpret_cast<const uint4*>(x + at_b.row[i] + k * (f8 ? 2 : 1));
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          if (j >= count) break;
           b[to][i][j] = make_uint4(0, 0, 0, 0);
-          if (half == 0 ? in0 : in1) b[to][i][j] = down ? __ldcg(at) : __ldg(at);
+          if (k + k0 + 64 * ((from + j) / (kWords / 2)) < red) b[to][i][j] = down ? __ldcg(row + word(j)) : __ldg(row + word(j));
         }
       }
     }
@@ -424,19 +449,19 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
   auto load_scales = [&](int to) {
     if constexpr (f8) {
       // One block of 128 a step.  A step past the end has zeros, times the last block's scale.
-      const int block = min(warp + at_b.turn * kWarps, wcols - 1);
+      const int block = min(team.sub + at_b.turn * team.split, wcols - 1);
       sw[to][0] = __ldg(at_b.w0 + block);
       sw[to][1] = down ? sw[to][0] : __ldg(at_b.w1 + block);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-          sx[to][i][q] = down ? __ldcg(xs + at_b.scale[i][q] + block) : xs[at_b.scale[i][q] + block];
+          sx[to][i][q] = down ? __ldcg(p.as + at_b.scale[i][q] + block) : load_shared(scales + 4 * (at_b.scale[i][q] + block));
     }
   };
   auto next_b = [&]() {
     if (++at_b.turn == turns) {
-      walk_b.next();
+      walk_b.advance(team.groups);
       if (walk_b.u < c.num_used && walk_b.tile < walk_b.tiles) place_b();
     }
   };
@@ -453,86 +478,91 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
     }
   done.wait();
   if (total > 0) place_b();
-  if (ahead && total > 0) load_b(kTokens - 1);
-  int n = 0;
-  for (int i0 = lo; i0 < hi; ++i0) {
-    const Piece o = walk_c.at();
-    float sum[NT][4] = {};
-    // One copy of a step and of a piece's end: two of each, for two buffers of
-    // the tokens' words, missed the instruction cache.
-#pragma unroll 1
-    for (int turn = 0; turn < turns; ++turn, ++n) {
-      if constexpr (ahead) {
+  if (ahead && total > 0) load_b(0);
+  float sum[NT][4];
+  int n = 0, n_tokens = 0;
+  // One step with the tokens' words in b[from], the next step's going to b[to].
+  auto step = [&](int from, int to) {
+    if (!ahead) load_scales(0);
+    else if (n + 1 < total) load_b(to);
+    tc::mbar_wait(ring.full + 8 * ring.slot, ring.phase, ring.gave_up);
+    const uint32_t in = ring.data + ring.slot * kSlotBytes + in_box;
+    float d[NT][4] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!ahead) load_words(0, h * kWords / 2, kWords / 2);
+      uint32_t u[4], v[4];
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(in ^ (h * 64)) : "memory");
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"((in ^ (h * 64)) + 1024) : "memory");
+#pragma unroll
+      for (int j = 0; j < (f8 ? 4 : 2); ++j) {
+        uint32_t u0 = u[2 * j & 3], u1 = u[(2 * j + 1) & 3], v0 = v[2 * j & 3], v1 = v[(2 * j + 1) & 3];
+        if constexpr (f8) {
+          fp16_of(u[j], &u0, &u1);
+          fp16_of(v[j], &v0, &v1);
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-#pragma unroll
-          for (int j = 0; j < kWords; ++j) b[0][i][j] = b[1][i][j];
-          sx[0][i][0] = sx[1][i][0];
-          sx[0][i][1] = sx[1][i][1];
-        }
-        sw[0][0] = sw[1][0];
-        sw[0][1] = sw[1][1];
-        if (n + 1 < total) load_b(1);
-      } else {
-        load_scales(0);
-      }
-      tc::mbar_wait(ring.full + 8 * ring.slot, ring.phase, ring.gave_up);
-      const uint32_t in = ring.data + ring.slot * kSlotBytes + in_box;
-      float d[NT][4] = {};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!ahead) load_words(0, h * kWords / 2, kWords / 2);
-        uint32_t u[4], v[4];
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(in ^ (h * 64)) : "memory");
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"((in ^ (h * 64)) + 1024) : "memory");
-#pragma unroll
-        for (int j = 0; j < (f8 ? 4 : 2); ++j) {
-          uint32_t u0 = u[2 * j & 3], u1 = u[(2 * j + 1) & 3], v0 = v[2 * j & 3], v1 = v[(2 * j + 1) & 3];
-          if constexpr (f8) {
-            fp16_of(u[j], &u0, &u1);
-            fp16_of(v[j], &v0, &v1);
-          }
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            if (NT > 1 && 8 * i >= o.n) break;
-            const uint4& y = b[0][i][(ahead ? h * kWords / 2 : 0) + j / 2];
-            mma<typename std::conditional<f8, __half, T>::type>(f8 ? d[i] : sum[i], u0, v0, u1, v1, j & 1 ? y.z : y.x, j & 1 ? y.w : y.y);
-          }
+          if (NT > 1 && 8 * i >= n_tokens) break;
+          const uint4& y = b[from][i][(ahead ? h * kWords / 2 : 0) + j / 2];
+          mma<typename std::conditional<f8, __half, T>::type>(f8 ? d[i] : sum[i], u0, v0, u1, v1, j & 1 ? y.z : y.x, j & 1 ? y.w : y.y);
         }
       }
-      __syncwarp();  // read by all lanes: the slot may be written again
-      if (n + kAhead < total && lane == 0) load_a(ring.slot);
-      ring.next();
-      if constexpr (f8) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[i][j], sw[0][j >> 1] * sx[0][i][j & 1], sum[i][j]);
-      }
-      if (!ahead) next_b();
     }
-    done(o, sum, i0 + 1 == hi);
-    walk_c.next();
+    __syncwarp();  // read by all lanes: the slot may be written again
+    if (n + kAhead < total && lane == 0) load_a(ring.slot);
+    ring.next();
+    if constexpr (f8) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[i][j], sw[from][j >> 1] * sx[from][i][j & 1], sum[i][j]);
+    }
+    if (!ahead) next_b();
+    ++n;
+  };
+  int mine = lo + team.group;
+  for (int first = lo; first < hi;) {
+    const int stop = done.segment_end(first, hi);
+    for (; mine < stop; mine += team.groups) {
+      const Piece o = walk_c.at();
+      n_tokens = o.n;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[i][j] = 0.0f;
+#pragma unroll 1
+      for (int turn = 0; turn < turns; ++turn) {
+        if (ahead && (n & 1)) step(1, 0);
+        else step(0, ahead ? 1 : 0);
+      }
+      done.put(o, mine - first, sum);
+      walk_c.advance(team.groups);
+    }
+    done.join(first, stop, stop == hi);
+    first = stop;
   }
 }
 
 // After a piece of the gated products its warps' sums go to shared memory;
-// after kBatch of them they are joined and the activation is taken and written;
-// with 8-bit weights it is quantised at the end of the run.
+// after kBatch pieces of each group they are joined and the activation is taken
+// and written; with 8-bit weights it is quantised at the end of the run.
 template <typename T, bool f8, int NT>
 struct UpDone {
   static constexpr int kCols = 8 * NT, kBatch = Depth<f8, NT>::kBatch;
-  static constexpr int kPieceFloats = kWarps * 16 * kCols;
-  static_assert(2 * kBatch * kPieceFloats == kRedFloats, "shared memory");
+  static constexpr int kWarpFloats = 16 * kCols;
+  static_assert(2 * kBatch * kWarps * kWarpFloats == kRedFloats, "shared memory");
   const FewParams& p;
   Choice& c;
-  float* red;  // [2][kBatch][kWarps][16][kCols]
-  int warp, lane, lo, first, have, turn;  // the run's and the batch's first piece
-  const float* scales;  // 8-bit weights: the tokens', in shared memory
-  __device__ __forceinline__ const float* token_scales() const { return scales; }
+  float* red;  // [2][kBatch pieces of each group][its warps][16][kCols]
+  const Team& team;
+  int warp, lane, lo, turn;
+  uint32_t scales;  // 8-bit weights: the tokens', in shared memory
+  __device__ __forceinline__ uint32_t token_scales() const { return scales; }
   __device__ __forceinline__ void wait() const {}
-  __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool end) {
-    float* mine = red + (turn * kBatch + have) * kPieceFloats + warp * 16 * kCols;
+  __device__ __forceinline__ int segment_end(int first, int hi) const { return min(hi, first + kBatch * team.groups); }
+  __device__ __forceinline__ void put(const Piece& o, int b, const float (&sum)[NT][4]) const {
+    float* mine = red + (turn * kBatch * kWarps + b * team.split + team.sub) * kWarpFloats;
     const int g = box_row(lane >> 2), t = lane & 3;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -540,18 +570,19 @@ struct UpDone {
       *reinterpret_cast<float2*>(mine + g * kCols + 8 * i + 2 * t) = make_float2(sum[i][0], sum[i][1]);
       *reinterpret_cast<float2*>(mine + (g + 8) * kCols + 8 * i + 2 * t) = make_float2(sum[i][2], sum[i][3]);
     }
-    if (++have < kBatch && !end) return;
+  }
+  __device__ __forceinline__ void join(int first, int stop, bool end) {
     __syncthreads();
-    const int col = threadIdx.x % kCols, f = threadIdx.x / kCols % 8, b = threadIdx.x / (8 * kCols);
-    if (b < have) {
+    for (int j = threadIdx.x; j < (stop - first) * 8 * kCols; j += kThreads) {
+      const int col = j % kCols, f = j / kCols % 8, b = j / (8 * kCols);
       const Piece q = Walk<false>(p, c, first + b).at();
       if (col < q.n) {
-        const float* at = red + (turn * kBatch + b) * kPieceFloats + f * kCols + col;
+        const float* at = red + (turn * kBatch * kWarps + b * team.split) * kWarpFloats + f * kCols + col;
         float gate = 0.0f, up = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          gate += at[w * 16 * kCols];
-          up += at[w * 16 * kCols + 8 * kCols];
+#pragma unroll 4
+        for (int w = 0; w < team.split; ++w) {
+          gate += at[w * kWarpFloats];
+          up += at[w * kWarpFloats + 8 * kCols];
         }
         const float a = swiglu(gate, up);
         const long long i = static_cast<long long>(q.pos + col) * p.F + q.tile * 8 + f;
@@ -560,17 +591,15 @@ struct UpDone {
       }
     }
     turn ^= 1;  // the other buffer next: the sums here are still being read
-    first += have;
-    have = 0;
     if constexpr (f8)
-      if (end) quantize_run();
+      if (end) quantize_run(stop);
   }
   // The run's features to 8 bits, a block of 128 (16 pieces) at a time.  The
   // first and the last may be other blocks' too: who brings the last piece
   // quantises them.
-  __device__ __forceinline__ void quantize_run() const {
+  __device__ __forceinline__ void quantize_run(int hi) const {
     constexpr int kPieces = kF8Block / 8;
-    const int hi = first, b0 = lo / kPieces, b1 = (hi - 1) / kPieces;
+    const int b0 = lo / kPieces, b1 = (hi - 1) / kPieces;
     __threadfence();
     if (threadIdx.x == 0) c.last = 0;
     __syncthreads();
@@ -611,7 +640,7 @@ struct DownDone {
   Choice& c;
   float* red;  // [kWarps][16][T]
   int warp, lane, lo, pieces, blocks;  // blocks: those that have pieces
-  __device__ __forceinline__ const float* token_scales() const { return nullptr; }
+  __device__ __forceinline__ uint32_t token_scales() const { return 0; }
   __device__ __forceinline__ void zero() const {
     for (int i = lane; i < 16 * p.T; i += 32) red[warp * 16 * p.T + i] = 0.0f;
     __syncwarp();
@@ -624,7 +653,8 @@ struct DownDone {
     return static_cast<int>(((piece + 1) * blocks - 1) / pieces);
   }
   __device__ __forceinline__ int start_of(long long block) const { return static_cast<int>(block * pieces / blocks); }
-  __device__ __forceinline__ void operator()(const Piece& o, const float (&sum)[NT][4], bool end) {
+  __device__ __forceinline__ int segment_end(int first, int hi) const { return min(hi, (first / c.num_used + 1) * c.num_used); }
+  __device__ __forceinline__ void put(const Piece& o, int, const float (&sum)[NT][4]) const {
     float* mine = red + warp * 16 * p.T;
     const int g = box_row(lane >> 2), t = lane & 3;
 #pragma unroll
@@ -642,15 +672,17 @@ struct DownDone {
       }
     }
     __syncwarp();  // an expert's columns are other lanes' in the next piece
-    if (!end && o.u + 1 < c.num_used) return;
+  }
+  __device__ __forceinline__ void join(int first, int, bool end) const {
+    const int at = first / c.num_used;  // the tile
     __syncthreads();
-    const bool alone = first_block(o.tile) == last_block(o.tile);
+    const bool alone = first_block(at) == last_block(at);
     for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
       float s = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) s += red[w * 16 * p.T + i];
-      if (alone) put(o.tile, i, s);
-      else part_of(blockIdx.x, o.tile)[i] = s;
+      if (alone) store(at, i, s);
+      else part_of(blockIdx.x, at)[i] = s;
     }
     if (end) {
       // This block's first and last tile may be others' too: it says that its
@@ -660,17 +692,17 @@ struct DownDone {
       if (threadIdx.x == 0) c.last = 0;
       __syncthreads();
       if (threadIdx.x < 2) {
-        const int tile = threadIdx.x == 0 ? begins : o.tile, others = last_block(tile) - first_block(tile);
+        const int tile = threadIdx.x == 0 ? begins : at, others = last_block(tile) - first_block(tile);
         if (others > 0 && (threadIdx.x == 0 || tile != begins) && atomicAdd(p.done + tile, 1) == others) atomicOr(&c.last, 1 << threadIdx.x);
         __threadfence();
       }
       __syncthreads();
       for (int left = c.last; left; left &= left - 1) {
-        const int tile = left & 1 ? begins : o.tile;
+        const int tile = left & 1 ? begins : at;
         for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
           float s = 0.0f;
           for (int b = first_block(tile); b <= last_block(tile); ++b) s += __ldcg(part_of(b, tile) + i);
-          put(tile, i, s);
+          store(tile, i, s);
         }
       }
       return;
@@ -684,7 +716,7 @@ struct DownDone {
   __device__ __forceinline__ float* part_of(int block, int tile) const {
     return p.part + (static_cast<long long>(block) * 2 + (start_of(block) / c.num_used == tile ? 0 : 1)) * 16 * p.T;
   }
-  __device__ __forceinline__ void put(int tile, int i, float s) const {
+  __device__ __forceinline__ void store(int tile, int i, float s) const {
     const int h = tile * kFewRows + i / p.T;
     if (h < p.H) static_cast<T*>(p.out)[static_cast<long long>(i % p.T) * p.H + h] = from_f32<T>(s);
   }
@@ -729,13 +761,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       static_cast<T*>(p.out)[i] = from_f32<T>(0.0f);
     return;
   }
+  constexpr int es = f8 ? 1 : 2;
   {
     const Run run(static_cast<long long>(c.num_used) * (p.F / 8));
-    run_pieces<T, f8, NT, false>(p, c, map13, ring, run.lo, run.hi, warp, lane, UpDone<T, f8, NT>{p, c, red, warp, lane, run.lo, run.lo, 0, 0, scales});
+    const Team team(run.pieces / run.blocks, (p.H * es + kStepBytes - 1) / kStepBytes, warp);
+    run_pieces<T, f8, NT, false>(p, c, map13, ring, run.lo, run.hi, team, lane,
+                                 UpDone<T, f8, NT>{p, c, red, team, warp, lane, run.lo, 0, tc::smem_addr(scales)});
   }
   {
     const Run run(static_cast<long long>(c.num_used) * ((p.H + kFewRows - 1) / kFewRows));
-    run_pieces<T, f8, NT, true>(p, c, map2, ring, run.lo, run.hi, warp, lane, DownDone<T, NT>{p, c, red, warp, lane, run.lo, run.pieces, run.blocks});
+    const Team team(run.pieces / run.blocks, (p.F * es + kStepBytes - 1) / kStepBytes, warp);
+    run_pieces<T, f8, NT, true>(p, c, map2, ring, run.lo, run.hi, team, lane,
+                                DownDone<T, NT>{p, c, red, warp, lane, run.lo, run.pieces, run.blocks});
   }
   __syncthreads();
   if (threadIdx.x == 0 && gave_up) {

@@ -102,98 +102,123 @@ __global__ void __launch_bounds__(1024) ep_norm_kernel(const NormParams p) {
       p.scales[static_cast<long long>(blockIdx.x) * scale_columns(p.H) + b] = 0.0f;
 }
 
-// A row's gradients and h, a thread's vectors of them.
-template <typename T, int NV>
-struct GradRow {
-  Raw8<T> dy[NV], h[NV], ds[NV];
-  __device__ __forceinline__ void load(const NormParams& p, int t) {
-    const long long row = static_cast<long long>(t) * p.H;
+// A thread's vector of a row's gradients and h.
+template <typename T>
+struct GradVec {
+  Raw8<T> dy, h, ds;
+  __device__ __forceinline__ void load(const NormParams& p, int t, int v, bool stream) {
+    const long long at = static_cast<long long>(t) * p.H + 8 * v;
+    dy.load_rw(static_cast<const T*>(p.dy) + at);
+    h.load_rw(static_cast<const T*>(p.x) + at);
+    if (stream && p.dsum != nullptr) ds.load_rw(static_cast<const T*>(p.dsum) + at);
+  }
+  __device__ __forceinline__ void sums(const float (&w)[8], float* ss, float* inner) const {
+    float a[8], b[8];
+    dy.get(a);
+    h.get(b);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (t < p.T && v < p.H / 8) {
-        dy[i].load_rw(static_cast<const T*>(p.dy) + row + 8 * v);
-        h[i].load_rw(static_cast<const T*>(p.x) + row + 8 * v);
-        if (p.dsum != nullptr) ds[i].load_rw(static_cast<const T*>(p.dsum) + row + 8 * v);
-      }
+    for (int j = 0; j < 8; ++j) {
+      *ss = fmaf(b[j], b[j], *ss);
+      *inner = fmaf(a[j] * w[j], b[j], *inner);
     }
+  }
+  __device__ __forceinline__ void finish(const NormParams& p, int t, int v, const float (&w)[8], float r, float c, float (&dw)[8]) const {
+    float a[8], b[8], s[8];
+    dy.get(a);
+    h.get(b);
+    if (p.dsum != nullptr) {
+      ds.get(s);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dw[j] = fmaf(a[j] * r, b[j], dw[j]);
+      s[j] = fmaf(r, fmaf(-b[j], c, a[j] * w[j]), s[j]);
+    }
+    store8<T>(static_cast<T*>(p.dh) + static_cast<long long>(t) * p.H + 8 * v, s);
   }
 };
 
-// Blocks stride over the rows; a thread keeps its columns' share of dw.  The
-// next row is loaded before the sums over this one are joined: without that a
-// block waits for memory between its rows (8,192 x 7168 bf16: 119 us).
+// Blocks stride over the rows; a thread keeps its columns' share of dw.  One
+// vector a thread (rows of up to 8192): the next row is loaded before the sums
+// over this one are joined, and the weights stay in registers (8,192 x 7168
+// bf16: 119 us without either, 92 with the first, 85 with both; then near two
+// thirds of the issue slots are busy).  Longer rows are read twice, the second
+// time from L2: the registers hold dw.
 template <typename T, int NV>
-__global__ void __launch_bounds__(1024) ep_norm_bwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) ep_norm_bwd_kernel(const NormParams p) {
   __shared__ float part[2][64];
   pdl_wait();
-  const int vectors = p.H / 8;
+  const int vectors = p.H / 8, v0 = threadIdx.x;
+  const T* weight = static_cast<const T*>(p.weight);
   float dw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   int turn = 0;
-  GradRow<T, NV> next;
-  next.load(p, blockIdx.x);
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
-    const long long row = static_cast<long long>(t) * p.H;
-    const GradRow<T, NV> at = next;
-    next.load(p, t + static_cast<int>(gridDim.x));
-    float ss = 0.0f, inner = 0.0f;
+  if constexpr (NV == 1) {
+    const bool in = v0 < vectors;
+    float w[8];
+    GradVec<T> next;
+    if (in) {
+      Raw8<T> wr;
+      wr.load(weight + 8 * v0);
+      wr.get(w);
+      if (static_cast<int>(blockIdx.x) < p.T) next.load(p, blockIdx.x, v0, true);
+    }
+    for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+      const GradVec<T> at = next;
+      if (in && t + static_cast<int>(gridDim.x) < p.T) next.load(p, t + gridDim.x, v0, true);
+      float ss = 0.0f, inner = 0.0f;
+      if (in) at.sums(w, &ss, &inner);
+      const float2 sums = block_sum2(ss, inner, part[turn]);
+      const float r = 1.0f / sqrtf(sums.x / static_cast<float>(p.H) + p.eps);
+      if (in) at.finish(p, t, v0, w, r, r * r * (sums.y / static_cast<float>(p.H)), dw[0]);
+    }
+  } else {
+    for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+      float ss = 0.0f, inner = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < vectors) {
-        Raw8<T> wr;
-        float a[8], b[8], w[8];
-        wr.load(static_cast<const T*>(p.weight) + 8 * v);
-        wr.get(w);
-        at.dy[i].get(a);
-        at.h[i].get(b);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ss = fmaf(b[j], b[j], ss);
-          inner = fmaf(a[j] * w[j], b[j], inner);
+      for (int i = 0; i < NV; ++i) {
+        const int v = v0 + i * blockDim.x;
+        if (v < vectors) {
+          GradVec<T> at;
+          Raw8<T> wr;
+          float w[8];
+          at.load(p, t, v, false);
+          wr.load(weight + 8 * v);
+          wr.get(w);
+          at.sums(w, &ss, &inner);
         }
       }
-    }
-    const float2 sums = block_sum2(ss, inner, part[turn]);
-    const float r = 1.0f / sqrtf(sums.x / static_cast<float>(p.H) + p.eps);
-    const float c = r * r * (sums.y / static_cast<float>(p.H));
+      const float2 sums = block_sum2(ss, inner, part[turn]);
+      const float r = 1.0f / sqrtf(sums.x / static_cast<float>(p.H) + p.eps), c = r * r * (sums.y / static_cast<float>(p.H));
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < vectors) {
-        Raw8<T> wr;
-        float a[8], b[8], w[8], s[8];
-        wr.load(static_cast<const T*>(p.weight) + 8 * v);
-        wr.get(w);
-        at.dy[i].get(a);
-        at.h[i].get(b);
-        if (p.dsum != nullptr) {
-          at.ds[i].get(s);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+      for (int i = 0; i < NV; ++i) {
+        const int v = v0 + i * blockDim.x;
+        if (v < vectors) {
+          GradVec<T> at;
+          Raw8<T> wr;
+          float w[8];
+          at.load(p, t, v, true);
+          wr.load(weight + 8 * v);
+          wr.get(w);
+          at.finish(p, t, v, w, r, c, dw[i]);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dw[i][j] = fmaf(a[j] * r, b[j], dw[i][j]);
-          s[j] = fmaf(r, fmaf(-b[j], c, a[j] * w[j]), s[j]);
-        }
-        store8<T>(static_cast<T*>(p.dh) + row + 8 * v, s);
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
+    const int v = v0 + i * blockDim.x;
     if (v < vectors) store8<float>(p.partial + static_cast<long long>(blockIdx.x) * p.H + 8 * v, dw[i]);
   }
 }
 
-constexpr int kSumRows = 8;  // groups of partial rows per block, 32 columns wide
+constexpr int kSumRows = 16;  // groups of partial rows per block, 32 columns wide
 
 __global__ void __launch_bounds__(32 * kSumRows) ep_norm_dw_kernel(const NormParams p, int parts) {
   __shared__ float part[kSumRows][33];
@@ -233,12 +258,11 @@ cudaError_t norm_typed(const NormParams& p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t norm_bwd_typed(const NormParams& p, int parts, cudaStream_t s) {
-  // One vector a thread as far as a block goes: the registers hold two rows.
-  const int vectors = p.H / 8, nv = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 4;
-  const dim3 grid(parts), block(std::min(1024, ((vectors + nv - 1) / nv + 31) / 32 * 32));
-  if (nv == 1) return launch_pdl(ep_norm_bwd_kernel<T, 1>, grid, block, 0, s, 0, p);
-  if (nv == 2) return launch_pdl(ep_norm_bwd_kernel<T, 2>, grid, block, 0, s, 0, p);
-  return launch_pdl(ep_norm_bwd_kernel<T, 4>, grid, block, 0, s, 0, p);
+  const int vectors = p.H / 8;
+  const dim3 grid(parts);
+  if (vectors <= 1024) return launch_pdl(ep_norm_bwd_kernel<T, 1>, grid, dim3((vectors + 31) / 32 * 32), 0, s, 0, p);
+  if (vectors <= 2048) return launch_pdl(ep_norm_bwd_kernel<T, 4>, grid, dim3(512), 0, s, 0, p);
+  return launch_pdl(ep_norm_bwd_kernel<T, 8>, grid, dim3(512), 0, s, 0, p);
 }
 
 // The expert of a receive row among offsets[0..E], by the warp: two rounds of
@@ -309,10 +333,12 @@ cudaError_t quantize_typed(const QuantParams& p, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-// One or two blocks for each of 152 SMs (rows over 4096 elements: a block of 513
-// to 1024 threads), whatever the device has, so that the order of dw's sum does
-// not depend on it.
-int norm_bwd_parts(long long T, long long H) { return static_cast<int>(std::min<long long>(T, H > 4096 ? 152 : 304)); }
+// One to four blocks for each of 152 SMs, whatever the device has, so that the
+// order of dw's sum does not depend on it: blocks of 513 to 1024 threads, 257 to
+// 512 and fewer.
+int norm_bwd_parts(long long T, long long H) {
+  return static_cast<int>(std::min<long long>(T, H > 8192 ? 304 : H > 4096 ? 152 : H > 2048 ? 304 : 608));
+}
 
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   if (p.dtype == EP_DTYPE_FP32) return norm_typed<float>(p, s);

@@ -135,7 +135,7 @@ def test_norm_gradient(ep, T, H, through, dtype):  # noqa: F811
         want = gh + (ds.double() if through else 0)
         bound = UNIT[dtype] * want.abs() + 8e-6 * terms + 2.0 ** -23 * want.abs() + TINY[dtype]
         assert bool(((dh.double() - want).abs() <= bound).all())
-        # T terms, each off by 3e-6 and added in at most T / 304 + 304 / 8 + 8 <= 64 steps, or T of them where fewer
+        # T terms, each off by 3e-6 and added in at most T / parts + parts / 16 + 16 <= 64 steps of 2^-24 (152 to 608 parts)
         mag = (dy.double() * hh * r).abs().sum(0)
         assert bool(((dw.double() - gw).abs() <= 8e-6 * mag + 1e-37).all())
     again, dw2 = dy.clone(), dw.clone()
