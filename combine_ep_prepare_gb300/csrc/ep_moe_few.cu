@@ -315,12 +315,12 @@ __device__ __forceinline__ float load_shared(uint32_t addr) {
 // warp's 16-byte loads meet all banks.
 __device__ __forceinline__ int box_row(int g) { return (g >> 1) | (g & 1) << 2; }
 
-// Whether the tokens' operand comes a step ahead or half a step at a time, just
-// before its use (registers), and the pieces of the gated products that are
-// joined at a time.
+// How many steps of the tokens' operand are in registers at a time (with one, it
+// comes half a step at a time, just before its use), and the pieces of the gated
+// products that are joined at a time.
 template <bool f8, int NT>
 struct Depth {
-  static constexpr bool kTokensAhead = NT == 1 || (NT == 2 && !f8);
+  static constexpr int kTokens = NT == 1 || (NT == 2 && !f8) ? 2 : 1;
   static constexpr int kBatch = 4 / NT;
 };
 constexpr int kRedFloats = 2 * 4 * kWarps * 16 * 8;  // two batches' sums
@@ -354,8 +354,8 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
                                            int lane, Done done) {
   using E = typename std::conditional<f8, uint8_t, T>::type;
   constexpr int kWords = f8 ? 4 : 2;  // 16-byte words of a token that meet a lane's two of a weight row
-  constexpr bool ahead = Depth<f8, NT>::kTokensAhead;
-  constexpr int kTokens = ahead ? 2 : 1;
+  constexpr int kTokens = Depth<f8, NT>::kTokens;
+  constexpr bool ahead = kTokens > 1;
   const int red = (down ? p.F : p.H) * static_cast<int>(sizeof(E)), rows = down ? p.H : 2 * p.F;  // red in bytes
   const int turns = ((red + kStepBytes - 1) / kStepBytes + team.split - 1) / team.split, stride = team.split * kStepBytes;
   const int own = max(0, (hi - lo - team.group + team.groups - 1) / team.groups), total = own * turns;
@@ -478,13 +478,31 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
     }
   done.wait();
   if (total > 0) place_b();
-  if (ahead && total > 0) load_b(0);
+  if (ahead && total > 0) load_b(1);
   float sum[NT][4];
   int n = 0, n_tokens = 0;
-  // One step with the tokens' words in b[from], the next step's going to b[to].
-  auto step = [&](int from, int to) {
-    if (!ahead) load_scales(0);
-    else if (n + 1 < total) load_b(to);
+  auto step = [&]() {
+    if constexpr (ahead) {
+      // The words change places, not the code: a copy of a step for each buffer
+      // of them misses the instruction cache (one token, 7168 -> 2 x 2048: 123 us
+      // with one copy, 126 with two, 134 with four).
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) b[0][i][j] = b[1][i][j];
+        if constexpr (f8) {
+          sx[0][i][0] = sx[1][i][0];
+          sx[0][i][1] = sx[1][i][1];
+        }
+      }
+      if constexpr (f8) {
+        sw[0][0] = sw[1][0];
+        sw[0][1] = sw[1][1];
+      }
+      if (n + 1 < total) load_b(1);
+    } else {
+      load_scales(0);
+    }
     tc::mbar_wait(ring.full + 8 * ring.slot, ring.phase, ring.gave_up);
     const uint32_t in = ring.data + ring.slot * kSlotBytes + in_box;
     float d[NT][4] = {};
@@ -504,7 +522,7 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           if (NT > 1 && 8 * i >= n_tokens) break;
-          const uint4& y = b[from][i][(ahead ? h * kWords / 2 : 0) + j / 2];
+          const uint4& y = b[0][i][(ahead ? h * kWords / 2 : 0) + j / 2];
           mma<typename std::conditional<f8, __half, T>::type>(f8 ? d[i] : sum[i], u0, v0, u1, v1, j & 1 ? y.z : y.x, j & 1 ? y.w : y.y);
         }
       }
@@ -516,7 +534,7 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[i][j], sw[from][j >> 1] * sx[from][i][j & 1], sum[i][j]);
+        for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(d[i][j], sw[0][j >> 1] * sx[0][i][j & 1], sum[i][j]);
     }
     if (!ahead) next_b();
     ++n;
@@ -532,10 +550,7 @@ __device__ __forceinline__ void run_pieces(const FewParams& p, const Choice& c, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[i][j] = 0.0f;
 #pragma unroll 1
-      for (int turn = 0; turn < turns; ++turn) {
-        if (ahead && (n & 1)) step(1, 0);
-        else step(0, ahead ? 1 : 0);
-      }
+      for (int turn = 0; turn < turns; ++turn) step();
       done.put(o, mine - first, sum);
       walk_c.advance(team.groups);
     }
