@@ -8,22 +8,35 @@
 // M side, 128 in each SM) times up to 256 rows of an expert (the N side), and
 // a slab of the reduction is 128 bytes wide -- here 128 elements, one block of
 // the scales.  The scales are arbitrary float32 numbers, so the tensor core
-// can sum over one block only: each slab goes to one of two accumulators in
-// tensor memory, and eight warps add it to sums in registers, times the row's
-// scale and the weights', while the next slab is multiplied into the other.
+// can sum over one block only: each slab goes to an accumulator in tensor
+// memory of its own (two of 256 columns in turn, up to eight where tiles have
+// few rows), and eight warps add it to sums in registers, times the row's scale
+// and the weights', while the next slab is multiplied into another.
 //
-// A slab's mma take 512 clocks at the nominal rate of 8-bit operands.  Adding
-// it takes a warp 64 packed multiply-adds, 8 loads from tensor memory and 16
-// of the scales.  The loads are 16 lanes x 256 bits, which give a lane two
-// columns (rows of the tile) in eight, so that it needs 32 rows' scales and
-// not all 128 of its half: with one lane per feature the scales' loads alone
-// would keep shared memory busy for 256 clocks a slab, next to the operands'.
-// A warp of its own brings the scales in, four slabs at a time.
+// Adding a slab takes a warp 64 packed multiply-adds, 16 loads from tensor
+// memory and 8 of the scales.  The loads are 16 lanes x 256 bits, which give a
+// lane two columns (rows of the tile) in eight, so that it needs 32 rows'
+// scales and not all 128 of its half: with one lane per feature the scales'
+// loads alone would keep shared memory busy for 256 clocks a slab, next to the
+// operands'.  A warp of its own brings the scales in, four slabs at a time.
+//
+// With many rows the additions bound it.  8 experts x 1,024 rows, 7168 -> 4096,
+// take 230 us (2.09 PFLOP/s), 139 without the additions and 221 with one mma of
+// four; the additions with neither loads nor mma take 152.  With ragged experts
+// (16,384 rows over 32 of them, 7168 -> 2 x 2048, 8-bit result) 557 us, with even
+// ones 496; the 16-bit product takes 655 to 712.  With a few rows per expert the
+// weights' bytes do: 64 experts x 4 rows, 301 us, 6.2 TB/s; 2048 -> 7168, 145 us,
+// 6.5 TB/s.  What it took: sums that stay in their registers (a branch on the
+// tile's width in the loop made 115 moves a slab and warp: 889 us for the 496),
+// packed multiply-adds from the compiler's own pairs (530), and mma issued from
+// uniform registers (up decode 375 us before, 301 after).  Columns per load,
+// loads further ahead, stages and the split of registers made no difference.
 //
 // The gated pair: 16 gate rows and the 16 up rows of the same features
 // alternate in the tile, and land in one lane's two halves of the sums.  Its
 // 8-bit result needs the largest magnitude of a row's 128 features, 64 in each
-// SM of the pair: they exchange theirs through distributed shared memory.
+// SM of the pair: they exchange theirs through distributed shared memory (19 us
+// of the 496 beside a 16-bit result).
 #include <algorithm>
 #include <atomic>
 

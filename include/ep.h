@@ -630,6 +630,8 @@ ep_status_t ep_router_bwd(ep_router_config_t config, const void* logits, const i
  * padding row's are zero.  Layers of bf16 and fp16 payload take them, which is
  * the type of their 16-bit operands and results.  Feature counts are multiples
  * of 16 up to 2^20; ffn_features, a gated pair's, are multiples of 128.
+ * Waits, EP_ST_TIMEOUT and graph capture are as for the other expert products:
+ * make the first call of each on a device before any capture.
  * ------------------------------------------------------------------------ */
 
 /* Largest feature count of the row calls that hold a row on chip. */
@@ -725,9 +727,12 @@ ep_status_t ep_expert_dgrad_f8_swiglu(ep_handle_t handle, const uint8_t* dy, con
  * used by one call at a time (calls on one workspace are ordered by a stream
  * or events; two graphs that may run at once need two).  Its contents need not
  * be set, and nothing is kept there from one call to the next.  The second
- * kernel is a cooperative launch whose blocks wait for one another once, with
- * a limit of about a second; if that runs out, out is incomplete and the
- * workspace's first 32-bit word is EP_ST_TIMEOUT, else 0.
+ * kernel is a cooperative launch whose blocks wait for one another once, and
+ * whose copies are waited for, with limits of one and two seconds; if one runs
+ * out, out is incomplete and the workspace's first 32-bit word is
+ * EP_ST_TIMEOUT, else 0.  The order of the sums goes by the sizes, the choice
+ * and the device's number of SMs.  Make the first call of each configuration's
+ * types on a device before any capture.
  * ------------------------------------------------------------------------ */
 #define EP_MAX_FEW_TOKENS 32
 
