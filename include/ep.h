@@ -640,7 +640,8 @@ ep_status_t ep_router_bwd(ep_router_config_t config, const void* logits, const i
 /* Root-mean-square norm of num_tokens rows, with an addition before it:
  *   h = x + residual, rounded to the payload type (h = x without a residual)
  *   y = h * (mean of h^2 + eps)^(-1/2) * weight
- * in float32 from h on.  Any of the results may be left out (NULL), not all:
+ * in float32 from h on (a row whose squares pass its range, 3.4e38, or vanish in
+ * it with eps = 0, has no norm there).  Any of the results may be left out (NULL), not all:
  * sum [T, H] receives h (only with a residual), y [T, H] the norm rounded to
  * the payload type, q [T, H] and scales float32 [T, S(H)] the unrounded norm
  * quantised (both or neither).  sum may be x or residual itself, y may be x.

@@ -193,3 +193,37 @@ def test_unprepared_and_empty_batches_write_nothing(ep):  # noqa: F811
         ep.ep_expert_quantize(h, y, q.view(F8), qs)
         assert bool((y == 3.0).all()) and bool((q == 5).all()) and bool((qs == 1).all())
         ep.ep_prepare(h, torch.full((8, 2), -1, device="cuda"), torch.empty(4, dtype=torch.int32, device="cuda"), 1)  # every route masked
+
+
+def test_offsets_past_2_to_the_31(ep):  # noqa: F811
+    """The last expert's rows lie past element 2^31 of the rows, then of the gradients."""
+    T, n, k = (1 << 18) + 96, 16, 8192
+    lid, size = ep.ep_register_layer(2, 1, k, T, 1)
+    R, h = ep.ep_recv_capacity(lid), ep.alloc_handle(lid, size)
+    last = 90
+    idx = torch.zeros(T, 1, dtype=torch.int64, device="cuda")
+    idx[-last:] = 1
+    ep.ep_prepare(h, idx, torch.empty(2, dtype=torch.int32, device="cuda"), 1)
+    own = slice(T - last, T)
+    x = torch.zeros(R, k, dtype=F8, device="cuda")
+    xs = torch.zeros(R, columns(k), device="cuda")
+    q, sc = torch.empty(last, k, dtype=F8, device="cuda"), torch.empty(last, columns(k), device="cuda")
+    ep.ep_quantize_rows(wl.payload_normal(last, k, 51, "fp32").cuda(), q, sc)
+    x.view(torch.uint8)[own], xs[own] = q.view(torch.uint8), sc
+    w, ws, wv = weights8(ep, 2, n, k, 52)
+    y = torch.empty(R, n, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_gemm_f8(h, x, xs, w, ws, y)
+    v = q.double() * sc.double().repeat_interleave(128, 1)[:, :k]
+    want, mag = v @ wv[1].t(), sum_bound(k) * (v.abs() @ wv[1].abs().t())
+    assert bool(((y[own].double() - want).abs() <= mag + UNIT["bf16"] * (want.abs() + mag)).all())
+    del x, xs
+    dy, ds = torch.zeros(R, n, dtype=F8, device="cuda"), torch.zeros(R, columns(n), device="cuda")
+    q, sc = torch.empty(last, n, dtype=F8, device="cuda"), torch.empty(last, columns(n), device="cuda")
+    ep.ep_quantize_rows(wl.payload_normal(last, n, 53, "fp32").cuda(), q, sc)
+    dy.view(torch.uint8)[own], ds[own] = q.view(torch.uint8), sc
+    dx = torch.empty(R, k, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_dgrad_f8(h, dy, ds, w, ws, dx)
+    v = q.double() * sc.double()[:, :1]
+    want, mag = v @ wv[1], sum_bound(n) * (v.abs() @ wv[1].abs())
+    assert bool(((dx[own].double() - want).abs() <= mag + UNIT["bf16"] * (want.abs() + mag)).all())
+    assert bool((dx[: T - last: 4096] == 0).all())

@@ -117,7 +117,7 @@ def test_norm_of_zero_rows_and_no_tokens(ep):  # noqa: F811
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("through", [False, True])
-@pytest.mark.parametrize("T,H", [(1, 8), (2, 80), (5, 1024), (700, 200), (1001, 2176), (40, 7168), (3, 32768)])
+@pytest.mark.parametrize("T,H", [(1, 8), (2, 80), (5, 1024), (700, 200), (1001, 2176), (40, 7168), (5, 8208), (310, 16384), (3, 32768)])
 def test_norm_gradient(ep, T, H, through, dtype):  # noqa: F811
     eps = 1e-5
     h, dy = rows(T, H, 10, dtype, spread=False), rows(T, H, 11, dtype, spread=False)
@@ -189,7 +189,8 @@ def test_expert_quantize_leaves_other_rows(ep, E, K, T, n, A, p_mask):  # noqa: 
 
 @pytest.mark.parametrize("A", [1, 16])
 @pytest.mark.parametrize("E,K,T,H,p_mask", [(8, 2, 40, 256, 0.1), (64, 8, 128, 7168, 0.5), (300, 8, 64, 1040, 0.3), (3, 1, 5, 16, 0.0),
-                                            (4, 2, 9, 528, 1.0), (2, 2, 2000, 2048, 0.0)])
+                                            (4, 2, 9, 528, 1.0), (2, 2, 2000, 2048, 0.0), (4, 2, 3001, 2080, 0.2), (4, 2, 1500, 2064, 0.2),
+                                            (2, 1, 2500, 16, 0.0)])
 def test_dispatch_f8(ep, E, K, T, H, A, p_mask):  # noqa: F811
     idx, wts = wl.random_routing(T, K, E, 22, p_mask=p_mask)
     lid, size = ep.ep_register_layer(E, K, H, T, A)
@@ -213,3 +214,36 @@ def test_dispatch_f8(ep, E, K, T, H, A, p_mask):  # noqa: F811
     wq[at], wsc[at], ww[at] = q.view(torch.uint8)[t], s[t], wts[t, k]
     assert torch.equal(rq[:P], wq) and torch.equal(rs[:P], wsc) and torch.equal(rw[:P], ww)
     assert bool((rq[P:] == 0x35).all()) and bool((rs[P:] == 7.0).all()) and bool((rw[P:] == 7.0).all())
+
+
+def test_offsets_past_2_to_the_31(ep):  # noqa: F811
+    """The last rows of tensors with more than 2^31 elements are those of a call on them alone."""
+    T, H, n = (1 << 18) + 40, 8192, 4
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(24))
+    w = (1 + 0.3 * rows(1, H, 25, "bf16", False)[0]).to(x.dtype)
+    q, s = torch.empty(T, H, dtype=F8, device="cuda"), torch.empty(T, columns(H), device="cuda")
+    q2, s2 = torch.empty(n, H, dtype=F8, device="cuda"), torch.empty(n, columns(H), device="cuda")
+    ep.ep_quantize_rows(x, q, s)
+    ep.ep_quantize_rows(x[-n:], q2, s2)
+    assert same(q[-n:], q2) and torch.equal(s[-n:], s2)
+    # every token to its own expert row, last to first expert and back
+    lid, size = ep.ep_register_layer(2, 1, H, T, 1)
+    R, h = ep.ep_recv_capacity(lid), ep.alloc_handle(lid, size)
+    idx = (torch.arange(T, device="cuda") % 2)[:, None].contiguous()
+    ep.ep_prepare(h, idx, torch.empty(2, dtype=torch.int32, device="cuda"), 1)
+    slots = torch.empty(T, 1, dtype=torch.int32, device="cuda")
+    ep.ep_token_slots(h, slots)
+    rq, rs, rw = torch.empty(R, H, dtype=F8, device="cuda"), torch.empty(R, columns(H), device="cuda"), torch.empty(R, device="cuda")
+    ep.ep_dispatch_f8(h, idx, q, s, torch.ones(T, 1, device="cuda"), rq, rs, rw)
+    at = slots[-n:, 0].long()
+    assert int(at.max()) * H > 1 << 31
+    assert same(rq.view(torch.uint8)[at], q2) and torch.equal(rs[at], s2)
+    y, total = torch.empty_like(x), x.clone()
+    ep.ep_rmsnorm(x, w, y=y, residual=total, sum=total, q=q, scales=s)
+    y2, t2 = torch.empty_like(x[-n:]), torch.empty_like(x[-n:])
+    ep.ep_rmsnorm(x[-n:], w, y=y2, residual=x[-n:], sum=t2, q=q2, scales=s2)
+    assert torch.equal(y[-n:], y2) and torch.equal(total[-n:], t2) and same(q[-n:], q2) and torch.equal(s[-n:], s2)
+    dw = torch.empty(H, device="cuda")
+    ep.ep_rmsnorm_bwd(x, total, w, y, dw, ep.rmsnorm_bwd_workspace(T, H))
+    ep.ep_rmsnorm_bwd(x[-n:], t2, w, y2, dw, ep.rmsnorm_bwd_workspace(n, H))
+    assert torch.equal(y[-n:], y2)

@@ -222,3 +222,53 @@ def test_agrees_with_the_8_bit_path(ep):  # noqa: F811
     ep.ep_combine_weighted(h, y, rw, out)
     # K expert outputs rounded to bf16 and the sum once more; a value of act on a border may land one e4m3 step away
     assert ((out.double() - m.out.double()).norm() / m.out.double().norm()).item() <= (K ** 0.5 + 1) * 2.0 ** -8
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("H,F", [(32768, 128), (128, 32768)])
+def test_longest_rows(ep, H, F, f8):  # noqa: F811
+    m = Few(ep, 3, 2, H, F, 32, f8=f8)
+    m.run(ep)
+    m.check()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_nan_tokens_stay_alone(ep, f8):  # noqa: F811
+    """No logit of a token with a NaN can be chosen: it gets zeros, the others their own results."""
+    m = Few(ep, 16, 4, 512, 256, 11, f8=f8)
+    m.x[3, 17] = float("nan")
+    m.run(ep)
+    assert bool((m.idx[3] == -1).all()) and bool((m.out[3] == 0).all())
+    m.x[3] = 0  # of no weight in what the others are compared with
+    keep = m.idx.clone()
+    want = Few(ep, 16, 4, 512, 256, 11, f8=f8)
+    want.x, want.out, want.idx, want.p = (t[torch.arange(11) != 3] for t in (m.x, m.out, keep, m.p))
+    want.check()
+
+
+def test_two_graphs_on_one_workspace_and_two_streams(ep):  # noqa: F811
+    """Two captured calls of other sizes take turns on one workspace; with a workspace each they may run at once."""
+    a, b = Few(ep, 64, 8, 1024, 256, 16, f8=True), Few(ep, 16, 4, 512, 256, 5, seed=90)
+    want = [m.run(ep).clone() for m in (a, b)]
+    both = torch.empty(max(a.work.numel(), b.work.numel()), dtype=torch.uint8, device="cuda")
+    own = [a.work, b.work]
+    a.work = b.work = both
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for g, m in zip(graphs, (a, b)):
+        with torch.cuda.graph(g):
+            m.run(ep)
+    for n in (0, 1, 1, 0, 1, 0, 0):
+        for m in (a, b):
+            m.out.fill_(float("nan"))
+        graphs[n].replay()
+        assert torch.equal((a, b)[n].out, want[n])
+    a.work, b.work = own
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for s, m in zip(streams, (a, b)):
+            m.run(ep, stream=s)
+    torch.cuda.synchronize()
+    for m, w in zip((a, b), want):
+        assert int(m.work[:4].view(torch.int32)) == 0 and torch.equal(m.out, w)
