@@ -210,6 +210,10 @@ __device__ __forceinline__ bool elect() {
   return is != 0;
 }
 
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* m, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y) : "memory");
+}
+
 __device__ __forceinline__ void store_peer(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -390,8 +394,10 @@ struct Epilogue {
   }
 
   // Sixteen rows at a time go through shared memory, unrounded; the gate and up
-  // values of the next sixteen are loaded meanwhile.
-  __device__ __forceinline__ void through_activation(const Tile& t, const Sums& a, int nh) const {
+  // values of the next 32 are loaded meanwhile, the first ones before the slabs
+  // are added (by `add`).
+  template <typename Add>
+  __device__ __forceinline__ void through_activation(const Tile& t, Sums& a, int nh, Add add) const {
     const int f = t.f0 + rank * kHalfM + 4 * lane;
     const long long cols = 2LL * p.K;
     float2* put = reinterpret_cast<float2*>(stage) + (lane & 3) * kPairStride32 + w * 32 + (lane >> 2);
@@ -399,7 +405,7 @@ struct Epilogue {
     const long long at0 = (static_cast<long long>(t.off) + t.r0 + half * nh + 4 * w) * cols + f;
     const T* pre = static_cast<const T*>(p.pre_in) + at0;
     T* out = static_cast<T*>(p.out) + at0;
-    uint2 g[2][4], u[2][4];
+    uint2 g[3][4], u[3][4];
     auto load = [&](int s, uint2 (&gs)[4], uint2 (&us)[4]) {
       const int c0 = half * nh + 16 * s + 4 * w;
 #pragma unroll
@@ -410,11 +416,13 @@ struct Epilogue {
         }
     };
     load(0, g[0], u[0]);
+    if (16 < nh) load(1, g[1], u[1]);
+    add();
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
       if (16 * s >= nh) break;
       const int c0 = half * nh + 16 * s + 4 * w;
-      if (16 * (s + 1) < nh) load(s + 1, g[(s + 1) & 1], u[(s + 1) & 1]);
+      if (16 * (s + 2) < nh) load(s + 2, g[(s + 2) % 3], u[(s + 2) % 3]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -432,7 +440,7 @@ struct Epilogue {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (c0 + r < stop) {
-          const float4 gv = unpack4<T>(g[s & 1][r]), uv = unpack4<T>(u[s & 1][r]);
+          const float4 gv = unpack4<T>(g[s % 3][r]), uv = unpack4<T>(u[s % 3][r]);
           const float gs[4] = {gv.x, gv.y, gv.z, gv.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
           float dg[4], du[4];
 #pragma unroll
@@ -598,7 +606,8 @@ template <typename T, int kind>
 __global__ void __launch_bounds__(kThreads, 1)
     ep_product_f8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                          const __grid_constant__ CUtensorMap map_b64, const __grid_constant__ CUtensorMap map_b32,
-                         const __grid_constant__ CUtensorMap map_b16, const F8Params p) {
+                         const __grid_constant__ CUtensorMap map_b16, const __grid_constant__ CUtensorMap map_pre,
+                         const F8Params p) {
   constexpr bool fwd = kind == kProdFwd || kind == kProdFwdSwiglu;
   extern __shared__ unsigned char raw[];
   unsigned char* ring = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
@@ -665,6 +674,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t bar = rank == 0 ? tc::smem_addr(&s.full[stage]) : tc::in_block(tc::smem_addr(&s.full[stage]), 0);
               if (rank == 0) tc::mbar_expect(bar, 2 * bytes);  // the other block's copies too
               const int x = k * kSlab;
+              if constexpr (kind == kProdDgradSwiglu) {
+                // The gate and up values that the tile's end reads go to L2 while
+                // its last slabs are added (what the other blocks then read and
+                // write at the same time): 297 us without, 295 twelve slabs from
+                // the end, 273 here.
+                const int f = t.f0 + rank * kHalfM;
+                if (!load_a && k == max(0, slabs - 3) && f < p.K)
+                  for (int r = 0; r < t.n; r += 128) {
+                    prefetch_2d(&map_pre, 2 * f, t.off + t.r0 + r);
+                    prefetch_2d(&map_pre, 2 * (f + p.K), t.off + t.r0 + r);
+                  }
+              }
               if (load_a) {
                 if constexpr (kind == kProdFwd) {
                   tc::tma_pair_3d(a, &map_a, bar, x, t.f0 + rank * kHalfM, t.e);
@@ -809,22 +830,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           at.slots.at = 0;
         }
         Sums a;
-        switch (nh / 16) {
-          case 1: add_slabs<kind, 1>(a, s, at, tmem, half, w, lane, slabs); break;
-          case 2: add_slabs<kind, 2>(a, s, at, tmem, half, w, lane, slabs); break;
-          case 3: add_slabs<kind, 3>(a, s, at, tmem, half, w, lane, slabs); break;
-          case 4: add_slabs<kind, 4>(a, s, at, tmem, half, w, lane, slabs); break;
-          case 5: add_slabs<kind, 5>(a, s, at, tmem, half, w, lane, slabs); break;
-          case 6: add_slabs<kind, 6>(a, s, at, tmem, half, w, lane, slabs); break;
-          case 7: add_slabs<kind, 7>(a, s, at, tmem, half, w, lane, slabs); break;
-          default: add_slabs<kind, 8>(a, s, at, tmem, half, w, lane, slabs); break;
-        }
+        auto add = [&]() {
+          switch (nh / 16) {
+            case 1: add_slabs<kind, 1>(a, s, at, tmem, half, w, lane, slabs); break;
+            case 2: add_slabs<kind, 2>(a, s, at, tmem, half, w, lane, slabs); break;
+            case 3: add_slabs<kind, 3>(a, s, at, tmem, half, w, lane, slabs); break;
+            case 4: add_slabs<kind, 4>(a, s, at, tmem, half, w, lane, slabs); break;
+            case 5: add_slabs<kind, 5>(a, s, at, tmem, half, w, lane, slabs); break;
+            case 6: add_slabs<kind, 6>(a, s, at, tmem, half, w, lane, slabs); break;
+            case 7: add_slabs<kind, 7>(a, s, at, tmem, half, w, lane, slabs); break;
+            default: add_slabs<kind, 8>(a, s, at, tmem, half, w, lane, slabs); break;
+          }
+        };
+        if constexpr (kind != kProdDgradSwiglu) add();
         if constexpr (kind == kProdFwdSwiglu) {
           out.gated(t, a, nh, turn, peer_phase);
           turn ^= 1;
           peer_phase ^= 1;
         } else if constexpr (kind == kProdDgradSwiglu) {
-          out.through_activation(t, a, nh);
+          out.through_activation(t, a, nh, add);
         } else {
           out.plain(t, a, nh);
         }
@@ -843,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // A map of [dim 4]..[dim 1][dim 0] bytes.
 bool make_map(CUtensorMap* m, const void* base, int dims, const long long (&size)[5], const long long (&stride)[4],
-              const int (&box)[5]) {
+              const int (&box)[5], bool swizzle = true) {
   const tc::EncodeFn f = tc::tensor_map_encoder();
   if (f == nullptr) return false;
   cuuint64_t sz[5], st[4];
@@ -855,7 +879,7 @@ bool make_map(CUtensorMap* m, const void* base, int dims, const long long (&size
     if (i + 1 < dims) st[i] = static_cast<cuuint64_t>(stride[i]);
   }
   return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(dims), const_cast<void*>(base), sz, st, bx, one,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -892,7 +916,7 @@ int resident_pairs(int num_sms) {
 
 template <typename T, int kind>
 cudaError_t launch_kind(const F8Params& p, int num_sms, cudaStream_t s) {
-  CUtensorMap a, b, b64, b32, b16;
+  CUtensorMap a, b, b64, b32, b16, pre = {};
   constexpr bool fwd = kind == kProdFwd || kind == kProdFwdSwiglu;
   const long long K = p.K, N = p.N, red = fwd ? K : N, F = N / 2;
   bool ok = kind == kProdFwdSwiglu
@@ -900,10 +924,12 @@ cudaError_t launch_kind(const F8Params& p, int num_sms, cudaStream_t s) {
                 : make_map(&a, p.w, 3, {K, N, p.E, 1, 1}, {K, N * K, 0, 0}, {kSlab, 128, 1, 1, 1});
   CUtensorMap* maps[4] = {&b, &b64, &b32, &b16};
   for (int i = 0; i < 4; ++i) ok = ok && make_map(maps[i], p.a, 2, {red, p.R, 1, 1, 1}, {red, 0, 0, 0}, {kSlab, 128 >> i, 1, 1, 1});
+  if (kind == kProdDgradSwiglu)  // 128 features of 128 rows
+    ok = ok && make_map(&pre, p.pre_in, 2, {4 * K, p.R, 1, 1, 1}, {4 * K, 0, 0, 0}, {256, 128, 1, 1, 1}, false);
   if (!ok) return cudaErrorInvalidValue;
   const int pairs = resident_pairs<T, kind>(num_sms);
   if (pairs == 0) return cudaErrorLaunchOutOfResources;
-  return launch_pdl(ep_product_f8_kernel<T, kind>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, 2, a, b, b64, b32, b16, p);
+  return launch_pdl(ep_product_f8_kernel<T, kind>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, s, 2, a, b, b64, b32, b16, pre, p);
 }
 
 template <typename T>
