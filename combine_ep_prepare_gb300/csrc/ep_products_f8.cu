@@ -139,14 +139,22 @@ struct Slots {
   }
 };
 
+// Buffers of the pair's exchange of largest magnitudes, taken by tiles in turn,
+// each with barriers of its own.  The other block may publish tile i + 1 when one
+// thread of this one has seen tile i; it publishes tile i + 2 only after this
+// block's half has published i + 1, all of its threads being past tile i's wait
+// by then.  So a barrier for every other tile is never two phases ahead of a
+// thread that waits on it, and its buffer is never written while it is read.
+constexpr int kExchanges = 2;
+
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[kSlots], acc_empty[kSlots], drained;
-  uint64_t scales_full[kGroups], scales_empty[kGroups], peer_full[2];
+  uint64_t scales_full[kGroups], scales_empty[kGroups], peer_full[kExchanges][2];  // peer_full: of each half
   uint32_t tmem;
   int gave_up, ok, most;  // most: rows of the largest tile
   int part[32];
   float ws[kGroups][2][kGroup];  // weight scales: the features', or gate's and up's
-  alignas(16) float peer_max[2][kTileN];  // the other block's largest magnitudes, a buffer for every other tile
+  alignas(16) float peer_max[kExchanges][kTileN];  // the other block's largest magnitudes
   alignas(16) float as[kGroups][kGroup][kTileN];
   int cum[EP_MAX_EXPERTS + 1];
 };
@@ -456,7 +464,7 @@ struct Epilogue {
     }
   }
 
-  // `turn`: which of the two buffers this tile's exchange uses; `parity` its phase.
+  // `turn`: which of the exchange's buffers this tile uses; `parity`: the phase of its barriers.
   __device__ __forceinline__ void gated(const Tile& t, Sums& a, int nh, int turn, uint32_t parity) const {
     const int F = p.N / 2, f = t.f0 + rank * (kHalfM / 2);
     Tile part = t;
@@ -530,8 +538,8 @@ struct Epilogue {
       store_peer(tc::in_block(tc::smem_addr(&s.peer_max[turn][half * nh + c]), rank ^ 1), m);
     }
     half_sync(half);
-    if (c == 0) tc::mbar_publish_cluster(tc::in_block(tc::smem_addr(&s.peer_full[half]), rank ^ 1));
-    tc::mbar_wait<true>(tc::smem_addr(&s.peer_full[half]), parity, &s.gave_up);
+    if (c == 0) tc::mbar_publish_cluster(tc::in_block(tc::smem_addr(&s.peer_full[turn][half]), rank ^ 1));
+    tc::mbar_wait<true>(tc::smem_addr(&s.peer_full[turn][half]), parity, &s.gave_up);
     if (c < nh) {
       const BlockScale b = block_scale(max_nan(m, s.peer_max[turn][half * nh + c]));
       most[c] = b.inv;
@@ -629,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(tc::smem_addr(&s.acc_full[i]), 1);
       tc::mbar_init(tc::smem_addr(&s.acc_empty[i]), 2 * kEpilogueWarps);
     }
-    for (int i = 0; i < 2; ++i) tc::mbar_init(tc::smem_addr(&s.peer_full[i]), 1);
+    for (int i = 0; i < kExchanges; ++i)
+      for (int j = 0; j < 2; ++j) tc::mbar_init(tc::smem_addr(&s.peer_full[i][j]), 1);
     for (int i = 0; i < kGroups; ++i) {
       tc::mbar_init(tc::smem_addr(&s.scales_full[i]), 32);
       tc::mbar_init(tc::smem_addr(&s.scales_empty[i]), kEpilogueWarps);
@@ -845,8 +854,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kind != kProdDgradSwiglu) add();
         if constexpr (kind == kProdFwdSwiglu) {
           out.gated(t, a, nh, turn, peer_phase);
-          turn ^= 1;
-          peer_phase ^= 1;
+          if (++turn == kExchanges) {
+            turn = 0;
+            peer_phase ^= 1;
+          }
         } else if constexpr (kind == kProdDgradSwiglu) {
           out.through_activation(t, a, nh, add);
         } else {
