@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(1024) ep_norm_kernel(const NormParams p) {
 template <typename T>
 struct GradVec {
   Raw8<T> dy, h, ds;
-  __device__ __forceinline__ void load(const NormParams& p, int t, int v, bool stream) {
+  __device__ __forceinline__ void load(const NormParams& p, unsigned t, int v, bool stream) {
     const long long at = static_cast<long long>(t) * p.H + 8 * v;
     dy.load_rw(static_cast<const T*>(p.dy) + at);
     h.load_rw(static_cast<const T*>(p.x) + at);
@@ -122,7 +122,7 @@ struct GradVec {
       *inner = fmaf(a[j] * w[j], b[j], *inner);
     }
   }
-  __device__ __forceinline__ void finish(const NormParams& p, int t, int v, const float (&w)[8], float r, float c, float (&dw)[8]) const {
+  __device__ __forceinline__ void finish(const NormParams& p, unsigned t, int v, const float (&w)[8], float r, float c, float (&dw)[8]) const {
     float a[8], b[8], s[8];
     dy.get(a);
     h.get(b);
@@ -158,6 +158,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) ep_norm_bwd_kernel(const
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  // Unsigned: the step past the last of 2^31 - 1 rows stays a number.
+  const unsigned rows = static_cast<unsigned>(p.T);
   int turn = 0;
   if constexpr (NV == 1) {
     const bool in = v0 < vectors;
@@ -167,11 +169,11 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) ep_norm_bwd_kernel(const
       Raw8<T> wr;
       wr.load(weight + 8 * v0);
       wr.get(w);
-      if (static_cast<int>(blockIdx.x) < p.T) next.load(p, blockIdx.x, v0, true);
+      if (blockIdx.x < rows) next.load(p, blockIdx.x, v0, true);
     }
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+    for (unsigned t = blockIdx.x; t < rows; t += gridDim.x, turn ^= 1) {
       const GradVec<T> at = next;
-      if (in && t + static_cast<int>(gridDim.x) < p.T) next.load(p, t + gridDim.x, v0, true);
+      if (in && t + gridDim.x < rows) next.load(p, t + gridDim.x, v0, true);
       float ss = 0.0f, inner = 0.0f;
       if (in) at.sums(w, &ss, &inner);
       const float2 sums = block_sum2(ss, inner, part[turn]);
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) ep_norm_bwd_kernel(const
       if (in) at.finish(p, t, v0, w, r, r * r * (sums.y / static_cast<float>(p.H)), dw[0]);
     }
   } else {
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+    for (unsigned t = blockIdx.x; t < rows; t += gridDim.x, turn ^= 1) {
       float ss = 0.0f, inner = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
