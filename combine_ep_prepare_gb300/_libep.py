@@ -45,6 +45,7 @@ DTYPE_CODES = {"bf16": 0, "fp16": 1, "fp32": 2}
 TORCH_DTYPES = {0: torch.bfloat16, 1: torch.float16, 2: torch.float32}
 _layer_dtype = {}  # layer id -> torch dtype of its payload rows
 _layer_experts = {}  # layer id -> (experts whose rows this rank holds, receive capacity)
+_layer_routes = {}   # layer id -> (hidden, top_k)
 
 
 class RouterConfig(ctypes.Structure):
@@ -241,6 +242,7 @@ def ep_register_layer(num_experts: int, top_k: int, hidden: int, max_tokens: int
     _check(_lib.ep_register_layer(cfg, ctypes.byref(lid), ctypes.byref(size)))
     _layer_dtype[int(lid.value)] = TORCH_DTYPES[code]
     _layer_experts[int(lid.value)] = (num_experts, ep_recv_capacity(int(lid.value)))
+    _layer_routes[int(lid.value)] = (hidden, top_k)
     return int(lid.value), int(size.value)
 
 
@@ -793,10 +795,21 @@ def ep_expert_quantize(h: EpHandle, x: torch.Tensor, q: torch.Tensor, scales: to
 def ep_dispatch_f8(h: EpHandle, topk_idx: torch.Tensor, tokens: torch.Tensor, scales: torch.Tensor,
                    topk_weights: torch.Tensor, recv_tokens: torch.Tensor, recv_scales: torch.Tensor,
                    recv_topk_weights: torch.Tensor, stream=None):
-    """ep_dispatch of 8-bit rows with their scales."""
-    if tokens.dim() != 2:
-        raise ValueError("tokens must be [tokens, hidden], got %s" % (tuple(tokens.shape),))
+    """ep_dispatch of 8-bit rows with their scales: tokens [T, hidden], scales
+    [T, scale_columns(hidden)], topk_idx and topk_weights [T, K], receive
+    buffers of the layer's capacity of rows."""
+    if tokens.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("tokens must be [tokens, hidden] and topk_idx [tokens, top_k], got %s and %s"
+                         % (tuple(tokens.shape), tuple(topk_idx.shape)))
     T, n = tokens.shape
+    hidden, K = _layer_routes.get(h.id, (n, topk_idx.shape[1]))
+    if n != hidden:  # the kernel steps by the layer's rows
+        raise ValueError("tokens must be [%d, %d], got %s" % (T, hidden, tuple(tokens.shape)))
+    _routes(topk_idx, T, K, "topk_idx")
+    _routes(topk_weights, T, K, "topk_weights")
+    capacity = _layer_experts.get(h.id, (0, 0))[1]
+    if recv_topk_weights.numel() < capacity:
+        raise ValueError("recv_topk_weights must be [>= %d rows], got %s" % (capacity, tuple(recv_topk_weights.shape)))
     sp = _shaped(scales, (T, scale_columns(n)), torch.float32, "scales")
     rp, rsp = _f8_rows(h, recv_tokens, recv_scales, n, "recv_tokens")
     _check(_lib.ep_dispatch_f8(h.c, _ptr(topk_idx, torch.int64, "topk_idx"), T, _f8_ptr(tokens, "tokens"), sp,
