@@ -734,25 +734,25 @@ def _f8_ptr(t: torch.Tensor, name: str) -> Optional[int]:
     return _ptr(t, F8, name)
 
 
-def _shaped(t: torch.Tensor, shape, dtype, name: str) -> Optional[int]:
+def _fits(t: torch.Tensor, shape, name: str):
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    return _ptr(t, dtype, name)
 
 
 def _f8_rows(h: EpHandle, t: torch.Tensor, scales: torch.Tensor, width: int, name: str):
     """8-bit receive rows and their scales: at least the layer's capacity."""
     capacity = _layer_experts.get(h.id, (0, 0))[1]
-    for x, cols, n, dtype in ((t, width, name, F8), (scales, scale_columns(width), name + "_scales", torch.float32)):
-        _ptr(x, dtype, n)
+    for x, cols, n in ((t, width, name), (scales, scale_columns(width), name + "_scales")):
         if x.dim() != 2 or x.shape[1] != cols or x.shape[0] < capacity:
             raise ValueError("%s must be [>= %d rows, %d], got %s" % (n, capacity, cols, tuple(x.shape)))
-    return t.data_ptr() or None, scales.data_ptr() or None
+    return _ptr(t, F8, name), _ptr(scales, torch.float32, name + "_scales")
 
 
 def _f8_weights(h: EpHandle, w: torch.Tensor, scales: torch.Tensor):
+    if w.dim() == 3:
+        _fits(scales, (w.shape[0], _f8_blocks(w.shape[1]), _f8_blocks(w.shape[2])), "w_scales")
     wp, n, k = _expert_weights(h, w, "w", F8)
-    return wp, _shaped(scales, (w.shape[0], _f8_blocks(n), _f8_blocks(k)), torch.float32, "w_scales"), n, k
+    return wp, _ptr(scales, torch.float32, "w_scales"), n, k
 
 
 def pack_f8(w: torch.Tensor):
@@ -777,8 +777,10 @@ def ep_quantize_rows(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, str
         raise ValueError("x must be [rows, features], got %s" % (tuple(x.shape),))
     rows, n = x.shape
     code = _dtype_code(x.dtype)
-    _check(_lib.ep_quantize_rows(_ptr(x, None, "x"), rows, n, code, _shaped(q, x.shape, F8, "q"),
-                                 _shaped(scales, (rows, scale_columns(n)), torch.float32, "scales"), _stream(stream)))
+    _fits(q, x.shape, "q")
+    _fits(scales, (rows, scale_columns(n)), "scales")
+    _check(_lib.ep_quantize_rows(_ptr(x, None, "x"), rows, n, code, _ptr(q, F8, "q"), _ptr(scales, torch.float32, "scales"),
+                                 _stream(stream)))
 
 
 def ep_expert_quantize(h: EpHandle, x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None):
@@ -787,9 +789,8 @@ def ep_expert_quantize(h: EpHandle, x: torch.Tensor, q: torch.Tensor, scales: to
     if x.dim() != 2:
         raise ValueError("x must be [rows, features], got %s" % (tuple(x.shape),))
     n = x.shape[1]
-    xp = _rows(h, x, n, "x")
     qp, sp = _f8_rows(h, q, scales, n, "q")
-    _check(_lib.ep_expert_quantize(h.c, xp, n, qp, sp, _stream(stream)))
+    _check(_lib.ep_expert_quantize(h.c, _rows(h, x, n, "x"), n, qp, sp, _stream(stream)))
 
 
 def ep_dispatch_f8(h: EpHandle, topk_idx: torch.Tensor, tokens: torch.Tensor, scales: torch.Tensor,
@@ -810,9 +811,10 @@ def ep_dispatch_f8(h: EpHandle, topk_idx: torch.Tensor, tokens: torch.Tensor, sc
     capacity = _layer_experts.get(h.id, (0, 0))[1]
     if recv_topk_weights.numel() < capacity:
         raise ValueError("recv_topk_weights must be [>= %d rows], got %s" % (capacity, tuple(recv_topk_weights.shape)))
-    sp = _shaped(scales, (T, scale_columns(n)), torch.float32, "scales")
+    _fits(scales, (T, scale_columns(n)), "scales")
     rp, rsp = _f8_rows(h, recv_tokens, recv_scales, n, "recv_tokens")
-    _check(_lib.ep_dispatch_f8(h.c, _ptr(topk_idx, torch.int64, "topk_idx"), T, _f8_ptr(tokens, "tokens"), sp,
+    _check(_lib.ep_dispatch_f8(h.c, _ptr(topk_idx, torch.int64, "topk_idx"), T, _f8_ptr(tokens, "tokens"),
+                               _ptr(scales, torch.float32, "scales"),
                                _ptr(topk_weights, torch.float32, "topk_weights"), rp, rsp,
                                _ptr(recv_topk_weights, torch.float32, "recv_topk_weights"), _stream(stream)))
 
@@ -875,10 +877,12 @@ def ep_rmsnorm(x: torch.Tensor, weight: torch.Tensor, y: Optional[torch.Tensor] 
         raise ValueError("x must be [tokens, hidden], got %s" % (tuple(x.shape),))
     T, H = x.shape
     code, dt = _dtype_code(x.dtype), x.dtype
-    opt = lambda t, name: None if t is None else _shaped(t, x.shape, dt, name)  # noqa: E731
-    _check(_lib.ep_rmsnorm(_ptr(x, None, "x"), opt(residual, "residual"), _shaped(weight, (H,), dt, "weight"), T, H, code, eps,
-                           opt(sum, "sum"), opt(y, "y"), None if q is None else _shaped(q, x.shape, F8, "q"),
-                           None if scales is None else _shaped(scales, (T, scale_columns(H)), torch.float32, "scales"),
+    for t, shape, name in ((residual, x.shape, "residual"), (weight, (H,), "weight"), (sum, x.shape, "sum"), (y, x.shape, "y"),
+                           (q, x.shape, "q"), (scales, (T, scale_columns(H)), "scales")):
+        if t is not None:
+            _fits(t, shape, name)
+    _check(_lib.ep_rmsnorm(_ptr(x, None, "x"), _ptr(residual, dt, "residual"), _ptr(weight, dt, "weight"), T, H, code, eps,
+                           _ptr(sum, dt, "sum"), _ptr(y, dt, "y"), _ptr(q, F8, "q"), _ptr(scales, torch.float32, "scales"),
                            _stream(stream)))
 
 
@@ -903,10 +907,14 @@ def ep_rmsnorm_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, 
     _check(_lib.ep_rmsnorm_bwd_workspace(T, H, ctypes.byref(size)))
     if workspace.numel() * workspace.element_size() < size.value:
         raise ValueError("workspace must hold %d bytes, got %d" % (size.value, workspace.numel() * workspace.element_size()))
-    _check(_lib.ep_rmsnorm_bwd(_shaped(grad_y, h.shape, dt, "grad_y"), _ptr(h, None, "h"), _shaped(weight, (H,), dt, "weight"),
-                               None if grad_sum is None else _shaped(grad_sum, h.shape, dt, "grad_sum"), T, H, code, eps,
-                               _shaped(grad_h, h.shape, dt, "grad_h"), _shaped(grad_weight, (H,), torch.float32, "grad_weight"),
-                               1 if accumulate else 0, _ptr(workspace, None, "workspace"), _stream(stream)))
+    for t, shape, name in ((grad_y, h.shape, "grad_y"), (weight, (H,), "weight"), (grad_sum, h.shape, "grad_sum"),
+                           (grad_h, h.shape, "grad_h"), (grad_weight, (H,), "grad_weight")):
+        if t is not None:
+            _fits(t, shape, name)
+    _check(_lib.ep_rmsnorm_bwd(_ptr(grad_y, dt, "grad_y"), _ptr(h, None, "h"), _ptr(weight, dt, "weight"),
+                               _ptr(grad_sum, dt, "grad_sum"), T, H, code, eps, _ptr(grad_h, dt, "grad_h"),
+                               _ptr(grad_weight, torch.float32, "grad_weight"), 1 if accumulate else 0,
+                               _ptr(workspace, None, "workspace"), _stream(stream)))
 
 
 # ----------------------------------------------------------------------------
@@ -966,11 +974,12 @@ def ep_moe_few(x: torch.Tensor, gate: torch.Tensor, w13: torch.Tensor, w2: torch
     wt = F8 if f8 else x.dtype
     if f8 and (s13 is None or s2 is None):
         raise ValueError("8-bit weights need s13 and s2")
-    sp = lambda s, n, k, name: None if s is None else _shaped(s, (E, _f8_blocks(n), _f8_blocks(k)), torch.float32, name)  # noqa: E731
-    _check(_lib.ep_moe_few(cfg, _ptr(x, None, "x"), _shaped(gate, (E, H), None, "gate"),
-                           None if bias is None else _shaped(bias, (E,), torch.float32, "bias"),
-                           _shaped(w13, (E, 2 * F, H), wt, "w13"), sp(s13, 2 * F, H, "s13"),
-                           _shaped(w2, (E, H, F), wt, "w2"), sp(s2, H, F, "s2"), T, _shaped(out, x.shape, x.dtype, "out"),
-                           _shaped(topk_idx, (T, K), torch.int64, "topk_idx"),
-                           _shaped(topk_weights, (T, K), torch.float32, "topk_weights"), _ptr(workspace, None, "workspace"),
-                           _stream(stream)))
+    for t, shape, name in ((gate, (E, H), "gate"), (bias, (E,), "bias"), (w13, (E, 2 * F, H), "w13"), (w2, (E, H, F), "w2"),
+                           (s13, (E, _f8_blocks(2 * F), _f8_blocks(H)), "s13"), (s2, (E, _f8_blocks(H), _f8_blocks(F)), "s2"),
+                           (out, x.shape, "out"), (topk_idx, (T, K), "topk_idx"), (topk_weights, (T, K), "topk_weights")):
+        if t is not None:
+            _fits(t, shape, name)
+    _check(_lib.ep_moe_few(cfg, _ptr(x, None, "x"), _ptr(gate, None, "gate"), _ptr(bias, torch.float32, "bias"),
+                           _ptr(w13, wt, "w13"), _ptr(s13, torch.float32, "s13"), _ptr(w2, wt, "w2"), _ptr(s2, torch.float32, "s2"),
+                           T, _ptr(out, x.dtype, "out"), _ptr(topk_idx, torch.int64, "topk_idx"),
+                           _ptr(topk_weights, torch.float32, "topk_weights"), _ptr(workspace, None, "workspace"), _stream(stream)))
