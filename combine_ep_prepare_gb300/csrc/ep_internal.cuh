@@ -300,12 +300,13 @@ cudaError_t launch_prepare_static_scratch(const RouteParams& p, int* scratch, in
 // dispatch (weights) and combine_bwd (no weights): token-major row scatter.
 cudaError_t launch_scatter(const RowParams& p, bool weights, int npad_max, int num_sms,
                            cudaStream_t s);
-// The same for a sharded layer: rows go to their owner's buffer through
-// p.dst_tab (and weights through p.wout_tab); padding rows of this rank's own
-// buffer are zeroed.
-// 8-bit rows (p.rowbytes of them) with their scales.
+// dispatch of a single-buffer layer's tokens as 8-bit rows of p.rowbytes, with
+// their scales [T][scale_columns(p.rowbytes)] and their weights.
 cudaError_t launch_dispatch_f8(const RowParams& p, const float* scales, float* recv_scales, int npad_max,
                                int num_sms, cudaStream_t s);
+// launch_scatter for a sharded layer: rows go to their owner's buffer through
+// p.dst_tab (and weights through p.wout_tab); padding rows of this rank's own
+// buffer are zeroed.
 cudaError_t launch_scatter_sharded(const RowParams& p, bool weights, int npad_max, int num_sms,
                                    cudaStream_t s);
 // combine / dispatch_bwd of a sharded layer: rows read from their owner's
