@@ -145,8 +145,10 @@ struct GradVec {
 // vector a thread (rows of up to 8192): the next row is loaded before the sums
 // over this one are joined, and the weights stay in registers (8,192 x 7168
 // bf16: 119 us without either, 92 with the first, 85 with both; then near two
-// thirds of the issue slots are busy).  Longer rows are read twice, the second
-// time from L2: the registers hold dw.
+// thirds of the issue slots are busy).  1,024 threads leave 64 registers, of which
+// fp32 rows, with twice the data in flight, spill 108 bytes and fp16 rows 20: 8,192 x
+// 7168 take 232 us in fp32 (4.0 TB/s) and 102 in fp16.  Longer rows are read twice,
+// the second time from L2: the registers hold dw.
 template <typename T, int NV>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) ep_norm_bwd_kernel(const NormParams p) {
   __shared__ float part[2][64];
@@ -240,7 +242,13 @@ __global__ void __launch_bounds__(32 * kSumRows) ep_norm_dw_kernel(const NormPar
   }
 }
 
-// Threads and vectors per thread for rows of H elements.
+// Threads and vectors per thread for rows of H elements.  Two vectors a thread keep
+// more loads of a batch in flight and its sum in fewer warps; one is quicker through
+// the few rows of a decode step, fp32's vectors are twice as wide and do not care.
+// bf16 with sum, y and q, 235 MB of x, and 128 rows: 2048 elements 167 us and 2.7
+// (one vector: 183 and 2.2), 7168 168 and 3.2 (219 and 2.8), 1024 178 and 2.1 with
+// the one that the rule takes (two: 166 and 2.7), 512 176 and 2.1 (181 and 2.5).  Four where 1,024
+// threads need them: 16384 elements take 173 us with two, 201 with four.
 void shape(int H, int* threads, int* nv) {
   const int vectors = H / 8;
   *nv = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 4;

@@ -20,7 +20,9 @@
 // loads alone would keep shared memory busy for 256 clocks a slab, next to the
 // operands'.  A warp of its own brings the scales in, four slabs at a time.
 //
-// With many rows the additions bound it.  8 experts x 1,024 rows, 7168 -> 4096,
+// With many rows the adding warps bound it, by their latencies: two for each
+// scheduler, which wait, load and multiply in turn, while no unit is busy for more
+// than 38% of the time.  8 experts x 1,024 rows, 7168 -> 4096,
 // take 230 us (2.09 PFLOP/s), 139 without the additions and 221 with one mma of
 // four; the additions with neither loads nor mma take 152.  With ragged experts
 // (16,384 rows over 32 of them, 7168 -> 2 x 2048, 8-bit result) 557 us, with even
@@ -30,13 +32,19 @@
 // tile's width in the loop made 115 moves a slab and warp: 889 us for the 496),
 // packed multiply-adds from the compiler's own pairs (530), and mma issued from
 // uniform registers (up decode 375 us before, 301 after).  Columns per load,
-// loads further ahead, stages and the split of registers made no difference.
+// loads further ahead, stages and the split of registers made no difference; more
+// adding warps with fewer sums each were not tried.  The kernels spill 40 to 48
+// bytes.  Plain input gradient: 16,384 even rows, 2 x 2048 -> 7168, 484 us
+// (1.99 PFLOP/s), 65,536 ragged ones of 128 experts, 2 x 1024 -> 2048, 343; 64
+// experts x 4 rows, 270.  (All are times of calls in a row, every expert with
+// rows.)
 //
 // The gated pair: 16 gate rows and the 16 up rows of the same features
 // alternate in the tile, and land in one lane's two halves of the sums.  Its
 // 8-bit result needs the largest magnitude of a row's 128 features, 64 in each
 // SM of the pair: they exchange theirs through distributed shared memory (19 us
-// of the 496 beside a 16-bit result).
+// of the 496 beside a 16-bit result).  The two 16-bit results that a backward pass
+// reads take 48 us more (545).
 #include <algorithm>
 #include <atomic>
 

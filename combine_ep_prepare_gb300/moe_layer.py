@@ -14,9 +14,12 @@ for serving with 4-bit weights, or of a few tokens in two kernels.
     out = layer.few(x, gate, w13, w2)              # up to 32 tokens; or layer.few(x, gate, q8)
 
 Weights: gate [E, H]; w13 [E, 2F, H] (gate rows, then up rows); w2 [E, H, F].
-Every buffer is allocated once; a step's routing stays on the device, so
-forward, backward and decode only enqueue work and can be captured in a CUDA
-graph (the gate's small matrix products are torch's).
+The buffers between the calls are allocated once (those of the 8-bit path and of
+few at their first use); results, and the norm gradient's workspace, are new
+tensors of each call.  A step's routing stays on the device, so all of these only
+enqueue work and can be captured in a CUDA graph (the gate's small matrix
+products are torch's).  A layer's buffers serve one step at a time: graphs or
+streams that may run at once need a layer each.
 
 As a command it runs one layer and prints the time of a training step and of
 a decode step:

@@ -731,9 +731,10 @@ ep_status_t ep_expert_dgrad_f8_swiglu(ep_handle_t handle, const uint8_t* dy, con
  * kernel is a cooperative launch whose blocks wait for one another once, and
  * whose copies are waited for, with limits of one and two seconds; if one runs
  * out, out is incomplete and the workspace's first 32-bit word is
- * EP_ST_TIMEOUT, else 0.  The order of the sums goes by the sizes, the choice
- * and the device's number of SMs.  Make the first call of each configuration's
- * types on a device before any capture.
+ * EP_ST_TIMEOUT, else 0 (a call without tokens leaves it as it was).  The
+ * order of the sums goes by the sizes, the choice and the device's number of
+ * SMs.  Make the first call of each configuration's types on a device before
+ * any capture.
  * ------------------------------------------------------------------------ */
 #define EP_MAX_FEW_TOKENS 32
 
